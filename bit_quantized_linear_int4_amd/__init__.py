@@ -24,10 +24,13 @@ __all__ = [
     "wq_linear_int8_decomp", "wq_linear_int8_decomp_noalloc", "wq_dequantize",
     "wq_status_string",
     "alloc_int4", "alloc_nf4", "alloc_fp4", "alloc_int8", "library_path", "FMT_FP4",
+    "FMT_FP8_BLOCK", "wq_add_rmsnorm", "wq_quantize_fp8_rows", "wq_quantize_fp8_block",
+    "wq_linear_fp8_workspace", "wq_linear_fp8", "alloc_fp8", "alloc_fp8_rows",
+    "wq_moe_workspace", "wq_moe",
 ]
 
 F16, BF16, F32 = 0, 1, 2
-FMT_INT4_ASYM, FMT_NF4, FMT_INT8_SYM_ROW, FMT_FP4 = 0, 1, 2, 3
+FMT_INT4_ASYM, FMT_NF4, FMT_INT8_SYM_ROW, FMT_FP4, FMT_FP8_BLOCK = 0, 1, 2, 3, 4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # WQ_LIBRARY names another build of the same library (for example one whose
@@ -93,6 +96,16 @@ def _load():
         "wq_dequantize": (c_i32, [wp, c_vp, c_i32, c_vp]),
         "wq_permute_columns": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp]),
         "wq_scale_columns": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp]),
+        "wq_add_rmsnorm": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_f,
+                                   c_vp, c_vp, c_vp, c_vp]),
+        "wq_quantize_fp8_rows": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp]),
+        "wq_quantize_fp8_block": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp]),
+        "wq_linear_fp8_workspace": (ctypes.c_size_t, [c_i64, wp]),
+        "wq_linear_fp8": (c_i32, [c_vp, c_vp, c_i64, wp, c_vp, c_i32, c_vp, ctypes.c_size_t,
+                                  c_vp]),
+        "wq_moe_workspace": (ctypes.c_size_t, [c_i64, c_i32, wp, c_i64]),
+        "wq_moe": (c_i32, [c_vp, c_i32, c_i64, c_vp, c_vp, c_i64, c_i32, c_i32, wp, wp, wp, c_vp,
+                           c_i32, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
         "wq_status_string": (ctypes.c_char_p, [c_i32]),
     }
     for name, (res, args) in sig.items():
@@ -215,6 +228,9 @@ def _weight_tensors(what, w):
     elif w.fmt == FMT_INT8_SYM_ROW:
         _dense(what, "codes", w.codes, n * k)
         _dense(what, "scales", w.scales, 4 * n)
+    elif w.fmt == FMT_FP8_BLOCK:
+        _dense(what, "codes", w.codes, n * k)
+        _dense(what, "scales", w.scales, 4 * (-(-n // 128)) * (-(-k // 128)))
     else:
         _fail(what, f"unknown weight format {w.fmt}", _ERR_UNSUP)
     return [w.codes, w.scales, w.zeros, w.scales2, w.perm]
@@ -285,6 +301,21 @@ def alloc_int8(n, k, device="cuda"):
     return QuantizedWeight(FMT_INT8_SYM_ROW, n, k, k,
                            torch.empty((n, k), dtype=torch.int8, device=device),
                            torch.empty((n,), dtype=torch.float32, device=device))
+
+
+def alloc_fp8(n, k, device="cuda"):
+    import torch
+    return QuantizedWeight(FMT_FP8_BLOCK, n, k, 128,
+                           torch.empty((n, k), dtype=torch.float8_e4m3fn, device=device),
+                           torch.empty((-(-n // 128), -(-k // 128)), dtype=torch.float32,
+                                       device=device))
+
+
+def alloc_fp8_rows(m, k, device="cuda"):
+    """(q, scales) of m activation rows: E4M3 [m][k] and fp32 [ceil(k/128)][m]."""
+    import torch
+    return (torch.empty((m, k), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((-(-k // 128), m), dtype=torch.float32, device=device))
 
 
 def wq_quantize_groupwise(w, bits, group, symmetric, codes, scales, zeros=None, stream=None):
@@ -472,6 +503,143 @@ def wq_scale_columns(src, scale, dst, stream=None):
     st = _load().wq_scale_columns(_ptr(src), _dt(src), rows, k, _ptr(scale), _ptr(dst),
                                   _stream(stream, src))
     _check(st, "wq_scale_columns")
+
+
+def _rows(what, name, t):
+    """(m, k, stride of the rows) of a 2-D tensor whose rows are contiguous."""
+    if t is None or t.dim() != 2:
+        _fail(what, f"{name} must be a 2-D [rows][k] tensor")
+    m, k = t.shape
+    ld, one = t.stride()
+    if m == 1:
+        ld = k
+    if k > 1 and one != 1 or ld < k:
+        _fail(what, f"the rows of {name} are not contiguous")
+    return m, k, ld
+
+
+def _fp8_rows(what, q, scales, m, k):
+    _dense(what, "q", q, m * k, (m, k))
+    _dense(what, "scales", scales, 4 * m * (-(-k // 128)), (-(-k // 128), m))
+
+
+def wq_add_rmsnorm(x, gain, eps, residual=None, residual_out=None, y=None, q=None, scales=None,
+                   stream=None):
+    what = "wq_add_rmsnorm"
+    m, k, ldx = _rows(what, "x", x)
+    dt = _dt(x)
+    ldr = k
+    _dense(what, "gain", gain, shape=(k,))
+    same = [("gain", gain)]
+    if residual is not None or residual_out is not None:
+        mr, kr, ldr = _rows(what, "residual", residual)
+        if (mr, kr) != (m, k) or _rows(what, "residual_out", residual_out) != (m, k, ldr):
+            _fail(what, "residual and residual_out must have x's shape and equal strides")
+        same += [("residual", residual), ("residual_out", residual_out)]
+    if y is not None:
+        _dense(what, "y", y, shape=(m, k))
+        same.append(("y", y))
+    for name, t in same:
+        if t.dtype != x.dtype:
+            _fail(what, f"{name} has dtype {t.dtype}, x {x.dtype}", _ERR_UNSUP)
+    if q is not None or scales is not None:
+        _fp8_rows(what, q, scales, m, k)
+    elif y is None:
+        _fail(what, "y or q is required")
+    _on_gpu(what, x, gain, residual, residual_out, y, q, scales)
+    st = _load().wq_add_rmsnorm(_ptr(x), dt, m, k, ldx, _ptr(residual), _ptr(residual_out), ldr,
+                                _ptr(gain), eps, _ptr(y), _ptr(q), _ptr(scales),
+                                _stream(stream, x))
+    _check(st, what)
+
+
+def wq_quantize_fp8_rows(x, q, scales, up=None, stream=None):
+    what = "wq_quantize_fp8_rows"
+    m, k = _matrix(what, "x", x)
+    if up is not None:
+        _dense(what, "up", up, shape=(m, k))
+        if up.dtype != x.dtype:
+            _fail(what, f"up has dtype {up.dtype}, x {x.dtype}", _ERR_UNSUP)
+    _fp8_rows(what, q, scales, m, k)
+    _on_gpu(what, x, up, q, scales)
+    st = _load().wq_quantize_fp8_rows(_ptr(x), _ptr(up), _dt(x), m, k, _ptr(q), _ptr(scales),
+                                      _stream(stream, x))
+    _check(st, what)
+
+
+def wq_quantize_fp8_block(w, codes, scales, stream=None):
+    what = "wq_quantize_fp8_block"
+    n, k = _matrix(what, "w", w)
+    _dense(what, "codes", codes, n * k)
+    _dense(what, "scales", scales, 4 * (-(-n // 128)) * (-(-k // 128)))
+    _on_gpu(what, w, codes, scales)
+    st = _load().wq_quantize_fp8_block(_ptr(w), _dt(w), n, k, _ptr(codes), _ptr(scales),
+                                       _stream(stream, w))
+    _check(st, what)
+
+
+def wq_linear_fp8_workspace(m, weight):
+    d = weight.descriptor()
+    return int(_load().wq_linear_fp8_workspace(int(m), ctypes.byref(d)))
+
+
+def wq_linear_fp8(q, scales, weight, y, workspace=None, stream=None):
+    what = "wq_linear_fp8"
+    m, ts = _check_linear(what, q, weight, [("y", y)])
+    _fp8_rows(what, q, scales, m, weight.k)
+    if workspace is not None:
+        _dense(what, "workspace", workspace)
+    _on_gpu(what, workspace, scales, *ts)
+    d = weight.descriptor()
+    ws_bytes = 0 if workspace is None else _nbytes(workspace)
+    st = _load().wq_linear_fp8(_ptr(q), _ptr(scales), m, ctypes.byref(d), _ptr(y), _dt(y),
+                               _ptr(workspace), ws_bytes, _stream(stream, q))
+    _check(st, what)
+
+
+def wq_moe_workspace(m, top_k, gate, experts):
+    d = gate.descriptor()
+    return int(_load().wq_moe_workspace(int(m), int(top_k), ctypes.byref(d), int(experts)))
+
+
+def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, logits=None,
+           ids=None, probs=None, stream=None):
+    """`router` [experts][h] in x's dtype, or None with `logits` fp32 [m][experts]."""
+    import torch
+    what = "wq_moe"
+    m, h = _matrix(what, "x", x)
+    if (router is None) == (logits is None):
+        _fail(what, "either router or logits is required")
+    if router is not None:
+        experts, k = _matrix(what, "router", router)
+        if k != h or router.dtype != x.dtype:
+            _fail(what, f"router must be {x.dtype} [experts][{h}]")
+    else:
+        _, experts = _matrix(what, "logits", logits)
+        _dense(what, "logits", logits, shape=(m, experts))
+        if logits.dtype != torch.float32:
+            _fail(what, "logits must be float32", _ERR_UNSUP)
+    ts = []
+    for w in (gate, up, down):
+        ts += _weight_tensors(what, w)
+    i = down.k
+    if (gate.n, gate.k) != (experts * i, h) or (up.n, up.k) != (experts * i, h) or (
+            down.n != experts * h):
+        _fail(what, f"gate and up must hold {experts} x {i} rows of {h}, "
+                    f"down {experts} x {h} rows of {i}")
+    _dense(what, "y", y, shape=(m, h))
+    if ids is not None:
+        _dense(what, "ids", ids, 4 * m * top_k, (m, top_k))
+    if probs is not None:
+        _dense(what, "probs", probs, 4 * m * top_k, (m, top_k))
+    _dense(what, "workspace", workspace)
+    _on_gpu(what, x, router, logits, y, ids, probs, workspace, *ts)
+    dg, du, dd = gate.descriptor(), up.descriptor(), down.descriptor()
+    st = _load().wq_moe(_ptr(x), _dt(x), m, _ptr(router), _ptr(logits), experts, int(top_k),
+                        1 if renormalize else 0, ctypes.byref(dg), ctypes.byref(du),
+                        ctypes.byref(dd), _ptr(y), _dt(y), _ptr(ids), _ptr(probs),
+                        _ptr(workspace), _nbytes(workspace), _stream(stream, x))
+    _check(st, what)
 
 
 def wq_dequantize(weight, out, stream=None):

@@ -2,11 +2,11 @@
 //
 // INT4: w_hat = round16((q - z) * s)      (the product is exact in fp32)
 // NF4 : w_hat = round16(L[code] * a_hat)  (a_hat = q8 * c2 with double quant)
-// INT8: w_hat = round16(fp32(q) * s)
+// INT8, FP8: w_hat = round16(fp32(q) * s)
 // These are the dequantizations the linear kernels apply in registers
 // ("LLM quantization selection", section 5 opening: weights go back to FP16
 // before the multiply-add; section 6.2: NF4 goes back to the compute dtype).
-#include "internal.h"
+#include "fp8_util.h"
 
 namespace wq {
 namespace {
@@ -43,6 +43,18 @@ __global__ __launch_bounds__(256) void dequant_kernel(wq_weight w, Levels lv,
       ah = static_cast<const float*>(w.scales)[blk];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = as_f32(lv.v[(word >> (4 * i)) & 15u] * ah);
+  } else if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
+    const uint2_t q = *reinterpret_cast<const uint2_t*>(static_cast<const uint8_t*>(w.codes) + e0);
+    const int64_t kb = (w.k + kF8Block - 1) / kF8Block;
+    const float s =
+        static_cast<const float*>(w.scales)[(r / kF8Block) * kb + c0 / kF8Block];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2v_t f = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i / 2], true)
+                                  : __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i / 2], false);
+      v[2 * i] = as_f32(f.x * s);
+      v[2 * i + 1] = as_f32(f.y * s);
+    }
   } else {
     const int8_t* q = static_cast<const int8_t*>(w.codes) + e0;
     const float s = static_cast<const float*>(w.scales)[r];
@@ -69,6 +81,7 @@ hipError_t dequant_odt(const wq_weight* w, const float* levels, uint16_t* out, h
   switch (w->fmt) {
     case WQ_FMT_INT4_ASYM: dequant_kernel<WQ_FMT_INT4_ASYM, ODT><<<grid, 256, 0, s>>>(*w, lv, out); break;
     case WQ_FMT_NF4: dequant_kernel<WQ_FMT_NF4, ODT><<<grid, 256, 0, s>>>(*w, lv, out); break;
+    case WQ_FMT_FP8_BLOCK: dequant_kernel<WQ_FMT_FP8_BLOCK, ODT><<<grid, 256, 0, s>>>(*w, lv, out); break;
     default: dequant_kernel<WQ_FMT_INT8_SYM_ROW, ODT><<<grid, 256, 0, s>>>(*w, lv, out); break;
   }
   return hipGetLastError();

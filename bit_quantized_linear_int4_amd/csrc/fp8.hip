@@ -1,0 +1,430 @@
+// FP8 linear: y[i][j] = sum_b sx[b][i] * sw[j/128][b] * sum_{c in block b} xq[i][c] * wq[j][c],
+// E4M3 activations with a scale per token and 128 values of k, E4M3 weights
+// with a scale per 128 x 128 block.
+//
+// The sum over one block of 128 is exactly one v_mfma_f32_16x16x128_f8f6f4,
+// so every matrix instruction starts from zero and its four results per lane
+// are added to the fp32 totals with one fused multiply-add each.
+//
+// The FP8 matrix instructions (all of them: 16x16x32, 16x16x128 and 32x32x64
+// give the same bits) drop bits below about 2^-16 of the largest products of
+// a sum: measured on N(0, 100) codes 1.5e-5 of the sum's size, 4.6e-5 with one
+// outlier per block.  That is far below the rounding of a 16-bit y (up to 2^-8
+// or 2^-11 of the value), so those outputs use it.  An fp32 y takes the exact
+// products instead: the codes converted to bf16 (exact) and four
+// v_mfma_f32_16x16x32_bf16 per block, 1e-8 on the same codes, at half the
+// matrix rate.
+//
+// Operands:  The weights
+// are the A operand (16 output features), the activations the B operand (16
+// tokens): a lane then holds four consecutive features of ONE token, whose
+// scale product sx * sw is one value per lane and instruction group, and which
+// store as one 8- or 16-byte piece of a row of y.
+//
+// Which bytes of a block a lane feeds into the K positions of the instruction
+// is free as long as both operands agree: lane group g = lane / 16 takes the
+// 16-byte chunks g and g + 4.
+//
+//  * decode (m <= 16): HBM-bound.  A workgroup owns 16 features over all of k;
+//    its waves take the blocks of k in turn and add their totals in LDS in a
+//    fixed order.
+//  * gemm: MFMA-bound.  Tiles of BN features x BM tokens, both operands staged
+//    128 bytes of k at a time by direct global -> LDS loads into two buffers,
+//    one barrier per block of k.  Where the tiles are too few to fill the GPU,
+//    k is split over workgroups whose fp32 totals a second kernel adds.
+#include <algorithm>
+#include <atomic>
+
+#include "fp8_util.h"
+
+namespace wq {
+namespace {
+
+struct Fp8Args {
+  const uint8_t* x;          // [m][k]
+  const float* sx;           // [kb][m]
+  const uint8_t* w;          // [n][k]
+  const float* sw;           // [ceil(n/128)][kb]
+  void* y;                   // [m][n]
+  float* part;               // split totals [splits][m][n], or nullptr
+  int m, n, k, kb, splits;
+};
+
+__device__ const uint4_t kZero16 = {0, 0, 0, 0};   // what chunks past k read
+
+__device__ __forceinline__ float4_t mfma_fp8(int8v_t a, int8v_t b) {
+  const float4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
+}
+
+// 4 E4M3 bytes -> 4 bf16 values (exact)
+__device__ __forceinline__ void fp8_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, true);
+  lo = __builtin_bit_cast(uint32_t, a);
+  hi = __builtin_bit_cast(uint32_t, b);
+}
+
+// A lane's 32 bytes of one block as an operand: as they are, or (EXACT)
+// converted to bf16, 8 values for each of four instructions
+template <bool EXACT>
+struct Operand;
+template <>
+struct Operand<false> {
+  int8v_t v;
+  __device__ __forceinline__ void set(uint4_t a, uint4_t b) {
+    const uint4_t t[2] = {a, b};
+    __builtin_memcpy(&v, t, 32);
+  }
+};
+template <>
+struct Operand<true> {
+  uint4_t v[4];
+  __device__ __forceinline__ void set(uint4_t a, uint4_t b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      fp8_to_bf16(a[i], lo, hi);
+      v[i >> 1][2 * (i & 1)] = lo;
+      v[i >> 1][2 * (i & 1) + 1] = hi;
+      fp8_to_bf16(b[i], lo, hi);
+      v[2 + (i >> 1)][2 * (i & 1)] = lo;
+      v[2 + (i >> 1)][2 * (i & 1) + 1] = hi;
+    }
+  }
+};
+
+// the sum over one block of k, from zero
+__device__ __forceinline__ float4_t block_sum(const Operand<false>& a, const Operand<false>& b) {
+  return mfma_fp8(a.v, b.v);
+}
+__device__ __forceinline__ float4_t block_sum(const Operand<true>& a, const Operand<true>& b) {
+  float4_t c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v[i]),
+                                                __builtin_bit_cast(bf16x8_t, b.v[i]), c, 0, 0, 0);
+  return c;
+}
+
+template <int YDT>
+__device__ __forceinline__ void store1(void* y, int64_t i, float v) {
+  if constexpr (YDT == WQ_F32) static_cast<float*>(y)[i] = v;
+  else static_cast<uint16_t*>(y)[i] = (uint16_t)pack2<YDT>(v, 0.0f);
+}
+// four consecutive values; `wide` when the address allows one store
+template <int YDT>
+__device__ __forceinline__ void store4(void* y, int64_t i, float4_t v, bool wide, int count) {
+  if (wide) {
+    if constexpr (YDT == WQ_F32) {
+      *reinterpret_cast<float4_t*>(static_cast<float*>(y) + i) = v;
+    } else {
+      *reinterpret_cast<uint2_t*>(static_cast<uint16_t*>(y) + i) =
+          uint2_t{pack2<YDT>(v[0], v[1]), pack2<YDT>(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) store1<YDT>(y, i + e, v[e]);
+  }
+}
+
+// ------------------------------------------------------------------ decode
+template <int YDT, int NW>
+__global__ __launch_bounds__(NW * 64) void fp8_decode_kernel(Fp8Args a) {
+  constexpr int D = 4;                       // blocks of k in flight per wave
+  __shared__ float4_t red[NW][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int nl = lane & 15, kq = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16;
+  const uint8_t* const wrow = a.w + (int64_t)min(n0 + nl, a.n - 1) * a.k;
+  const int tok = min(nl, a.m - 1);
+  const uint8_t* const xrow = a.x + (int64_t)tok * a.k;
+  const float* const swr = a.sw + (int64_t)(n0 / kF8Block) * a.kb;
+  float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int b0 = wave; b0 < a.kb; b0 += NW * D) {
+    uint4_t wv[D][2], xv[D][2];
+    float s[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int b = b0 + d * NW;
+      if (b >= a.kb) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = b * kF8Block + kq * 16 + j * 64;
+        const bool in = c < a.k;             // k is a multiple of 16
+        wv[d][j] = in ? *reinterpret_cast<const uint4_t*>(wrow + c) : uint4_t{0, 0, 0, 0};
+        xv[d][j] = in ? *reinterpret_cast<const uint4_t*>(xrow + c) : uint4_t{0, 0, 0, 0};
+      }
+      s[d] = a.sx[(int64_t)b * a.m + tok] * swr[b];
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (b0 + d * NW >= a.kb) break;
+      Operand<YDT == WQ_F32> wa, xb;
+      wa.set(wv[d][0], wv[d][1]);
+      xb.set(xv[d][0], xv[d][1]);
+      const float4_t c = block_sum(wa, xb);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s[d], acc[e]);
+    }
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+    float4_t t = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) t += red[w][lane];
+    const int n = n0 + kq * 4;
+    if (nl < a.m && n < a.n)
+      store4<YDT>(a.y, (int64_t)nl * a.n + n, t, (a.n & 3) == 0, a.n - n);
+  }
+}
+
+// -------------------------------------------------------------------- gemm
+// direct global -> LDS load with a uniform base and a 32-bit lane offset
+__device__ __forceinline__ void lds_dma16_s(const void* base, uint32_t off, lds_void_t* lds) {
+  const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l)
+               : "memory");
+}
+
+// tile t of T in an order in which each XCD (workgroups reach the 8 XCDs in
+// turn) runs a contiguous range, walked GM token tiles at a time
+__device__ __forceinline__ void tile_of_block(int bid, int T, int tm, int tn, int& im, int& in) {
+  constexpr int GM = 4;
+  const int q = T >> 3, r = T & 7, xcd = bid & 7;
+  const int t = xcd * q + min(xcd, r) + (bid >> 3);
+  const int per = GM * tn, g = t / per, w = t - g * per;
+  const int gm = min(GM, tm - g * GM);
+  im = g * GM + w % gm;
+  in = w / gm;
+}
+
+template <int WN, int WM, int TN, int TM>
+constexpr int fp8_buf_bytes() {
+  return (WN * TN + WM * TM) * 16 * kF8Block + WM * TM * 16 * 4;
+}
+
+// WN x WM waves, each TN x TM tiles of 16 features x 16 tokens
+template <int YDT, int WN, int WM, int TN, int TM>
+__global__ __launch_bounds__(WN * WM * 64) void fp8_gemm_kernel(Fp8Args a, int tm, int tn) {
+  constexpr int NW = WN * WM;
+  constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
+  constexpr int BUF = fp8_buf_bytes<WN, WM, TN, TM>();
+  constexpr int WI = BN / 8 / NW, XI = BM / 8 / NW;      // direct loads per wave
+  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0, "whole loads");
+  static_assert(kF8Block % (TN * 16) == 0, "a wave's features share a scale block");
+  extern __shared__ uint4_t dsm[];
+  char* const lds = reinterpret_cast<char*>(dsm);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+  const int nl = lane & 15, kq = lane >> 4;
+  int im, in;
+  tile_of_block((int)blockIdx.x, tm * tn, tm, tn, im, in);
+  const int n0 = in * BN, m0 = im * BM;
+  // this workgroup's blocks of k
+  const int per = (a.kb + a.splits - 1) / a.splits;
+  const int b0 = (int)blockIdx.y * per, b1 = min(b0 + per, a.kb);
+
+  // lane l of a load brings chunk (l & 7) ^ (row & 7) of row l / 8 into slot
+  // l & 7 of that row, so the 8 rows of an operand read that share LDS banks
+  // hold the same chunk in 8 different slots.  Rows past the end read the last
+  // row; their results are not stored.
+  const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
+  const uint8_t* const wbase = a.w + (int64_t)n0 * a.k;
+  const uint8_t* const xbase = a.x + (int64_t)m0 * a.k;
+  uint32_t woff[WI], xoff[XI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+    woff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.n - 1 - n0) * (uint32_t)a.k + lc;
+#pragma unroll
+  for (int i = 0; i < XI; ++i)
+    xoff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.m - 1 - m0) * (uint32_t)a.k + lc;
+
+  auto issue = [&](int b, int buf) {
+    char* const wl = lds + buf * BUF;
+    char* const xl = wl + BN * kF8Block;
+    char* const sl = xl + BM * kF8Block;
+    const int kc = b * kF8Block;
+    if (kc + kF8Block <= a.k) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+        lds_dma16_s(wbase + kc, woff[i], (lds_void_t*)(wl + (i * NW + wave) * 1024));
+#pragma unroll
+      for (int i = 0; i < XI; ++i)
+        lds_dma16_s(xbase + kc, xoff[i], (lds_void_t*)(xl + (i * NW + wave) * 1024));
+    } else {                               // chunks past k are zeros in both
+      const bool past = kc + lc >= a.k;
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+        lds_dma16(past ? (const void*)&kZero16 : wbase + kc + woff[i],
+                  (lds_void_t*)(wl + (i * NW + wave) * 1024));
+#pragma unroll
+      for (int i = 0; i < XI; ++i)
+        lds_dma16(past ? (const void*)&kZero16 : xbase + kc + xoff[i],
+                  (lds_void_t*)(xl + (i * NW + wave) * 1024));
+    }
+    // the tokens' scales of this block, by the first BM / 64 waves
+    if (wave < BM / 64)
+      lds_dma4(a.sx + (int64_t)b * a.m + min(m0 + wave * 64 + lane, a.m - 1),
+               (lds_void_t*)(sl + wave * 256));
+  };
+
+  // the weight scales of 64 blocks at a time, one per lane
+  const int nbw = min((n0 + wn * TN * 16) / kF8Block, (a.n - 1) / kF8Block);
+  const float* const swr = a.sw + (int64_t)nbw * a.kb;
+  float swl = 0.0f;
+
+  float4_t acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // slots of this lane's two chunks in its operand rows (row & 7 = nl & 7)
+  const int s0 = (kq ^ (nl & 7)) * 16, s1 = ((kq + 4) ^ (nl & 7)) * 16;
+  if (b0 < b1) issue(b0, 0);
+  for (int b = b0; b < b1; ++b) {
+    const int buf = (b - b0) & 1;
+    if (((b - b0) & 63) == 0) swl = swr[min(b + lane, a.kb - 1)];
+    vm_wait<0>();
+    wg_barrier();
+    if (b + 1 < b1) issue(b + 1, buf ^ 1);
+    const char* const wl = lds + buf * BUF + (wn * TN * 16 + nl) * kF8Block;
+    const char* const xl = lds + buf * BUF + (BN + wm * TM * 16 + nl) * kF8Block;
+    const float* const sl =
+        reinterpret_cast<const float*>(lds + buf * BUF + (BN + BM) * kF8Block) + wm * TM * 16 + nl;
+    const float sw =
+        __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), (b - b0) & 63));
+    Operand<YDT == WQ_F32> xb[TM];
+    float s[TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      xb[j].set(*reinterpret_cast<const uint4_t*>(xl + j * 16 * kF8Block + s0),
+                *reinterpret_cast<const uint4_t*>(xl + j * 16 * kF8Block + s1));
+      s[j] = sl[j * 16] * sw;
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      Operand<YDT == WQ_F32> wa;
+      wa.set(*reinterpret_cast<const uint4_t*>(wl + i * 16 * kF8Block + s0),
+             *reinterpret_cast<const uint4_t*>(wl + i * 16 * kF8Block + s1));
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const float4_t c = block_sum(wa, xb[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], s[j], acc[i][j][e]);
+      }
+    }
+  }
+
+  void* const out = a.part != nullptr ? a.part + (int64_t)blockIdx.y * a.m * a.n : a.y;
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int m = m0 + (wm * TM + j) * 16 + nl;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int n = n0 + (wn * TN + i) * 16 + kq * 4;
+      if (m < a.m && n < a.n) {
+        const int64_t o = (int64_t)m * a.n + n;
+        const bool wide = (a.n & 3) == 0;
+        if (a.part != nullptr) store4<WQ_F32>(out, o, acc[i][j], wide, a.n - n);
+        else store4<YDT>(out, o, acc[i][j], wide, a.n - n);
+      }
+    }
+  }
+}
+
+// y = the sum of the splits' totals, in their order
+template <int YDT>
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ part, int splits,
+                                                       int64_t count, void* y) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  if (i + 4 <= count && (count & 3) == 0) {
+    float4_t t = *reinterpret_cast<const float4_t*>(part + i);
+    for (int s = 1; s < splits; ++s) t += *reinterpret_cast<const float4_t*>(part + s * count + i);
+    store4<YDT>(y, i, t, true, 4);
+  } else {
+    for (int64_t e = i; e < min(i + 4, count); ++e) {
+      float t = part[e];
+      for (int s = 1; s < splits; ++s) t += part[s * count + e];
+      store1<YDT>(y, e, t);
+    }
+  }
+}
+
+template <int YDT, int WN, int WM, int TN, int TM>
+hipError_t gemm_launch(const Fp8Args& a, hipStream_t s) {
+  constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
+  constexpr int bytes = 2 * fp8_buf_bytes<WN, WM, TN, TM>();
+  auto* kern = &fp8_gemm_kernel<YDT, WN, WM, TN, TM>;
+  static std::atomic<bool> ready{false};
+  if (!ready.load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    ready.store(true, std::memory_order_release);
+  }
+  const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
+  kern<<<dim3((unsigned)(tm * tn), (unsigned)a.splits), WN * WM * 64, bytes, s>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
+template <int YDT>
+hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
+  if (p.tile == 0) {
+    fp8_decode_kernel<YDT, 8><<<dim3((unsigned)((a.n + 15) / 16)), 512, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  // the exact products need twice the operand registers: smaller wave tiles
+  constexpr int TM2 = YDT == WQ_F32 ? 4 : 8;
+  hipError_t e = p.tile == 2 ? gemm_launch<YDT, 4, 2, 4, TM2>(a, s)
+                             : gemm_launch<YDT, 2, 2, 4, 4>(a, s);
+  if (e != hipSuccess || a.part == nullptr) return e;
+  const int64_t count = (int64_t)a.m * a.n;
+  fp8_join_kernel<YDT><<<dim3((unsigned)((count + 1023) / 1024)), 256, 0, s>>>(a.part, a.splits,
+                                                                              count, a.y);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k) {
+  Fp8Plan p{};
+  p.splits = 1;
+  const int64_t kb = (k + kF8Block - 1) / kF8Block;
+  if (m <= 16) {
+    p.tile = 0;
+    return p;
+  }
+  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
+  p.tile = big >= 192 ? 2 : 1;
+  if (p.tile == 1) {
+    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
+    int64_t s = std::max<int64_t>(1, 512 / tiles);
+    s = std::min<int64_t>(s, std::max<int64_t>(1, kb / 4));
+    while (s > 1 && s * m * n * 4 > ((int64_t)64 << 20)) --s;
+    // no empty split
+    const int64_t per = (kb + s - 1) / s;
+    p.splits = (int)((kb + per - 1) / per);
+  }
+  p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
+  return p;
+}
+
+hipError_t launch_linear_fp8(const uint8_t* x, const float* sx, int64_t m, const wq_weight* w,
+                             void* y, int ydt, const Fp8Plan& plan, float* part, hipStream_t s) {
+  const Fp8Args a{x, sx, static_cast<const uint8_t*>(w->codes),
+                  static_cast<const float*>(w->scales), y, plan.splits > 1 ? part : nullptr,
+                  (int)m, (int)w->n, (int)w->k, (int)((w->k + kF8Block - 1) / kF8Block),
+                  plan.splits};
+  if (ydt == WQ_F32) return fp8_ydt<WQ_F32>(a, plan, s);
+  if (ydt == WQ_BF16) return fp8_ydt<WQ_BF16>(a, plan, s);
+  return fp8_ydt<WQ_F16>(a, plan, s);
+}
+
+}  // namespace wq

@@ -1,0 +1,117 @@
+// Device helpers shared by the FP8 and mixture-of-experts kernels: 16-bit
+// vector access, E4M3 scales and conversions, reductions inside a wave.
+#pragma once
+
+#include "internal.h"
+
+namespace wq {
+
+constexpr int kF8Block = 128;      // elements that share an FP8 scale
+constexpr float kF8Max = 448.0f;   // largest finite E4M3 value
+
+typedef float float2v_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
+typedef unsigned int uint2_t __attribute__((ext_vector_type(2)));
+typedef int int8v_t __attribute__((ext_vector_type(8)));
+
+// the two 16-bit values of a word (low half first) as fp32
+template <int DT>
+__device__ __forceinline__ void unpack2(uint32_t u, float& lo, float& hi) {
+  if constexpr (DT == WQ_BF16) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xFFFF0000u);
+  } else {
+    half2_t h;
+    __builtin_memcpy(&h, &u, 4);
+    lo = (float)h.x;
+    hi = (float)h.y;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4_t raw, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2<DT>(raw[i], v[2 * i], v[2 * i + 1]);
+}
+
+// two fp32 values rounded to nearest even into one word (low half = lo);
+// unlike the integer rounding of f32_to_bf16_bits a NaN stays a NaN
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const float2v_t v = {as_f32(lo), as_f32(hi)};
+  uint32_t u;
+  if constexpr (DT == WQ_BF16) {
+    const bf16x2v_t b = __builtin_convertvector(v, bf16x2v_t);
+    __builtin_memcpy(&u, &b, 4);
+  } else {
+    const half2_t h = __builtin_convertvector(v, half2_t);
+    __builtin_memcpy(&u, &h, 4);
+  }
+  return u;
+}
+template <int DT>
+__device__ __forceinline__ uint4_t pack8(const float (&v)[8]) {
+  uint4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+  return o;
+}
+
+// four fp32 values -> four E4M3 bytes (nearest even)
+__device__ __forceinline__ uint32_t pack4_fp8(float a, float b, float c, float d) {
+  int o = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, o, true);
+}
+
+// The scale of a block whose largest magnitude has the fp32 bits `bits`
+// (sign cleared): amax / 448, 1 for a block of zeros, and never below the
+// smallest normal fp32 value, so that 1 / s stays finite and |v| * (1 / s)
+// at most 448.  The bits of an infinity or a NaN compare above every finite
+// magnitude, so a block that holds one gets that as its scale, and what is
+// read back from it is not finite either.
+__device__ __forceinline__ float fp8_scale(uint32_t bits) {
+  const float a = __uint_as_float(bits);
+  const float s = __fdiv_rn(a, kF8Max);
+  constexpr float kTiny = 1.17549435e-38f;
+  if (s < kTiny) return a == 0.0f ? 1.0f : kTiny;
+  return s;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+// largest value over each 16 lanes of a wave, in all of them (lane xor 1, xor
+// 2, then mirrored halves and rows)
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  v = max(v, dpp<0x140>(v));
+  return v;
+}
+// sum over each 16 lanes of a wave, in all of them
+__device__ __forceinline__ float sum16(float v) {
+  v += __uint_as_float(dpp<0xB1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x4E>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x141>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x140>(__float_as_uint(v)));
+  return v;
+}
+// sum over the wave, in every lane (uniform)
+__device__ __forceinline__ float sum64(float v) {
+  const int s = __float_as_int(sum16(v));
+  return (__int_as_float(__builtin_amdgcn_readlane(s, 0)) +
+          __int_as_float(__builtin_amdgcn_readlane(s, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(s, 32)) +
+          __int_as_float(__builtin_amdgcn_readlane(s, 48)));
+}
+
+// v / (1 + exp(-v)) with the hardware exponential and reciprocal (about 1e-6
+// relative for |v| up to 20; exp overflow gives the limit 0)
+__device__ __forceinline__ float silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
+
+}  // namespace wq

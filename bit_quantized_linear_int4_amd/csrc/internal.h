@@ -166,6 +166,44 @@ hipError_t launch_permute_cols(const uint16_t* src, int64_t rows, int64_t k,
 hipError_t launch_scale_cols(const uint16_t* src, int dt, int64_t rows, int64_t k,
                              const float* scale, uint16_t* dst, hipStream_t s);
 
+// residual addition + RMS norm, FP8 packers (arguments as in wq.h)
+hipError_t launch_add_rmsnorm(const uint16_t* x, int dt, int64_t m, int64_t k, int64_t ldx,
+                              const uint16_t* res, uint16_t* res_out, int64_t ldr,
+                              const uint16_t* gain, float eps, uint16_t* y, uint8_t* q,
+                              float* scales, hipStream_t s);
+hipError_t launch_quantize_fp8_rows(const uint16_t* x, const uint16_t* up, int dt, int64_t m,
+                                    int64_t k, uint8_t* q, float* scales, hipStream_t s);
+hipError_t launch_quantize_fp8_block(const uint16_t* w, int dt, int64_t n, int64_t k, uint8_t* q,
+                                     float* scales, hipStream_t s);
+
+struct Fp8Plan {
+  int tile;          // 0 = decode (m <= 16), 1 = 128 x 128 tiles, 2 = 256 x 256
+  int splits;        // parts of k summed by a second kernel (1 = none)
+  size_t ws_bytes;   // their fp32 totals
+};
+Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k);
+hipError_t launch_linear_fp8(const uint8_t* x, const float* sx, int64_t m, const wq_weight* w,
+                             void* y, int ydt, const Fp8Plan& plan, float* part, hipStream_t s);
+
+// mixture of experts: the launches of wq_moe (limits and sizes checked)
+constexpr int kMoeMaxExperts = 512, kMoeMaxTokens = 64, kMoeMaxTopK = 16;
+struct MoeCall {
+  const uint16_t* x;
+  int xdt;
+  int64_t t, h, e, i;
+  int top_k, renorm;
+  const uint16_t* router;    // or nullptr: `logits` is given
+  const float* logits;
+  const wq_weight *gate, *up, *down;
+  void* y;
+  int ydt;
+  int32_t* ids;
+  float* probs;
+  void* workspace;
+};
+size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t i);
+hipError_t launch_moe(const MoeCall& c, hipStream_t s);
+
 hipError_t launch_dequantize(const wq_weight* w, const float* levels16, void* out, int odt,
                              hipStream_t s);
 

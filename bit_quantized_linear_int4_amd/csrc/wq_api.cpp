@@ -62,6 +62,12 @@ wq_status check_weight(const wq_weight* w, bool linear_w4) {
       if (w->group != w->k || w->k % 16 != 0) return WQ_ERR_SHAPE;
       if (!aligned(w->scales, 4)) return WQ_ERR_ALIGN;
       return WQ_OK;
+    case WQ_FMT_FP8_BLOCK:
+      if (linear_w4) return WQ_ERR_UNSUPPORTED;
+      if (w->group != 128) return WQ_ERR_UNSUPPORTED;
+      if (w->k % 16 != 0) return WQ_ERR_SHAPE;
+      if (!aligned(w->scales, 4)) return WQ_ERR_ALIGN;
+      return WQ_OK;
     default:
       return WQ_ERR_UNSUPPORTED;
   }
@@ -396,6 +402,120 @@ wq_status wq_scale_columns(const void* src, int32_t dt, int64_t rows, int64_t k,
   return hip_status(launch_scale_cols(static_cast<const uint16_t*>(src), dt, rows, k, scale,
                                       static_cast<uint16_t*>(dst),
                                       static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_add_rmsnorm(const void* x, int32_t dt, int64_t m, int64_t k, int64_t ldx,
+                         const void* residual, void* residual_out, int64_t ldr,
+                         const void* gain, float eps, void* y, void* q, float* scales,
+                         void* stream) {
+  if (x == nullptr || gain == nullptr || (y == nullptr && q == nullptr)) return WQ_ERR_NULL;
+  if ((residual == nullptr) != (residual_out == nullptr)) return WQ_ERR_NULL;
+  if ((q == nullptr) != (scales == nullptr)) return WQ_ERR_NULL;
+  if (!is16(dt)) return WQ_ERR_UNSUPPORTED;
+  if (!sizes_ok(m, k) || k % 8 != 0) return WQ_ERR_SHAPE;
+  if (ldx < k || ldx >= kMaxDim || ldx % 8 != 0) return WQ_ERR_SHAPE;
+  if (residual != nullptr && (ldr < k || ldr >= kMaxDim || ldr % 8 != 0)) return WQ_ERR_SHAPE;
+  if (!(eps >= 0.0f)) return WQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(gain, 16) || !aligned(residual, 16) ||
+      !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(q, 8) || !aligned(scales, 4))
+    return WQ_ERR_ALIGN;
+  return hip_status(launch_add_rmsnorm(
+      static_cast<const uint16_t*>(x), dt, m, k, ldx, static_cast<const uint16_t*>(residual),
+      static_cast<uint16_t*>(residual_out), ldr, static_cast<const uint16_t*>(gain), eps,
+      static_cast<uint16_t*>(y), static_cast<uint8_t*>(q), scales,
+      static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_quantize_fp8_rows(const void* x, const void* up, int32_t dt, int64_t m, int64_t k,
+                               void* q, float* scales, void* stream) {
+  if (x == nullptr || q == nullptr || scales == nullptr) return WQ_ERR_NULL;
+  if (!is16(dt)) return WQ_ERR_UNSUPPORTED;
+  if (!sizes_ok(m, k) || k % 8 != 0) return WQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(up, 16) || !aligned(q, 8) || !aligned(scales, 4))
+    return WQ_ERR_ALIGN;
+  return hip_status(launch_quantize_fp8_rows(
+      static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up), dt, m, k,
+      static_cast<uint8_t*>(q), scales, static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_quantize_fp8_block(const void* w, int32_t wdt, int64_t n, int64_t k, void* codes,
+                                float* scales, void* stream) {
+  if (w == nullptr || codes == nullptr || scales == nullptr) return WQ_ERR_NULL;
+  if (!is16(wdt)) return WQ_ERR_UNSUPPORTED;
+  if (!sizes_ok(n, k) || k % 16 != 0) return WQ_ERR_SHAPE;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return WQ_ERR_ALIGN;
+  return hip_status(launch_quantize_fp8_block(static_cast<const uint16_t*>(w), wdt, n, k,
+                                              static_cast<uint8_t*>(codes), scales,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t wq_linear_fp8_workspace(int64_t m, const wq_weight* w) {
+  if (check_weight(w, false) != WQ_OK || w->fmt != WQ_FMT_FP8_BLOCK) return 0;
+  if (!sizes_ok(m, w->k) || m > kMaxElems / w->n) return 0;
+  return plan_fp8(m, w->n, w->k).ws_bytes;
+}
+
+wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_weight* w,
+                        void* y, int32_t ydt, void* workspace, size_t ws_bytes, void* stream) {
+  if (q == nullptr || scales == nullptr || y == nullptr) return WQ_ERR_NULL;
+  const wq_status st = check_weight(w, false);
+  if (st != WQ_OK) return st;
+  if (w->fmt != WQ_FMT_FP8_BLOCK || !is_out(ydt)) return WQ_ERR_UNSUPPORTED;
+  if (!sizes_ok(m, w->k) || m > kMaxElems / w->n) return WQ_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(y, 16)) return WQ_ERR_ALIGN;
+  const Fp8Plan plan = plan_fp8(m, w->n, w->k);
+  if (plan.ws_bytes > 0) {
+    if (workspace == nullptr || ws_bytes < plan.ws_bytes) return WQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  }
+  return hip_status(launch_linear_fp8(static_cast<const uint8_t*>(q), scales, m, w, y, ydt, plan,
+                                      static_cast<float*>(workspace),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+size_t wq_moe_workspace(int64_t m, int32_t top_k, const wq_weight* gate, int64_t experts) {
+  if (gate == nullptr || m < 1 || m > kMoeMaxTokens || experts < 1 || experts > kMoeMaxExperts ||
+      top_k < 1 || top_k > kMoeMaxTopK || top_k > experts)
+    return 0;
+  if (check_weight(gate, gate->fmt != WQ_FMT_FP8_BLOCK) != WQ_OK || gate->n % experts != 0)
+    return 0;
+  return moe_ws_bytes(m, experts, top_k, gate->n / experts);
+}
+
+wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, const float* logits,
+                 int64_t experts, int32_t top_k, int32_t renormalize, const wq_weight* gate,
+                 const wq_weight* up, const wq_weight* down, void* y, int32_t ydt, int32_t* ids,
+                 float* probs, void* workspace, size_t ws_bytes, void* stream) {
+  if (x == nullptr || y == nullptr || (router == nullptr) == (logits == nullptr))
+    return WQ_ERR_NULL;
+  for (const wq_weight* w : {gate, up, down}) {
+    if (w == nullptr) return WQ_ERR_NULL;
+    const wq_status st = check_weight(w, w->fmt != WQ_FMT_FP8_BLOCK);
+    if (st != WQ_OK) return st;
+    if (w->fmt != WQ_FMT_INT4_ASYM && w->fmt != WQ_FMT_FP8_BLOCK) return WQ_ERR_UNSUPPORTED;
+    if (w->fmt != gate->fmt || w->perm != nullptr) return WQ_ERR_UNSUPPORTED;
+    if (w->fmt == WQ_FMT_INT4_ASYM && (!aligned(w->scales, 8) || !aligned(w->zeros, 2)))
+      return WQ_ERR_ALIGN;
+  }
+  if (!is16(xdt) || !is_out(ydt)) return WQ_ERR_UNSUPPORTED;
+  if (m < 1 || experts < 1 || top_k < 1 || top_k > experts) return WQ_ERR_SHAPE;
+  if (m > kMoeMaxTokens || experts > kMoeMaxExperts || top_k > kMoeMaxTopK)
+    return WQ_ERR_UNSUPPORTED;
+  if (gate->group != up->group || gate->group != down->group) return WQ_ERR_SHAPE;
+  const int64_t h = gate->k, i = down->k;
+  if (h % 128 != 0 || i % 128 != 0 || gate->n != experts * i || up->n != gate->n || up->k != h ||
+      down->n != experts * h)
+    return WQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(logits, 4) ||
+      !aligned(y, dt_bytes(ydt)) || !aligned(ids, 4) || !aligned(probs, 4))
+    return WQ_ERR_ALIGN;
+  if (workspace == nullptr || ws_bytes < moe_ws_bytes(m, experts, top_k, i))
+    return WQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  const MoeCall c{static_cast<const uint16_t*>(x), xdt, m, h, experts, i, top_k,
+                  renormalize ? 1 : 0, static_cast<const uint16_t*>(router), logits, gate, up,
+                  down, y, ydt, ids, probs, workspace};
+  return hip_status(launch_moe(c, static_cast<hipStream_t>(stream)));
 }
 
 wq_status wq_dequantize(const wq_weight* w, void* out, int32_t odt, void* stream) {

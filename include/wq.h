@@ -68,7 +68,8 @@ typedef enum {
   WQ_FMT_INT4_ASYM = 0,   /* wq_quantize_groupwise(bits=4, symmetric=0)       */
   WQ_FMT_NF4 = 1,         /* wq_pack_nf4                                      */
   WQ_FMT_INT8_SYM_ROW = 2,/* wq_quantize_groupwise(bits=8, symmetric=1, k)    */
-  WQ_FMT_FP4 = 3          /* wq_pack_fp4                                      */
+  WQ_FMT_FP4 = 3,         /* wq_pack_fp4                                      */
+  WQ_FMT_FP8_BLOCK = 4    /* wq_quantize_fp8_block                            */
 } wq_format;
 
 /*
@@ -98,6 +99,11 @@ typedef enum {
  *    x[:, perm] into its workspace before the multiply.  NULL: plain order.
  *  fmt = WQ_FMT_INT8_SYM_ROW:
  *    codes   int8 [n][k], 16-byte aligned; scales fp32 [n]; group = k.
+ *  fmt = WQ_FMT_FP8_BLOCK:
+ *    codes   E4M3 (OCP: largest 448, no infinities) [n][k], one byte each,
+ *            16-byte aligned, k % 16 == 0.
+ *    scales  fp32 [ceil(n/128)][ceil(k/128)], one per block of 128 rows x 128
+ *            columns (blocks at the ends may be smaller); group = 128.
  */
 typedef struct {
   int32_t fmt;            /* wq_format                                        */
@@ -341,10 +347,118 @@ wq_status wq_scale_columns(const void* src, int32_t dt, int64_t rows, int64_t k,
                            const float* scale, void* dst, void* stream);
 
 /*
+ * Residual addition and root-mean-square norm, with 16-bit and / or FP8
+ * outputs.  Per row of k values:
+ *   h = x + residual  (x alone when residual is NULL), in fp32
+ *   residual_out = round16(h)
+ *   v = h * rsqrt(sum(h^2) / k + eps) * gain, in fp32, of the unrounded h
+ *   y = round16(v)
+ *   per block b of 128 consecutive values (the last may be shorter):
+ *     s = max|v| / 448 (1.0 if 0; at least 2^-126),
+ *     q = E4M3(v * (1 / s)), scales[b][row] = s
+ *
+ * x, residual, residual_out, gain, y: dt in {WQ_F16, WQ_BF16}; x [m] rows of
+ * k, ldx elements apart; residual and residual_out [m] rows ldr apart; gain
+ * [k]; y [m][k]; q E4M3 [m][k]; scales fp32 [ceil(k/128)][m] (the scales of
+ * one block over all rows are contiguous).  residual and residual_out are
+ * both given or both NULL; residual_out may be the residual, or x with
+ * ldx == ldr (in place); no other output may overlap an input.  y may be
+ * NULL when q is given; q and scales are both given or both NULL.
+ * k % 8 == 0; ldx and ldr at least k and multiples of 8; m, k and the strides
+ * below 2^23; every 16-bit pointer 16-byte, q 8-byte, scales 4-byte aligned;
+ * eps >= 0.  Infinities and NaN follow the formula, within their row: a NaN
+ * makes all of v NaN; an infinity, or a sum of squares past the fp32 range
+ * (bf16 values above 1e18), makes v 0, and NaN where h is infinite.  A block
+ * of v with a NaN has a NaN scale.
+ */
+wq_status wq_add_rmsnorm(const void* x, int32_t dt, int64_t m, int64_t k, int64_t ldx,
+                         const void* residual, void* residual_out, int64_t ldr,
+                         const void* gain, float eps, void* y, void* q, float* scales,
+                         void* stream);
+
+/*
+ * Quantize activation rows to E4M3 with a scale per 128 values:
+ *   v = x, or silu(x) * up when up is given (silu(t) = t / (1 + exp(-t)), fp32),
+ *   s, q as in wq_add_rmsnorm.
+ * x, up: dt in {WQ_F16, WQ_BF16} [m][k], 16-byte aligned; q E4M3 [m][k], 8-byte
+ * aligned; scales fp32 [ceil(k/128)][m]; k % 8 == 0.  A NaN or an infinity
+ * makes the scale of its block one, and what q * s gives for that block is
+ * not finite where the value was not.
+ */
+wq_status wq_quantize_fp8_rows(const void* x, const void* up, int32_t dt, int64_t m, int64_t k,
+                               void* q, float* scales, void* stream);
+
+/*
+ * Quantize a weight to WQ_FMT_FP8_BLOCK: per block of 128 x 128
+ *   s = max|w| / 448 (1.0 if 0; at least 2^-126), q = E4M3(w * (1 / s)).
+ * w: wdt in {WQ_F16, WQ_BF16} [n][k], 16-byte aligned, k % 16 == 0; codes E4M3
+ * [n][k], 16-byte aligned; scales fp32 [ceil(n/128)][ceil(k/128)].
+ */
+wq_status wq_quantize_fp8_block(const void* w, int32_t wdt, int64_t n, int64_t k, void* codes,
+                                float* scales, void* stream);
+
+/*
+ * Scratch bytes of wq_linear_fp8 for this (m, weight) pair, at most 64 MiB:
+ * fp32 totals of the parts k is split into where the output tiles alone do
+ * not fill the GPU, 0 elsewhere (and for invalid arguments).
+ */
+size_t wq_linear_fp8_workspace(int64_t m, const wq_weight* w);
+
+/*
+ * FP8 linear with block scales:
+ *   y[i][j] = sum_b sx[b][i] * sw[j/128][b] * sum_{c in block b} q[i][c] * codes[j][c]
+ * Every sum over a block of 128 is one matrix instruction into fp32; the
+ * scaled sums are added in fp32, in an order fixed by the sizes (results are
+ * deterministic), and rounded once to ydt.
+ * q: E4M3 [m][k], 16-byte aligned; scales fp32 [ceil(k/128)][m] (as
+ * wq_add_rmsnorm and wq_quantize_fp8_rows write them); w: fmt FP8_BLOCK, any n;
+ * y: ydt in {F16, BF16, F32} [m][n], 16-byte aligned.  workspace: at least
+ * wq_linear_fp8_workspace(m, w) bytes, 256-byte aligned (may be NULL when that
+ * is 0).  m >= 1.  NaN codes give NaN in the rows or columns that hold them.
+ */
+wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_weight* w,
+                        void* y, int32_t ydt, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Mixture-of-experts layer for a few tokens (m <= 64):
+ *   l = x . router^T (fp32), or the caller's `logits`
+ *   p = softmax(l); the top_k experts of the largest l, ties to the lowest
+ *   index; renormalize != 0: their p divided by their sum
+ *   a = round16(p_j * silu(x . gate_e^T) * (x . up_e^T))
+ *   y = sum_j a . down_e^T
+ * with fp32 sums; a is rounded to xdt (as any 16-bit model keeps it), y to ydt.
+ * The order of every sum is fixed by the sizes and the routing: results are
+ * deterministic.  INT4 weights enter as (q - z) * s, unrounded.
+ *
+ * x: xdt in {F16, BF16} [m][h], 16-byte aligned.  router: xdt [experts][h],
+ * 16-byte aligned, or NULL with logits: fp32 [m][experts] (exactly one of the
+ * two).  gate, up: the experts' matrices stacked, n = experts * i, k = h; down:
+ * n = experts * h, k = i; all three in one format: INT4_ASYM without perm
+ * (equal groups) or FP8_BLOCK.  y: ydt in {F16, BF16, F32} [m][h].
+ * ids: int32 [m][top_k] and probs: fp32 [m][top_k], NULL or written, in the
+ * order of decreasing l.  workspace: at least wq_moe_workspace(m, top_k, gate,
+ * experts) bytes, 256-byte aligned.
+ * h and i multiples of 128; INT4 scales 8-byte and zeros 2-byte aligned;
+ * experts <= 512; top_k <= min(experts, 16).
+ *
+ * A logit of -inf masks its expert: its p is 0 and it is chosen only after all
+ * others; a token whose experts are all masked gets p = 0 and y = 0.  A choice
+ * with p = 0 is not computed.  A NaN or +inf logit gives NaN in that token's
+ * probs and y, and in no other token's.
+ * Errors: WQ_ERR_UNSUPPORTED for m, experts or top_k past their limits, mixed
+ * or other formats.
+ */
+size_t wq_moe_workspace(int64_t m, int32_t top_k, const wq_weight* gate, int64_t experts);
+wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, const float* logits,
+                 int64_t experts, int32_t top_k, int32_t renormalize, const wq_weight* gate,
+                 const wq_weight* up, const wq_weight* down, void* y, int32_t ydt, int32_t* ids,
+                 float* probs, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Dequantize a whole weight into 16-bit values (a test and debugging hook;
  * an act-order weight comes out in its stored column order):
  * INT4: fp(q - z) * s rounded to odt; NF4, FP4: L[code] * a_hat rounded to odt;
- * INT8: fp32(q) * s rounded to odt.  out: odt in {F16, BF16} [n][k].
+ * INT8 and FP8: fp32(q) * s rounded to odt.  out: odt in {F16, BF16} [n][k].
  */
 wq_status wq_dequantize(const wq_weight* w, void* out, int32_t odt, void* stream);
 

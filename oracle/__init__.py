@@ -34,6 +34,8 @@ Modules:
   nf4        -- NF4 codebook, blockwise absmax encode, double quantization
   llm_int8   -- LLM.int8() vector-wise int8 with outlier-column decomposition
   linear     -- the fp64 reference linear y = x . w_hat^T
+  fp8        -- E4M3 codes with block scales, RMS norm, gated product
+  moe        -- routing and the mixture-of-experts layer
 """
 
-from . import numerics, int4, nf4, llm_int8, linear  # noqa: F401
+from . import numerics, int4, nf4, llm_int8, linear, fp8, moe  # noqa: F401
