@@ -125,25 +125,33 @@ def _check(status, what):
         raise WqError(status, f"{what}: {wq_status_string(status)}")
 
 
+_DTYPES = None
+
+
 def _dt(t):
-    import torch
-    m = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
-    if t.dtype not in m:
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+    d = _DTYPES.get(t.dtype)
+    if d is None:
         raise WqError(4, f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return d
 
 
+# Addresses and streams go to ctypes as plain integers (its void* arguments
+# take them), which costs less than wrapping each one.
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, t):
-    import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 # ------------------------------------------------------------ validation
@@ -168,7 +176,7 @@ def _dense(what, name, t, nbytes=None, shape=None):
     (if given)."""
     if t is None:
         _fail(what, f"{name} is required")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         _fail(what, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         _fail(what, f"{name} is not contiguous")
@@ -181,19 +189,20 @@ def _on_gpu(what, *ts):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            _fail(what, "tensors must be GPU tensors", _ERR_UNSUP)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            _fail(what, "tensors are on different devices", _ERR_UNSUP)
+        d = t.get_device()          # -1 for a CPU tensor
+        if d != dev:
+            if d < 0:
+                _fail(what, "tensors must be GPU tensors", _ERR_UNSUP)
+            if dev is not None:
+                _fail(what, "tensors are on different devices", _ERR_UNSUP)
+            dev = d
 
 
 def _matrix(what, name, t):
     if t is None or t.dim() != 2:
         _fail(what, f"{name} must be a 2-D [rows][k] tensor")
     _dense(what, name, t)
-    return int(t.shape[0]), int(t.shape[1])
+    return t.shape
 
 
 def _weight_tensors(what, w):
@@ -247,16 +256,9 @@ class QuantizedWeight:
         self.perm = perm          # INT4 act-order: device int32 [k], or None
 
     def descriptor(self):
-        d = _Weight()
-        d.fmt, d.group, d.n, d.k = self.fmt, self.group, self.n, self.k
-        d.codes = self.codes.data_ptr()
-        d.scales = self.scales.data_ptr()
-        d.zeros = self.zeros.data_ptr() if self.zeros is not None else None
-        d.scales2 = self.scales2.data_ptr() if self.scales2 is not None else None
-        d.group2 = self.group2
-        d.reserved = 0
-        d.perm = self.perm.data_ptr() if self.perm is not None else None
-        return d
+        return _Weight(self.fmt, self.group, self.n, self.k, self.codes.data_ptr(),
+                       self.scales.data_ptr(), _ptr(self.zeros), _ptr(self.scales2), self.group2,
+                       0, _ptr(self.perm))
 
     def nbytes(self):
         return sum(t.numel() * t.element_size()
