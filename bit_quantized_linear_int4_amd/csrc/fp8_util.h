@@ -78,6 +78,19 @@ __device__ __forceinline__ float fp8_scale(uint32_t bits) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// *(T*)(base + off) with a base that is the same in every lane.  The empty asm
+// holds the base in scalar registers and the offset in one 32-bit register
+// until here, so the load takes the form with a scalar base and a lane offset;
+// left to itself the compiler keeps a 64-bit address per lane and load in
+// vector registers across a loop.
+template <typename T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t off) {
+  uint64_t b = reinterpret_cast<uint64_t>(base);
+  asm("" : "+s"(b), "+v"(off));
+  using G = const __attribute__((address_space(1))) char*;
+  return *(const __attribute__((address_space(1))) T*)((G)b + off);
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);

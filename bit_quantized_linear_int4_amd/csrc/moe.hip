@@ -12,10 +12,10 @@
 //                 walks units of 16 gate rows and the same 16 up rows of one
 //                 expert; its waves split k.  It stores
 //                 a = round16(p * silu(g) * u) for every token of the expert.
-//                 The first workgroup also leaves the table of active experts.
 //   3. down       a workgroup owns 16 rows of y over all active experts, whose
 //                 columns form one long k that its waves split; nothing leaves
 //                 the workgroup but y, and the order of the sum is fixed.
+// The first workgroup of 2 leaves the routing (experts, rows, tokens) for 3.
 //
 // The multiply runs on v_mfma_f32_16x16x32 with up to 16 tokens as the A
 // operand and 16 weight rows as the B operand.  INT4 codes are not rounded to
@@ -36,9 +36,15 @@ constexpr int kMaxE = kMoeMaxExperts, kMaxT = kMoeMaxTokens, kMaxK = kMoeMaxTopK
 
 // an expert some token is routed to
 struct Active {
-  uint64_t tokens;    // bit t: token t
   int32_t expert;
   int32_t slot;       // its first row of the intermediate, one row per token
+  int32_t cnt;        // its tokens
+  int32_t chunk;      // pieces of 16 tokens of the experts before it
+};
+constexpr int kMaxChunks = kMaxE + kMaxT * kMaxK / 16;
+// at most 16 tokens of one expert
+struct Chunk {
+  int32_t expert, slot, cnt;
 };
 
 struct MoeArgs {
@@ -47,8 +53,9 @@ struct MoeArgs {
   float* logits;             // [t][e]
   const void *gate, *gate_s, *up, *up_s, *down, *down_s;
   const uint8_t *gate_z, *up_z, *down_z;
-  Active* table;             // [min(e, t * top_k)], after the int32 count
-  int32_t* count;
+  int32_t* count;            // of chunks
+  Chunk* table;
+  uint8_t* slot_tok;         // [t * top_k] token of a row of the intermediate
   uint16_t* mid;             // [t * top_k][i]
   void* y;                   // [t][h]
   int32_t* ids;              // [t][top_k] or nullptr
@@ -123,7 +130,7 @@ struct Routing {
   uint8_t slot_tok[kMaxT * kMaxK];
   int32_t slot_of[kMaxE];
   Active act[kMaxE];
-  int32_t count;
+  int32_t count, chunks;
 };
 
 // The top_k of one token by one wave: lane j < top_k gets choice j.  A masked
@@ -201,27 +208,34 @@ __device__ void route(const MoeArgs& a, Routing& r) {
   }
   __syncthreads();
   if (wave == 0) {
-    int na = 0, slot = 0;
+    int na = 0, slot = 0, chunk = 0;
     for (int e0 = 0; e0 < a.e; e0 += 64) {
       const int e = e0 + lane;
       const uint64_t m = e < a.e ? ((uint64_t)r.mask[e][1] << 32) | r.mask[e][0] : 0;
       const int cnt = __popcll(m);
-      int run = cnt;                      // inclusive sum over the lanes
+      // inclusive sums over the lanes: tokens, and pieces of 16 above bit 16
+      const int own = cnt | ((cnt + 15) >> 4) << 16;
+      int run = own;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(run, o);
         if (lane >= o) run += v;
       }
+      const int before = run - own, all = __shfl(run, 63);
       const uint64_t on = __ballot(m != 0);
       if (m != 0) {
         const int at = na + __popcll(on & ((1ull << lane) - 1));
-        r.act[at] = Active{m, e, slot + run - cnt};
-        r.slot_of[e] = slot + run - cnt;
+        r.act[at] = Active{e, slot + (before & 0xFFFF), cnt, chunk + (before >> 16)};
+        r.slot_of[e] = slot + (before & 0xFFFF);
       }
       na += __popcll(on);
-      slot += __shfl(run, 63);
+      slot += all & 0xFFFF;
+      chunk += all >> 16;
     }
-    if (lane == 0) r.count = na;
+    if (lane == 0) {
+      r.count = na;
+      r.chunks = chunk;
+    }
   }
   __syncthreads();
   for (int i = tid; i < picks; i += NW * 64) {
@@ -241,45 +255,47 @@ __device__ void route(const MoeArgs& a, Routing& r) {
 // the B operand: lane (row nl, quarter kq).
 //   INT4 (S groups per unit): 16 bytes = codes [32 kq, 32 kq + 32) of the row.
 //   FP8: bytes [16 kq, +16) and [64 + 16 kq, +16).
+// The codes are kept as loaded: arithmetic on a value right after its load
+// would make the wave wait for it there.
 template <int FMT>
 struct Unit {
   uint4_t c[FMT == WQ_FMT_FP8_BLOCK ? 2 : 1];
-  uint32_t s[2];       // INT4: S fp16 scales; FP8: s[0] = the fp32 scale
-  uint32_t z;          // INT4: S zero points, 4 bits each
+  uint32_t s;          // FP8: the fp32 scale
 };
 
+// One matrix of an expert from a row tile on (uniform).  Every code load is a
+// uniform base plus a 32-bit lane offset that never changes.
+struct Tile {
+  const uint8_t *codes, *scales, *zeros;
+};
+template <int FMT>
+__device__ __forceinline__ uint32_t code_off(int k, int nl, int kq) {
+  return (uint32_t)(nl * (FMT == WQ_FMT_FP8_BLOCK ? k : k >> 1) + kq * 16);
+}
 template <int FMT, int S>
-__device__ __forceinline__ Unit<FMT> load_unit(const void* codes, const void* scales,
-                                               const uint8_t* zeros, int64_t row, int k, int u,
-                                               int kq) {
-  Unit<FMT> w;
-  const int ku = k >> 7;
+__device__ __forceinline__ Tile tile_at(const void* codes, const void* scales,
+                                        const uint8_t* zeros, int64_t row, int k) {
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  const uint8_t* s = static_cast<const uint8_t*>(scales);
+  const int64_t g = (k >> 7) * S;
+  if constexpr (FMT == WQ_FMT_FP8_BLOCK) return {c + row * k, s + (row >> 7) * g * 4, nullptr};
+  else return {c + row * (k >> 1), s + row * g * 2, zeros + row * ((g + 1) >> 1)};
+}
+
+template <int FMT>
+__device__ __forceinline__ void load_unit(Unit<FMT>& w, const Tile& t, uint32_t off, int u) {
   if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
-    const uint8_t* p = static_cast<const uint8_t*>(codes) + row * k + u * 128 + kq * 16;
-    w.c[0] = *reinterpret_cast<const uint4_t*>(p);
-    w.c[1] = *reinterpret_cast<const uint4_t*>(p + 64);
-    w.s[0] = static_cast<const uint32_t*>(scales)[(row >> 7) * ku + u];
-    w.s[1] = 0;
-    w.z = 0;
+    w.c[0] = load_at<uint4_t>(t.codes + u * 128, off);
+    w.c[1] = load_at<uint4_t>(t.codes + u * 128, off + 64);
+    w.s = reinterpret_cast<const uint32_t*>(t.scales)[u];
   } else {
-    w.c[0] = *reinterpret_cast<const uint4_t*>(static_cast<const uint8_t*>(codes) +
-                                               row * (k >> 1) + u * 64 + kq * 16);
-    const uint16_t* sp = static_cast<const uint16_t*>(scales) + row * (ku * S) + u * S;
-    const uint8_t* zp = zeros + row * ((ku * S + 1) >> 1) + ((u * S) >> 1);
-    w.s[1] = 0;
-    if constexpr (S == 1) {
-      w.s[0] = *sp;
-      w.z = (u & 1) ? (uint32_t)*zp >> 4 : (uint32_t)*zp & 15u;
-    } else if constexpr (S == 2) {
-      w.s[0] = *reinterpret_cast<const uint32_t*>(sp);
-      w.z = *zp;
-    } else {
-      w.s[0] = reinterpret_cast<const uint32_t*>(sp)[0];
-      w.s[1] = reinterpret_cast<const uint32_t*>(sp)[1];
-      w.z = (uint32_t)zp[0] | ((uint32_t)zp[1] << 8);
-    }
+    w.c[0] = load_at<uint4_t>(t.codes + u * 64, off);
   }
-  return w;
+}
+
+// INT4: the scale and zero point of one group in one word
+__device__ __forceinline__ uint32_t meta_word(uint32_t scale16, uint32_t zero4) {
+  return scale16 | zero4 << 16;
 }
 
 // first value of k (within the unit) that operand f of lane quarter kq holds
@@ -304,19 +320,22 @@ __device__ __forceinline__ uint4_t pair_order(uint4_t d) {
 // in the top four mantissa bits of 16.0 (fp16: bits 6-9, bf16: bits 3-6)
 template <int XDT>
 __device__ __forceinline__ uint4_t unpack_codes(uint32_t w) {
+  // the constants in vector registers, opaque to the compiler: one and-or
+  // instruction cannot take two scalar or literal operands
+  uint32_t m = XDT == WQ_BF16 ? 0x00780078u : 0x03C003C0u;
+  uint32_t b = XDT == WQ_BF16 ? 0x41804180u : 0x4C004C00u;
+  asm("" : "+v"(m), "+v"(b));
   uint4_t r;
   if constexpr (XDT == WQ_BF16) {
-    constexpr uint32_t kM = 0x00780078u, kB = 0x41804180u;
-    r[0] = ((w << 3) & kM) | kB;
-    r[1] = ((w >> 1) & kM) | kB;
-    r[2] = ((w >> 5) & kM) | kB;
-    r[3] = ((w >> 9) & kM) | kB;
+    r[0] = ((w << 3) & m) | b;
+    r[1] = ((w >> 1) & m) | b;
+    r[2] = ((w >> 5) & m) | b;
+    r[3] = ((w >> 9) & m) | b;
   } else {
-    constexpr uint32_t kM = 0x03C003C0u, kB = 0x4C004C00u;
-    r[0] = ((w << 6) & kM) | kB;
-    r[1] = ((w << 2) & kM) | kB;
-    r[2] = ((w >> 2) & kM) | kB;
-    r[3] = ((w >> 6) & kM) | kB;
+    r[0] = ((w << 6) & m) | b;
+    r[1] = ((w << 2) & m) | b;
+    r[2] = ((w >> 2) & m) | b;
+    r[3] = ((w >> 6) & m) | b;
   }
   return r;
 }
@@ -354,173 +373,440 @@ __device__ __forceinline__ uint4_t quarter_transpose(uint4_t v) {
   return uint4_t{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
 }
 
-// The activations of one unit as A operands, and (INT4) their sums per group
+// The intermediate is laid out as the down product reads it: the rows of one
+// chunk (cnt <= 16 tokens of one expert) together, within them [unit of k]
+// [operand f][row][quarter kq][8 values], the 8 values in pair order for INT4.
+// One operand load of a wave is then cnt * 64 contiguous bytes, and needs no
+// reordering.  Element offset of value k of row j from the chunk's begin:
 template <int FMT, int S>
+__device__ __forceinline__ int64_t mid_offset(int k, int j, int cnt) {
+  const int q = k & 127, e = k & 7;
+  int f, kq;
+  if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
+    f = 2 * (q >> 6) + ((q >> 3) & 1);
+    kq = (q >> 4) & 3;
+  } else if constexpr (S == 1) {
+    f = (q >> 3) & 3;
+    kq = q >> 5;
+  } else {
+    f = q >> 5;
+    kq = (q >> 3) & 3;
+  }
+  const int at = FMT == WQ_FMT_FP8_BLOCK ? e : (e < 4 ? 2 * e : 2 * e - 7);
+  return ((int64_t)((k >> 7) * 4 + f) * cnt + j) * 32 + kq * 8 + at;
+}
+
+// The activations of one unit as A operands
 struct Acts {
   uint4_t f[4];
-  float4_t sum[FMT == WQ_FMT_FP8_BLOCK ? 1 : S];
 };
 
-template <int XDT, int FMT, int S>
-__device__ __forceinline__ void prepare_acts(Acts<FMT, S>& x) {
-  if constexpr (FMT != WQ_FMT_FP8_BLOCK) {
+// acc[i] += x . w[i]^T over one unit of N matrices.  INT4: x in pair order,
+// meta[i][g] the word of group g of matrix i.
+template <int XDT, int FMT, int S, int N>
+__device__ __forceinline__ void unit_mac(const Unit<FMT> (&w)[N], const uint32_t (&meta)[N][S],
+                                         const Acts& x, float4_t (&acc)[N]) {
+  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float4_t c = zero;
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        c = mfma16<XDT>(x.f[f], unpack_fp8<XDT>(w[i].c[f >> 1][2 * (f & 1)],
+                                                w[i].c[f >> 1][2 * (f & 1) + 1]), c);
+      const float s = __uint_as_float(w[i].s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(c[e], s, acc[i][e]);
+    }
+  } else {
     constexpr uint32_t kOne = XDT == WQ_BF16 ? 0x3F803F80u : 0x3C003C00u;
     const uint4_t ones = {kOne, kOne, kOne, kOne};
+    uint4_t q[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = S == 1 ? w[i].c[0] : quarter_transpose(w[i].c[0]);
 #pragma unroll
     for (int g = 0; g < S; ++g) {
-      x.sum[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      float4_t sum = zero, c[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) c[i] = zero;
 #pragma unroll
       for (int f = g * 4 / S; f < (g + 1) * 4 / S; ++f) {
-        x.f[f] = pair_order(x.f[f]);
-        x.sum[g] = mfma16<XDT>(x.f[f], ones, x.sum[g]);
+        sum = mfma16<XDT>(x.f[f], ones, sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma16<XDT>(x.f[f], unpack_codes<XDT>(q[i][f]), c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float s = f16_bits_to_f32((uint16_t)meta[i][g]);
+        const float z = 16.0f + (float)(meta[i][g] >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s, fmaf(-z, sum[e], c[i][e]), acc[i][e]);
       }
     }
   }
 }
 
-// acc += x . w^T over one unit
-template <int XDT, int FMT, int S>
-__device__ __forceinline__ void unit_mac(const Unit<FMT>& w, const Acts<FMT, S>& x, float4_t& acc) {
-  const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
-    float4_t c = zero;
+// ----------------------------------------------------------------- gate/up
+// The loads of the streams below are never under a branch: after one the
+// compiler no longer knows how many loads are in flight and waits for all of
+// them.  Positions past the end load the last valid data again, and lanes
+// without a token the row of the last one (their results are not used).
+//
+// `off`: byte offset of the lane's token row from base.
+template <int FMT, int S>
+__device__ __forceinline__ void load_acts(Acts& x, const uint16_t* base, uint32_t off, int u,
+                                          int kq) {
+  const char* const p = reinterpret_cast<const char*>(base) + u * 256;
+  const uint32_t lo = off + 2 * unit_k<FMT, S>(0, kq);
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
-      c = mfma16<XDT>(x.f[f], unpack_fp8<XDT>(w.c[f >> 1][2 * (f & 1)], w.c[f >> 1][2 * (f & 1) + 1]), c);
-    const float s = __uint_as_float(w.s[0]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s, acc[e]);
-  } else {
-    const uint4_t q = S == 1 ? w.c[0] : quarter_transpose(w.c[0]);
-#pragma unroll
-    for (int g = 0; g < S; ++g) {
-      float4_t c = zero;
-#pragma unroll
-      for (int f = g * 4 / S; f < (g + 1) * 4 / S; ++f)
-        c = mfma16<XDT>(x.f[f], unpack_codes<XDT>(q[f]), c);
-      const float s = f16_bits_to_f32((uint16_t)(w.s[g >> 1] >> (16 * (g & 1))));
-      const float z = 16.0f + (float)((w.z >> (4 * g)) & 15u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(s, fmaf(-z, x.sum[g][e], c[e]), acc[e]);
-    }
-  }
+  for (int f = 0; f < 4; ++f)
+    x.f[f] = load_at<uint4_t>(p, lo + 2 * (unit_k<FMT, S>(f, 0) - unit_k<FMT, S>(0, 0)));
 }
 
-// ----------------------------------------------------------------- gate/up
+// A workgroup walks tiles of 16 gate rows and the same up rows of one expert
+// after the other; its waves split k, two units each (`passes` rounds of that
+// where k is longer).  With one pass a wave meets the same values of k in
+// every tile, so it keeps the activations of the expert's tokens (up to 16 at a
+// time), in pair order, in registers, and the loop streams nothing but codes
+// and scales, one tile ahead and also across experts.
+//
+// The INT4 scales and zero points of a tile come in one load of each per
+// thread and group of a unit, and reach the lanes through LDS (two buffers).
+// Loaded by every wave for its own two units, two bytes and one byte from each
+// of 16 rows, they cost more than the codes: 444 against 300 us with them
+// left out, 64 tokens through 2 of 8 experts of 4096 x 14336.
 template <int XDT, int FMT, int S, int NW>
-__global__ __launch_bounds__(NW * 64) void moe_gate_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int passes) {
+  constexpr bool kInt4 = FMT == WQ_FMT_INT4_ASYM;
+  constexpr int GP = NW * 2 * S;       // groups of k per row and pass
   __shared__ Routing r;
-  __shared__ float4_t red[2][NW][64];
+  __shared__ float4_t red[2][2][NW][64];
+  __shared__ uint32_t meta[kInt4 ? 2 : 1][kInt4 ? 2 * GP * 16 : 1];
   route<NW>(a, r);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int nact = __builtin_amdgcn_readfirstlane(r.count);
   if (blockIdx.x == 0) {
-    for (int i = tid; i < nact; i += NW * 64) a.table[i] = r.act[i];
-    if (tid == 0) *a.count = nact;
+    for (int i = tid; i < nact; i += NW * 64) {
+      const Active ac = r.act[i];
+      for (int c = 0; c < ac.cnt; c += 16)
+        a.table[ac.chunk + (c >> 4)] = Chunk{ac.expert, ac.slot + c, min(16, ac.cnt - c)};
+    }
+    if (tid == 0) *a.count = r.chunks;
     for (int i = tid; i < a.t * a.top_k; i += NW * 64) {
+      a.slot_tok[i] = r.slot_tok[i];
       if (a.ids != nullptr) a.ids[i] = r.ids[i];
       if (a.probs != nullptr) a.probs[i] = r.probs[i];
     }
   }
-  const int tiles = a.i >> 4, units = nact * tiles, ku = a.h >> 7;
+  const int tiles = a.i >> 4, units = nact * tiles, ku = a.h >> 7, groups = ku * S;
   const int per = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per, u1 = min(u0 + per, units);
-  for (int un = u0; un < u1; ++un) {
-    const int ai = un / tiles, tile = un - ai * tiles;
-    const int expert = __builtin_amdgcn_readfirstlane(r.act[ai].expert);
-    const int slot = __builtin_amdgcn_readfirstlane(r.act[ai].slot);
-    const int cnt = __builtin_amdgcn_readfirstlane(__popcll(r.act[ai].tokens));
-    const int64_t row = (int64_t)expert * a.i + tile * 16 + nl;
-    for (int c0 = 0; c0 < cnt; c0 += 16) {
-      const bool on = c0 + nl < cnt;
-      const uint16_t* const xr =
-          a.x + (int64_t)(on ? r.slot_tok[slot + c0 + nl] : 0) * a.h;
-      float4_t ga = {0, 0, 0, 0}, ua = {0, 0, 0, 0};
-      for (int u = wave; u < ku; u += NW) {
-        const Unit<FMT> gw = load_unit<FMT, S>(a.gate, a.gate_s, a.gate_z, row, a.h, u, kq);
-        const Unit<FMT> uw = load_unit<FMT, S>(a.up, a.up_s, a.up_z, row, a.h, u, kq);
-        Acts<FMT, S> x;
+  if (u0 >= u1) return;
+  const uint32_t off = code_off<FMT>(a.h, nl, kq);
+
+  // position in the stream: tiles [lo, hi) of one expert for its tokens from
+  // c0 on, then for the next 16 of them, then the next expert
+  struct Pos {
+    int64_t row;                       // first gate row of the expert
+    int un, lo, hi, c0, pass, slot, cnt;
+    int fresh;                         // other activations than the step before
+  };
+  auto enter = [&](Pos& p) {           // the expert of tile p.un
+    const int ai = p.un / tiles;
+    const Active ac = r.act[ai];
+    p.lo = p.un;
+    p.hi = min(u1, (ai + 1) * tiles);
+    p.slot = __builtin_amdgcn_readfirstlane(ac.slot);
+    p.cnt = __builtin_amdgcn_readfirstlane(ac.cnt);
+    p.row = (int64_t)__builtin_amdgcn_readfirstlane(ac.expert) * a.i - (int64_t)ai * a.i;
+  };
+  auto advance = [&](Pos& p) {
+    p.fresh = passes > 1;
+    if (++p.pass < passes) return;
+    p.pass = 0;
+    if (++p.un < p.hi) return;
+    p.fresh = true;
+    p.c0 += 16;
+    if (p.c0 < p.cnt) {
+      p.un = p.lo;
+      return;
+    }
+    p.c0 = 0;
+    if (p.un < u1) enter(p);
+  };
+  auto unit_of = [&](const Pos& p) { return (p.pass * NW + wave) * 2; };
+  auto row_of = [&](const Pos& p) { return p.row + (int64_t)min(p.un, u1 - 1) * 16; };
+  // unit u + j of both matrices at position p
+  auto load = [&](const Pos& p, int j, Unit<FMT> (&w)[2]) {
+    const int u = min(unit_of(p) + j, ku - 1);
+    const int64_t row = row_of(p);
+    load_unit<FMT>(w[0], tile_at<FMT, S>(a.gate, a.gate_s, a.gate_z, row, a.h), off, u);
+    load_unit<FMT>(w[1], tile_at<FMT, S>(a.up, a.up_s, a.up_z, row, a.h), off, u);
+  };
+  // this thread's share of a tile's 2 x 16 x GP metadata words: words tid +
+  // NW * 64 * i in the order [matrix][row][group]
+  uint32_t ms[S], mz[S];
+  auto load_meta = [&](const Pos& p) {
+    const int64_t row = row_of(p);
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          x.f[f] = on ? *reinterpret_cast<const uint4_t*>(xr + u * 128 + unit_k<FMT, S>(f, kq))
-                      : uint4_t{0, 0, 0, 0};
-        prepare_acts<XDT, FMT, S>(x);
-        unit_mac<XDT, FMT, S>(gw, x, ga);
-        unit_mac<XDT, FMT, S>(uw, x, ua);
+    for (int i = 0; i < S; ++i) {
+      const int e = tid + NW * 64 * i, mat = e / (16 * GP), rw = (e / GP) & 15;
+      const int g = min(p.pass * GP + e % GP, groups - 1);
+      const Tile t = mat ? tile_at<FMT, S>(a.up, a.up_s, a.up_z, row, a.h)
+                         : tile_at<FMT, S>(a.gate, a.gate_s, a.gate_z, row, a.h);
+      ms[i] = *reinterpret_cast<const uint16_t*>(t.scales + (rw * groups + g) * 2);
+      mz[i] = t.zeros[rw * ((groups + 1) >> 1) + (g >> 1)];
+    }
+  };
+  auto keep_meta = [&](const Pos& p, int buf) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int e = tid + NW * 64 * i, mat = e / (16 * GP), rw = (e / GP) & 15;
+      const int g = min(p.pass * GP + e % GP, groups - 1);
+      meta[buf][(mat * GP + e % GP) * 16 + rw] = meta_word(ms[i], (mz[i] >> (4 * (g & 1))) & 15u);
+    }
+  };
+
+  float4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  int flip = 0, rflip = 0;
+  Pos cur{0, u0, 0, 0, 0, 0, 0, 0, 1};
+  enter(cur);
+  Acts x0, x1;                         // of the wave's two units
+  // a unit's registers take the next tile's as soon as it is multiplied
+  Unit<FMT> w0[2], w1[2];
+  if constexpr (kInt4) load_meta(cur);
+  // in this order, as the loop waits for them
+  load(cur, 0, w0);
+  __builtin_amdgcn_sched_barrier(0);
+  load(cur, 1, w1);
+  if constexpr (kInt4) {
+    keep_meta(cur, 0);
+    lgkm_wait0();
+    wg_barrier();
+  }
+  while (cur.un < u1) {
+    const int u = unit_of(cur);
+    Pos nxt = cur;
+    advance(nxt);
+    if (cur.fresh) {
+      const uint32_t tok = r.slot_tok[cur.slot + min(cur.c0 + nl, cur.cnt - 1)];
+      const uint32_t xo = tok * (uint32_t)(a.h * 2);
+      load_acts<FMT, S>(x0, a.x, xo, min(u, ku - 1), kq);
+      load_acts<FMT, S>(x1, a.x, xo, min(u + 1, ku - 1), kq);
+      vm_wait<0>();
+      // units past the end of k add nothing
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if (u >= ku) x0.f[f] = uint4_t{0, 0, 0, 0};
+        if (u + 1 >= ku) x1.f[f] = uint4_t{0, 0, 0, 0};
+        if constexpr (kInt4) {
+          x0.f[f] = pair_order(x0.f[f]);
+          x1.f[f] = pair_order(x1.f[f]);
+        }
       }
-      red[0][wave][lane] = ga;
-      red[1][wave][lane] = ua;
-      __syncthreads();
+    }
+    // the words of unit j of both matrices
+    auto read_meta = [&](int j, uint32_t (&m)[2][S]) {
+      if constexpr (kInt4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < S; ++g)
+            m[i][g] = meta[flip][(i * GP + (2 * wave + j) * S + g) * 16 + nl];
+      }
+    };
+    if constexpr (kInt4) load_meta(nxt);
+    uint32_t m[2][S];
+    read_meta(0, m);
+    // the barriers keep the compiler from unpacking everything at once, which
+    // would not fit the registers
+    __builtin_amdgcn_sched_barrier(0);
+    unit_mac<XDT, FMT, S, 2>(w0, m, x0, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load(nxt, 0, w0);
+    read_meta(1, m);
+    __builtin_amdgcn_sched_barrier(0);
+    unit_mac<XDT, FMT, S, 2>(w1, m, x1, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    load(nxt, 1, w1);
+    if constexpr (kInt4) keep_meta(nxt, flip ^ 1);
+    const bool last = cur.pass + 1 == passes;
+    // the buffers of the step before are free: every wave has passed the
+    // barrier after its last read of them
+    if (last) {
+      red[rflip][0][wave][lane] = acc[0];
+      red[rflip][1][wave][lane] = acc[1];
+      acc[0] = acc[1] = float4_t{0, 0, 0, 0};
+    }
+    if (kInt4 || last) {
+      lgkm_wait0();
+      wg_barrier();                    // the loads stay in flight
+    }
+    if (last) {
       // value (token j, row n) of the tile sits in lane 16 (j / 4) + n, element j % 4
       if (tid < 256) {
         const int j = tid >> 4, n = tid & 15, l = (j >> 2) * 16 + n, e = j & 3;
-        float g = 0.0f, u = 0.0f;
+        float g = 0.0f, v = 0.0f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          g += red[0][w][l][e];
-          u += red[1][w][l][e];
+          g += red[rflip][0][w][l][e];
+          v += red[rflip][1][w][l][e];
         }
-        if (c0 + j < cnt) {
-          const int s = slot + c0 + j;
-          a.mid[(int64_t)s * a.i + tile * 16 + n] =
-              (uint16_t)pack2<XDT>(silu(g) * u * r.slot_prob[s], 0.0f);
+        if (cur.c0 + j < cur.cnt) {
+          const int sl = cur.slot + cur.c0;
+          a.mid[(int64_t)sl * a.i +
+                mid_offset<FMT, S>((cur.un % tiles) * 16 + n, j, min(16, cur.cnt - cur.c0))] =
+              (uint16_t)pack2<XDT>(silu(g) * v * r.slot_prob[sl + j], 0.0f);
         }
       }
-      __syncthreads();
+      rflip ^= 1;
     }
+    flip ^= 1;
+    cur = nxt;
   }
 }
 
 // -------------------------------------------------------------------- down
-template <int XDT, int FMT, int S, int NW, int TC>
+// The columns of all chunks (up to 16 tokens of one expert) form one k of
+// chunks * i values; each wave takes a contiguous part of it, in groups of R
+// units.  Its sums over one chunk (a row of the MFMA result per token) go into
+// the wave's own rows of y in LDS when the chunk ends, so no two waves touch
+// the same value and the order is fixed.  R units per wave are in flight, and
+// 16 waves share the CU.
+//
+// INT4 (R = 4): one load of scales and one of zero points serves the group,
+// each lane quarter fetching those of one unit for its row; the lanes pass
+// them on with a permute.
+template <int XDT, int FMT, int S, int NW>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
+  constexpr bool kInt4 = FMT == WQ_FMT_INT4_ASYM;
+  constexpr int R = kInt4 ? 4 : 2;
   extern __shared__ uint4_t dsm[];
-  Active* const act = reinterpret_cast<Active*>(dsm);                    // [kMaxE]
-  float4_t* const red = reinterpret_cast<float4_t*>(act + kMaxE);        // [NW][TC][64]
+  Chunk* const chunk = reinterpret_cast<Chunk*>(dsm);                  // [kMaxChunks]
+  uint8_t* const tok = reinterpret_cast<uint8_t*>(chunk + kMaxChunks); // [kMaxT * kMaxK]
+  float* const ys = reinterpret_cast<float*>(tok + kMaxT * kMaxK);     // [NW][t][16]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
-  const int nact = *a.count;
-  for (int i = tid; i < nact; i += NW * 64) act[i] = a.table[i];
+  const int chunks = *a.count;
+  for (int i = tid; i < chunks; i += NW * 64) chunk[i] = a.table[i];
+  for (int i = tid; i < a.t * a.top_k; i += NW * 64) tok[i] = a.slot_tok[i];
+  for (int i = tid; i < NW * a.t * 16; i += NW * 64) ys[i] = 0.0f;
   __syncthreads();
-  const int ku = a.i >> 7, steps = nact * ku, n0 = (int)blockIdx.x * 16;
-  float4_t acc[TC];
+  const int ku = a.i >> 7, kg = (ku + R - 1) / R, steps = chunks * kg, n0 = (int)blockIdx.x * 16;
+  const int per = (steps + NW - 1) / NW;
+  const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
+  float* const yw = ys + wave * a.t * 16;
+  const uint32_t off = code_off<FMT>(a.i, nl, kq);
+
+  if (s0 < s1) {
+    // a group of units: its chunk, and the first of its units
+    struct Pos {
+      Tile tile;
+      int ci, g, slot, cnt;
+    };
+    auto enter = [&](Pos& p) {
+      const Chunk c = chunk[p.ci];
+      p.slot = __builtin_amdgcn_readfirstlane(c.slot);
+      p.cnt = __builtin_amdgcn_readfirstlane(c.cnt);
+      p.tile = tile_at<FMT, S>(a.down, a.down_s, a.down_z,
+                               (int64_t)__builtin_amdgcn_readfirstlane(c.expert) * a.h + n0, a.i);
+    };
+    auto load = [&](const Pos& p, int j, Unit<FMT> (&w)[1], Acts& x) {
+      const int u = min(p.g * R + j, ku - 1);
+      load_unit<FMT>(w[0], p.tile, off, u);
+      const uint16_t* const m = a.mid + (int64_t)p.slot * a.i + u * 128 * p.cnt;
+      const uint32_t xo = (uint32_t)(min(nl, p.cnt - 1) * 64 + kq * 16);
 #pragma unroll
-  for (int c = 0; c < TC; ++c) acc[c] = float4_t{0, 0, 0, 0};
-  for (int st = wave; st < steps; st += NW) {
-    const int ai = st / ku, u = st - ai * ku;
-    const Active ac = act[ai];
-    const int64_t row = (int64_t)ac.expert * a.h + n0 + nl;
-    const Unit<FMT> w = load_unit<FMT, S>(a.down, a.down_s, a.down_z, row, a.i, u, kq);
+      for (int f = 0; f < 4; ++f) x.f[f] = load_at<uint4_t>(m + f * 32 * p.cnt, xo);
+    };
+    // scales and zero points of unit kq of the group, row nl
+    uint32_t ms[2], mz;
+    auto load_meta = [&](const Pos& p) {
+      const int u = min(p.g * R + kq, ku - 1), g = ku * S;
+      const uint32_t so = (uint32_t)((nl * g + u * S) * 2);
+      const uint32_t zo = (uint32_t)(nl * ((g + 1) >> 1) + ((u * S) >> 1));
+      if constexpr (S == 1) {
+        ms[0] = load_at<uint16_t>(p.tile.scales, so);
+        mz = load_at<uint8_t>(p.tile.zeros, zo);
+      } else if constexpr (S == 2) {
+        ms[0] = load_at<uint32_t>(p.tile.scales, so);
+        mz = load_at<uint8_t>(p.tile.zeros, zo);
+      } else {
+        const uint2_t v = load_at<uint2_t>(p.tile.scales, so);
+        ms[0] = v[0];
+        ms[1] = v[1];
+        mz = load_at<uint16_t>(p.tile.zeros, zo);
+      }
+    };
+    // as one word per group of k
+    auto words = [&](const Pos& p, uint32_t (&m)[S]) {
+      const int u = min(p.g * R + kq, ku - 1);
 #pragma unroll
-    for (int c = 0; c < TC; ++c) {
-      if (((ac.tokens >> (16 * c)) & 0xFFFFu) == 0) continue;
-      const int t = 16 * c + nl;
-      const bool on = (ac.tokens >> t) & 1;
-      const int s = ac.slot + __popcll(ac.tokens & ((1ull << t) - 1));
-      Acts<FMT, S> x;
+      for (int g = 0; g < S; ++g)
+        m[g] = meta_word((ms[g >> 1] >> (16 * (g & 1))) & 0xFFFFu,
+                         (mz >> (4 * (S == 1 ? u & 1 : g))) & 15u);
+    };
+
+    Pos cur{{}, s0 / kg, 0, 0, 0};
+    cur.g = s0 - cur.ci * kg;
+    enter(cur);
+    float4_t acc[1] = {{0, 0, 0, 0}};
+    auto flush = [&](const Pos& p) {
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
-        x.f[f] = on ? *reinterpret_cast<const uint4_t*>(a.mid + (int64_t)s * a.i + u * 128 +
-                                                        unit_k<FMT, S>(f, kq))
-                    : uint4_t{0, 0, 0, 0};
-      prepare_acts<XDT, FMT, S>(x);
-      unit_mac<XDT, FMT, S>(w, x, acc[c]);
+      for (int e = 0; e < 4; ++e) {
+        const int j = 4 * kq + e;
+        if (j < p.cnt) yw[tok[p.slot + j] * 16 + nl] += acc[0][e];
+      }
+      acc[0] = float4_t{0, 0, 0, 0};
+    };
+    Unit<FMT> w[R][1];
+    Acts x[R];
+    if constexpr (kInt4) load_meta(cur);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      load(cur, j, w[j], x[j]);
+      // in this order, as the loop waits for them
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int st = s0; st < s1; ++st) {
+      Pos nxt = cur;
+      if (st + 1 < s1 && ++nxt.g == kg) {
+        nxt.g = 0;
+        ++nxt.ci;
+        enter(nxt);
+      }
+      uint32_t m[S];
+      if constexpr (kInt4) {
+        words(cur, m);
+        load_meta(nxt);
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        uint32_t mj[1][S];
+        if constexpr (kInt4) {
+#pragma unroll
+          for (int g = 0; g < S; ++g)
+            mj[0][g] = (uint32_t)__builtin_amdgcn_ds_bpermute((j * 16 + nl) * 4, (int)m[g]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (cur.g * R + j < ku) unit_mac<XDT, FMT, S, 1>(w[j], mj, x[j], acc);
+        __builtin_amdgcn_sched_barrier(0);
+        load(nxt, j, w[j], x[j]);
+      }
+      if (nxt.ci != cur.ci || st + 1 == s1) flush(cur);
+      cur = nxt;
     }
   }
-#pragma unroll
-  for (int c = 0; c < TC; ++c) red[(wave * TC + c) * 64 + lane] = acc[c];
   __syncthreads();
-  for (int i = tid; i < TC * 256; i += NW * 64) {
-    const int c = i >> 8, j = (i >> 4) & 15, n = i & 15, l = (j >> 2) * 16 + n, e = j & 3;
-    const int t = 16 * c + j;
-    if (t >= a.t) continue;
+  for (int i = tid; i < a.t * 16; i += NW * 64) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[(w * TC + c) * 64 + l][e];
-    const int64_t o = (int64_t)t * a.h + n0 + n;
+    for (int w = 0; w < NW; ++w) v += ys[w * a.t * 16 + i];
+    const int64_t o = (int64_t)(i >> 4) * a.h + n0 + (i & 15);
     if (a.ydt == WQ_F32) static_cast<float*>(a.y)[o] = v;
     else if (a.ydt == WQ_BF16) static_cast<uint16_t*>(a.y)[o] = (uint16_t)pack2<WQ_BF16>(v, 0.0f);
     else static_cast<uint16_t*>(a.y)[o] = (uint16_t)pack2<WQ_F16>(v, 0.0f);
@@ -528,31 +814,47 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
 }
 
 // ------------------------------------------------------------------ launch
-template <int XDT, int FMT, int S, int TC>
-hipError_t down_tc(const MoeArgs& a, hipStream_t s) {
-  constexpr int NW = 8;
-  constexpr int bytes = kMaxE * (int)sizeof(Active) + NW * TC * 1024;
-  moe_down_kernel<XDT, FMT, S, NW, TC><<<dim3((unsigned)(a.h / 16)), NW * 64, bytes, s>>>(a);
+constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK;
+
+template <int XDT, int FMT, int S>
+hipError_t down_launch(const MoeArgs& a, hipStream_t s) {
+  constexpr int NW = 16;
+  constexpr int most = kDownTables + NW * kMaxT * 64;
+  auto* kern = &moe_down_kernel<XDT, FMT, S, NW>;
+  static std::atomic<bool> ready{false};
+  if (!ready.load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != hipSuccess) return e;
+    ready.store(true, std::memory_order_release);
+  }
+  const int bytes = kDownTables + NW * a.t * 64;
+  kern<<<dim3((unsigned)(a.h / 16)), NW * 64, bytes, s>>>(a);
   return hipGetLastError();
 }
 
 template <int XDT, int FMT, int S>
 hipError_t moe_fmt(const MoeArgs& a, hipStream_t s) {
-  constexpr int NW = 8;
   if (a.router != nullptr) {
     const dim3 grid((unsigned)((a.e + 3) / 4), (unsigned)((a.t + kRouterTok - 1) / kRouterTok));
     moe_router_kernel<XDT><<<grid, 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  // 8 waves and two workgroups per CU where they cover k in one pass, else 16
+  // waves and one
   const int64_t units = (int64_t)std::min(a.e, a.t * a.top_k) * (a.i / 16);
-  const unsigned grid = (unsigned)std::min<int64_t>(units, 512);
-  moe_gate_up_kernel<XDT, FMT, S, NW><<<dim3(grid), NW * 64, 0, s>>>(a);
+  if (a.h <= 8 * 256) {
+    const unsigned grid = (unsigned)std::min<int64_t>(units, 512);
+    moe_gate_up_kernel<XDT, FMT, S, 8><<<dim3(grid), 8 * 64, 0, s>>>(a, 1);
+  } else {
+    const unsigned grid = (unsigned)std::min<int64_t>(units, 256);
+    moe_gate_up_kernel<XDT, FMT, S, 16>
+        <<<dim3(grid), 16 * 64, 0, s>>>(a, (a.h + 16 * 256 - 1) / (16 * 256));
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.t <= 16) return down_tc<XDT, FMT, S, 1>(a, s);
-  if (a.t <= 32) return down_tc<XDT, FMT, S, 2>(a, s);
-  return down_tc<XDT, FMT, S, 4>(a, s);
+  return down_launch<XDT, FMT, S>(a, s);
 }
 
 template <int XDT>
@@ -567,9 +869,10 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
 
-// workspace: logits fp32 [t][e] | count | table | intermediate [t * top_k][i]
+// workspace: logits fp32 [t][e] | count | table | token of each row |
+// intermediate [t * top_k][i]
 size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t i) {
-  return up256((size_t)(t * e) * 4) + 256 + up256(kMaxE * sizeof(Active)) +
+  return up256((size_t)(t * e) * 4) + 256 + up256(kMaxChunks * sizeof(Chunk)) + kMaxT * kMaxK +
          up256((size_t)(t * top_k * i) * 2);
 }
 
@@ -585,8 +888,10 @@ hipError_t launch_moe(const MoeCall& c, hipStream_t s) {
   p += up256((size_t)(c.t * c.e) * 4);
   a.count = reinterpret_cast<int32_t*>(p);
   p += 256;
-  a.table = reinterpret_cast<Active*>(p);
-  p += up256(kMaxE * sizeof(Active));
+  a.table = reinterpret_cast<Chunk*>(p);
+  p += up256(kMaxChunks * sizeof(Chunk));
+  a.slot_tok = reinterpret_cast<uint8_t*>(p);
+  p += kMaxT * kMaxK;
   a.mid = reinterpret_cast<uint16_t*>(p);
   a.y = c.y;
   a.ids = c.ids;
