@@ -251,12 +251,16 @@ __device__ void route(const MoeArgs& a, Routing& r) {
 }
 
 // ------------------------------------------------------------ weight units
-// One unit: 16 rows x 128 values of k of one matrix, in the lane layout of
-// the B operand: lane (row nl, quarter kq).
+// One unit: 16 rows x 128 values of k of one matrix.  The B operand wants it
+// in lane (row nl, quarter kq):
 //   INT4 (S groups per unit): 16 bytes = codes [32 kq, 32 kq + 32) of the row.
 //   FP8: bytes [16 kq, +16) and [64 + 16 kq, +16).
-// The codes are kept as loaded: arithmetic on a value right after its load
-// would make the wave wait for it there.
+// It is loaded with a row's four pieces in adjacent lanes (lane 4 nl + kq):
+// a load whose adjacent lanes are on different lines takes 64 cycles to
+// address instead of 16, and that was what bound the kernels.  operand_order()
+// moves the pieces to their lanes when they are used; until then they are kept
+// as loaded, since arithmetic on a value right after its load would make the
+// wave wait for it there.
 template <int FMT>
 struct Unit {
   uint4_t c[FMT == WQ_FMT_FP8_BLOCK ? 2 : 1];
@@ -269,8 +273,16 @@ struct Tile {
   const uint8_t *codes, *scales, *zeros;
 };
 template <int FMT>
-__device__ __forceinline__ uint32_t code_off(int k, int nl, int kq) {
-  return (uint32_t)(nl * (FMT == WQ_FMT_FP8_BLOCK ? k : k >> 1) + kq * 16);
+__device__ __forceinline__ uint32_t code_off(int k, int lane) {
+  return (uint32_t)((lane >> 2) * (FMT == WQ_FMT_FP8_BLOCK ? k : k >> 1) + (lane & 3) * 16);
+}
+// the 16 bytes that lane 4 nl + kq holds, in lane 16 kq + nl
+__device__ __forceinline__ uint4_t operand_order(uint4_t v) {
+  const int lane = (int)__lane_id(), from = ((lane & 15) * 4 + (lane >> 4)) * 4;
+  uint4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+  return r;
 }
 template <int FMT, int S>
 __device__ __forceinline__ Tile tile_at(const void* codes, const void* scales,
@@ -375,9 +387,10 @@ __device__ __forceinline__ uint4_t quarter_transpose(uint4_t v) {
 
 // The intermediate is laid out as the down product reads it: the rows of one
 // chunk (cnt <= 16 tokens of one expert) together, within them [unit of k]
-// [operand f][row][quarter kq][8 values], the 8 values in pair order for INT4.
-// One operand load of a wave is then cnt * 64 contiguous bytes, and needs no
-// reordering.  Element offset of value k of row j from the chunk's begin:
+// [operand f][quarter kq][row][8 values], the 8 values in pair order for INT4.
+// One operand load of a wave is then cnt * 64 contiguous bytes, adjacent lanes
+// 16 bytes apart (with adjacent lanes on different lines a load takes four
+// times as long to address), and needs no reordering.  Element offset of value k of row j from the chunk's begin:
 template <int FMT, int S>
 __device__ __forceinline__ int64_t mid_offset(int k, int j, int cnt) {
   const int q = k & 127, e = k & 7;
@@ -393,7 +406,7 @@ __device__ __forceinline__ int64_t mid_offset(int k, int j, int cnt) {
     kq = (q >> 3) & 3;
   }
   const int at = FMT == WQ_FMT_FP8_BLOCK ? e : (e < 4 ? 2 * e : 2 * e - 7);
-  return ((int64_t)((k >> 7) * 4 + f) * cnt + j) * 32 + kq * 8 + at;
+  return ((int64_t)((k >> 7) * 16 + f * 4 + kq) * cnt + j) * 8 + at;
 }
 
 // The activations of one unit as A operands
@@ -410,11 +423,12 @@ __device__ __forceinline__ void unit_mac(const Unit<FMT> (&w)[N], const uint32_t
   if constexpr (FMT == WQ_FMT_FP8_BLOCK) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      const uint4_t q[2] = {operand_order(w[i].c[0]), operand_order(w[i].c[1])};
       float4_t c = zero;
 #pragma unroll
       for (int f = 0; f < 4; ++f)
-        c = mfma16<XDT>(x.f[f], unpack_fp8<XDT>(w[i].c[f >> 1][2 * (f & 1)],
-                                                w[i].c[f >> 1][2 * (f & 1) + 1]), c);
+        c = mfma16<XDT>(x.f[f], unpack_fp8<XDT>(q[f >> 1][2 * (f & 1)],
+                                                q[f >> 1][2 * (f & 1) + 1]), c);
       const float s = __uint_as_float(w[i].s);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(c[e], s, acc[i][e]);
@@ -424,7 +438,10 @@ __device__ __forceinline__ void unit_mac(const Unit<FMT> (&w)[N], const uint32_t
     const uint4_t ones = {kOne, kOne, kOne, kOne};
     uint4_t q[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = S == 1 ? w[i].c[0] : quarter_transpose(w[i].c[0]);
+    for (int i = 0; i < N; ++i) {
+      q[i] = operand_order(w[i].c[0]);
+      if constexpr (S > 1) q[i] = quarter_transpose(q[i]);
+    }
 #pragma unroll
     for (int g = 0; g < S; ++g) {
       float4_t sum = zero, c[N];
@@ -505,7 +522,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
   const int per = (units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int u0 = (int)blockIdx.x * per, u1 = min(u0 + per, units);
   if (u0 >= u1) return;
-  const uint32_t off = code_off<FMT>(a.h, nl, kq);
+  const uint32_t off = code_off<FMT>(a.h, lane);
 
   // position in the stream: tiles [lo, hi) of one expert for its tokens from
   // c0 on, then for the next 16 of them, then the next expert
@@ -678,8 +695,8 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
 // 16 waves share the CU.
 //
 // INT4 (R = 4): one load of scales and one of zero points serves the group,
-// each lane quarter fetching those of one unit for its row; the lanes pass
-// them on with a permute.
+// four adjacent lanes fetching those of its units for one row; a permute brings
+// them to the lanes of that row.
 template <int XDT, int FMT, int S, int NW>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   constexpr bool kInt4 = FMT == WQ_FMT_INT4_ASYM;
@@ -700,7 +717,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   const int per = (steps + NW - 1) / NW;
   const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
   float* const yw = ys + wave * a.t * 16;
-  const uint32_t off = code_off<FMT>(a.i, nl, kq);
+  const uint32_t off = code_off<FMT>(a.i, lane);
 
   if (s0 < s1) {
     // a group of units: its chunk, and the first of its units
@@ -719,16 +736,16 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
       const int u = min(p.g * R + j, ku - 1);
       load_unit<FMT>(w[0], p.tile, off, u);
       const uint16_t* const m = a.mid + (int64_t)p.slot * a.i + u * 128 * p.cnt;
-      const uint32_t xo = (uint32_t)(min(nl, p.cnt - 1) * 64 + kq * 16);
+      const uint32_t xo = (uint32_t)(kq * p.cnt + min(nl, p.cnt - 1)) * 16;
 #pragma unroll
       for (int f = 0; f < 4; ++f) x.f[f] = load_at<uint4_t>(m + f * 32 * p.cnt, xo);
     };
-    // scales and zero points of unit kq of the group, row nl
+    // scales and zero points of unit lane % 4 of the group, row lane / 4
     uint32_t ms[2], mz;
     auto load_meta = [&](const Pos& p) {
-      const int u = min(p.g * R + kq, ku - 1), g = ku * S;
-      const uint32_t so = (uint32_t)((nl * g + u * S) * 2);
-      const uint32_t zo = (uint32_t)(nl * ((g + 1) >> 1) + ((u * S) >> 1));
+      const int u = min(p.g * R + (lane & 3), ku - 1), g = ku * S;
+      const uint32_t so = (uint32_t)(((lane >> 2) * g + u * S) * 2);
+      const uint32_t zo = (uint32_t)((lane >> 2) * ((g + 1) >> 1) + ((u * S) >> 1));
       if constexpr (S == 1) {
         ms[0] = load_at<uint16_t>(p.tile.scales, so);
         mz = load_at<uint8_t>(p.tile.zeros, zo);
@@ -744,7 +761,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
     };
     // as one word per group of k
     auto words = [&](const Pos& p, uint32_t (&m)[S]) {
-      const int u = min(p.g * R + kq, ku - 1);
+      const int u = min(p.g * R + (lane & 3), ku - 1);
 #pragma unroll
       for (int g = 0; g < S; ++g)
         m[g] = meta_word((ms[g >> 1] >> (16 * (g & 1))) & 0xFFFFu,
@@ -790,7 +807,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
         if constexpr (kInt4) {
 #pragma unroll
           for (int g = 0; g < S; ++g)
-            mj[0][g] = (uint32_t)__builtin_amdgcn_ds_bpermute((j * 16 + nl) * 4, (int)m[g]);
+            mj[0][g] = (uint32_t)__builtin_amdgcn_ds_bpermute((nl * 4 + j) * 4, (int)m[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (cur.g * R + j < ku) unit_mac<XDT, FMT, S, 1>(w[j], mj, x[j], acc);
