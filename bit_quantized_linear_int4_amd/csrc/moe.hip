@@ -130,6 +130,7 @@ struct Routing {
   uint8_t slot_tok[kMaxT * kMaxK];
   int32_t slot_of[kMaxE];
   Active act[kMaxE];
+  uint16_t act_of[kMaxChunks];        // the active expert of a chunk
   int32_t count, chunks;
 };
 
@@ -226,6 +227,7 @@ __device__ void route(const MoeArgs& a, Routing& r) {
       if (m != 0) {
         const int at = na + __popcll(on & ((1ull << lane) - 1));
         r.act[at] = Active{e, slot + (before & 0xFFFF), cnt, chunk + (before >> 16)};
+        for (int c = 0; 16 * c < cnt; ++c) r.act_of[chunk + (before >> 16) + c] = (uint16_t)at;
         r.slot_of[e] = slot + (before & 0xFFFF);
       }
       na += __popcll(on);
@@ -518,44 +520,72 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
       if (a.probs != nullptr) a.probs[i] = r.probs[i];
     }
   }
-  const int tiles = a.i >> 4, units = nact * tiles, ku = a.h >> 7, groups = ku * S;
-  const int per = (units + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int u0 = (int)blockIdx.x * per, u1 = min(u0 + per, units);
-  if (u0 >= u1) return;
+  // Every workgroup takes as many steps: tiles times chunks (16 tokens of an
+  // expert).  The order is expert, block of `per` tiles, chunk, tile, and
+  // neighbours in it run on the same XCD: the chunks of one block are about
+  // one workgroup each, next to each other, so the codes of a block come from
+  // HBM for the first and from that XCD's L2 for the others.
+  const int tiles = a.i >> 4, ku = a.h >> 7, groups = ku * S;
+  const int steps = tiles * __builtin_amdgcn_readfirstlane(r.chunks), G = (int)gridDim.x;
+  const int per = (steps + G - 1) / G;
+  const int xcd = (int)blockIdx.x & 7;
+  const int wg = xcd * (G >> 3) + min(xcd, G & 7) + ((int)blockIdx.x >> 3);
+  const int st0 = wg * per, st1 = min(st0 + per, steps);
+  if (st0 >= st1) return;
   const uint32_t off = code_off<FMT>(a.h, lane);
 
-  // position in the stream: tiles [lo, hi) of one expert for its tokens from
-  // c0 on, then for the next 16 of them, then the next expert
   struct Pos {
     int64_t row;                       // first gate row of the expert
-    int un, lo, hi, c0, pass, slot, cnt;
+    int st;                            // step
+    int ai, cnt, slot;                 // expert, its tokens and their first row
+    int lo, hi, tile, ch;              // block [lo, hi), tile and chunk in it
+    int pass;
     int fresh;                         // other activations than the step before
   };
-  auto enter = [&](Pos& p) {           // the expert of tile p.un
-    const int ai = p.un / tiles;
-    const Active ac = r.act[ai];
-    p.lo = p.un;
-    p.hi = min(u1, (ai + 1) * tiles);
+  auto enter = [&](Pos& p) {           // expert p.ai
+    const Active ac = r.act[p.ai];
     p.slot = __builtin_amdgcn_readfirstlane(ac.slot);
     p.cnt = __builtin_amdgcn_readfirstlane(ac.cnt);
-    p.row = (int64_t)__builtin_amdgcn_readfirstlane(ac.expert) * a.i - (int64_t)ai * a.i;
+    p.row = (int64_t)__builtin_amdgcn_readfirstlane(ac.expert) * a.i;
   };
   auto advance = [&](Pos& p) {
     p.fresh = passes > 1;
     if (++p.pass < passes) return;
     p.pass = 0;
-    if (++p.un < p.hi) return;
-    p.fresh = true;
-    p.c0 += 16;
-    if (p.c0 < p.cnt) {
-      p.un = p.lo;
-      return;
+    if (++p.st >= st1) {               // stays on the last tile
+      --p.tile;
+    } else if (p.tile + 1 == p.hi) {
+      p.fresh = true;
+      if (16 * ++p.ch >= p.cnt) {
+        p.ch = 0;
+        p.lo = p.hi;
+        if (p.lo == tiles) {
+          p.lo = 0;
+          ++p.ai;
+          enter(p);
+        }
+        p.hi = min(p.lo + per, tiles);
+      }
+      p.tile = p.lo - 1;
     }
-    p.c0 = 0;
-    if (p.un < u1) enter(p);
+    ++p.tile;
+  };
+  auto start = [&]() {                 // at step st0
+    Pos p{};
+    p.st = st0;
+    p.ai = __builtin_amdgcn_readfirstlane((int)r.act_of[st0 / tiles]);
+    enter(p);
+    const int nch = (p.cnt + 15) >> 4;
+    const int in = st0 - __builtin_amdgcn_readfirstlane(r.act[p.ai].chunk) * tiles;
+    p.lo = in / (per * nch) * per;
+    p.hi = min(p.lo + per, tiles);
+    p.ch = (in - p.lo * nch) / (p.hi - p.lo);
+    p.tile = p.lo + (in - p.lo * nch) % (p.hi - p.lo);
+    p.fresh = true;
+    return p;
   };
   auto unit_of = [&](const Pos& p) { return (p.pass * NW + wave) * 2; };
-  auto row_of = [&](const Pos& p) { return p.row + (int64_t)min(p.un, u1 - 1) * 16; };
+  auto row_of = [&](const Pos& p) { return p.row + (int64_t)p.tile * 16; };
   // unit u + j of both matrices at position p
   auto load = [&](const Pos& p, int j, Unit<FMT> (&w)[2]) {
     const int u = min(unit_of(p) + j, ku - 1);
@@ -589,8 +619,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
 
   float4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   int flip = 0, rflip = 0;
-  Pos cur{0, u0, 0, 0, 0, 0, 0, 0, 1};
-  enter(cur);
+  Pos cur = start();
   Acts x0, x1;                         // of the wave's two units
   // a unit's registers take the next tile's as soon as it is multiplied
   Unit<FMT> w0[2], w1[2];
@@ -604,12 +633,12 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     lgkm_wait0();
     wg_barrier();
   }
-  while (cur.un < u1) {
+  while (cur.st < st1) {
     const int u = unit_of(cur);
     Pos nxt = cur;
     advance(nxt);
     if (cur.fresh) {
-      const uint32_t tok = r.slot_tok[cur.slot + min(cur.c0 + nl, cur.cnt - 1)];
+      const uint32_t tok = r.slot_tok[cur.slot + min(16 * cur.ch + nl, cur.cnt - 1)];
       const uint32_t xo = tok * (uint32_t)(a.h * 2);
       load_acts<FMT, S>(x0, a.x, xo, min(u, ku - 1), kq);
       load_acts<FMT, S>(x1, a.x, xo, min(u + 1, ku - 1), kq);
@@ -672,10 +701,11 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
           g += red[rflip][0][w][l][e];
           v += red[rflip][1][w][l][e];
         }
-        if (cur.c0 + j < cur.cnt) {
-          const int sl = cur.slot + cur.c0;
+        const int c0 = 16 * cur.ch;
+        if (c0 + j < cur.cnt) {
+          const int sl = cur.slot + c0;
           a.mid[(int64_t)sl * a.i +
-                mid_offset<FMT, S>((cur.un % tiles) * 16 + n, j, min(16, cur.cnt - cur.c0))] =
+                mid_offset<FMT, S>(cur.tile * 16 + n, j, min(16, cur.cnt - c0))] =
               (uint16_t)pack2<XDT>(silu(g) * v * r.slot_prob[sl + j], 0.0f);
         }
       }
