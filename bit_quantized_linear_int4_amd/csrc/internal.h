@@ -201,7 +201,7 @@ struct MoeCall {
   float* probs;
   void* workspace;
 };
-size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t i);
+size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t h, int64_t i);
 hipError_t launch_moe(const MoeCall& c, hipStream_t s);
 
 hipError_t launch_dequantize(const wq_weight* w, const float* levels16, void* out, int odt,

@@ -57,11 +57,18 @@ struct MoeArgs {
   Chunk* table;
   uint8_t* slot_tok;         // [t * top_k] token of a row of the intermediate
   uint16_t* mid;             // [t * top_k][i]
+  float* part;               // [parts][t][h]
   void* y;                   // [t][h]
   int32_t* ids;              // [t][top_k] or nullptr
   float* probs;              // [t][top_k] or nullptr
   int t, e, top_k, h, i, renorm, ydt;
 };
+
+__device__ __forceinline__ void store_as(void* y, int dt, int64_t i, float v) {
+  if (dt == WQ_F32) static_cast<float*>(y)[i] = v;
+  else if (dt == WQ_BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)pack2<WQ_BF16>(v, 0.0f);
+  else static_cast<uint16_t*>(y)[i] = (uint16_t)pack2<WQ_F16>(v, 0.0f);
+}
 
 template <int XDT>
 __device__ __forceinline__ float4_t mfma16(uint4_t a, uint4_t b, float4_t c) {
@@ -717,100 +724,111 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
 }
 
 // -------------------------------------------------------------------- down
-// The columns of all chunks (up to 16 tokens of one expert) form one k of
-// chunks * i values; each wave takes a contiguous part of it, in groups of R
-// units.  Its sums over one chunk (a row of the MFMA result per token) go into
-// the wave's own rows of y in LDS when the chunk ends, so no two waves touch
-// the same value and the order is fixed.  R units per wave are in flight, and
-// 16 waves share the CU.
+// A workgroup owns RT tiles of 16 rows of y.  The columns of all chunks (up to
+// 16 tokens of one expert) form one k of chunks * i values, in groups of R
+// units; its gridDim.y parts go to as many workgroups, and of a part each wave
+// takes a contiguous piece.  A wave's sums over one chunk (a row of the MFMA
+// result per token) go into the wave's own rows of y in LDS when the chunk
+// ends, so no two waves touch the same value and the order is fixed.  R units
+// per wave are in flight, and 16 waves share the CU.
 //
-// INT4 (R = 4): one load of scales and one of zero points serves the group,
-// four adjacent lanes fetching those of its units for one row; a permute brings
+// INT4: one load of scales and one of zero points serves the R x RT units of a
+// group (four), R adjacent lanes fetching those of one row; a permute brings
 // them to the lanes of that row.
-template <int XDT, int FMT, int S, int NW>
+template <int XDT, int FMT, int S, int NW, int RT>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   constexpr bool kInt4 = FMT == WQ_FMT_INT4_ASYM;
-  constexpr int R = kInt4 ? 4 : 2;
+  constexpr int R = (kInt4 ? 4 : 2) / RT;
   extern __shared__ uint4_t dsm[];
   Chunk* const chunk = reinterpret_cast<Chunk*>(dsm);                  // [kMaxChunks]
   uint8_t* const tok = reinterpret_cast<uint8_t*>(chunk + kMaxChunks); // [kMaxT * kMaxK]
-  float* const ys = reinterpret_cast<float*>(tok + kMaxT * kMaxK);     // [NW][t][16]
+  float* const ys = reinterpret_cast<float*>(tok + kMaxT * kMaxK);     // [NW][t][16 RT]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int chunks = *a.count;
   for (int i = tid; i < chunks; i += NW * 64) chunk[i] = a.table[i];
   for (int i = tid; i < a.t * a.top_k; i += NW * 64) tok[i] = a.slot_tok[i];
-  for (int i = tid; i < NW * a.t * 16; i += NW * 64) ys[i] = 0.0f;
+  for (int i = tid; i < NW * a.t * 16 * RT; i += NW * 64) ys[i] = 0.0f;
   __syncthreads();
-  const int ku = a.i >> 7, kg = (ku + R - 1) / R, steps = chunks * kg, n0 = (int)blockIdx.x * 16;
-  const int per = (steps + NW - 1) / NW;
-  const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
-  float* const yw = ys + wave * a.t * 16;
+  const int ku = a.i >> 7, kg = (ku + R - 1) / R, n0 = (int)blockIdx.x * 16 * RT;
+  const int steps = chunks * kg, pieces = (int)gridDim.y * NW;
+  const int per = (steps + pieces - 1) / pieces;
+  const int s0 = min(((int)blockIdx.y * NW + wave) * per, steps), s1 = min(s0 + per, steps);
+  float* const yw = ys + wave * a.t * 16 * RT;
   const uint32_t off = code_off<FMT>(a.i, lane);
 
   if (s0 < s1) {
     // a group of units: its chunk, and the first of its units
     struct Pos {
-      Tile tile;
+      int64_t row;
       int ci, g, slot, cnt;
     };
     auto enter = [&](Pos& p) {
       const Chunk c = chunk[p.ci];
       p.slot = __builtin_amdgcn_readfirstlane(c.slot);
       p.cnt = __builtin_amdgcn_readfirstlane(c.cnt);
-      p.tile = tile_at<FMT, S>(a.down, a.down_s, a.down_z,
-                               (int64_t)__builtin_amdgcn_readfirstlane(c.expert) * a.h + n0, a.i);
+      p.row = (int64_t)__builtin_amdgcn_readfirstlane(c.expert) * a.h + n0;
     };
-    auto load = [&](const Pos& p, int j, Unit<FMT> (&w)[1], Acts& x) {
+    auto tile_of = [&](const Pos& p, int r) {
+      return tile_at<FMT, S>(a.down, a.down_s, a.down_z, p.row + 16 * r, a.i);
+    };
+    auto load = [&](const Pos& p, int j, Unit<FMT> (&w)[RT], Acts& x) {
       const int u = min(p.g * R + j, ku - 1);
-      load_unit<FMT>(w[0], p.tile, off, u);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) load_unit<FMT>(w[r], tile_of(p, r), off, u);
       const uint16_t* const m = a.mid + (int64_t)p.slot * a.i + u * 128 * p.cnt;
       const uint32_t xo = (uint32_t)(kq * p.cnt + min(nl, p.cnt - 1)) * 16;
 #pragma unroll
       for (int f = 0; f < 4; ++f) x.f[f] = load_at<uint4_t>(m + f * 32 * p.cnt, xo);
     };
-    // scales and zero points of unit lane % 4 of the group, row lane / 4
+    // scales and zero points of unit lane % R of the group, row lane / R
     uint32_t ms[2], mz;
     auto load_meta = [&](const Pos& p) {
-      const int u = min(p.g * R + (lane & 3), ku - 1), g = ku * S;
-      const uint32_t so = (uint32_t)(((lane >> 2) * g + u * S) * 2);
-      const uint32_t zo = (uint32_t)((lane >> 2) * ((g + 1) >> 1) + ((u * S) >> 1));
+      const int u = min(p.g * R + (lane & (R - 1)), ku - 1), g = ku * S, rw = lane / R;
+      const uint32_t so = (uint32_t)((rw * g + u * S) * 2);
+      const uint32_t zo = (uint32_t)(rw * ((g + 1) >> 1) + ((u * S) >> 1));
+      const Tile t = tile_of(p, 0);
       if constexpr (S == 1) {
-        ms[0] = load_at<uint16_t>(p.tile.scales, so);
-        mz = load_at<uint8_t>(p.tile.zeros, zo);
+        ms[0] = load_at<uint16_t>(t.scales, so);
+        mz = load_at<uint8_t>(t.zeros, zo);
       } else if constexpr (S == 2) {
-        ms[0] = load_at<uint32_t>(p.tile.scales, so);
-        mz = load_at<uint8_t>(p.tile.zeros, zo);
+        ms[0] = load_at<uint32_t>(t.scales, so);
+        mz = load_at<uint8_t>(t.zeros, zo);
       } else {
-        const uint2_t v = load_at<uint2_t>(p.tile.scales, so);
+        const uint2_t v = load_at<uint2_t>(t.scales, so);
         ms[0] = v[0];
         ms[1] = v[1];
-        mz = load_at<uint16_t>(p.tile.zeros, zo);
+        mz = load_at<uint16_t>(t.zeros, zo);
       }
     };
     // as one word per group of k
     auto words = [&](const Pos& p, uint32_t (&m)[S]) {
-      const int u = min(p.g * R + (lane & 3), ku - 1);
+      const int u = min(p.g * R + (lane & (R - 1)), ku - 1);
 #pragma unroll
       for (int g = 0; g < S; ++g)
         m[g] = meta_word((ms[g >> 1] >> (16 * (g & 1))) & 0xFFFFu,
                          (mz >> (4 * (S == 1 ? u & 1 : g))) & 15u);
     };
 
-    Pos cur{{}, s0 / kg, 0, 0, 0};
+    Pos cur{0, s0 / kg, 0, 0, 0};
     cur.g = s0 - cur.ci * kg;
     enter(cur);
-    float4_t acc[1] = {{0, 0, 0, 0}};
+    float4_t acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = float4_t{0, 0, 0, 0};
     auto flush = [&](const Pos& p) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = 4 * kq + e;
-        if (j < p.cnt) yw[tok[p.slot + j] * 16 + nl] += acc[0][e];
+      for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 4 * kq + e;
+          if (j < p.cnt) yw[(tok[p.slot + j] * RT + r) * 16 + nl] += acc[r][e];
+        }
+        acc[r] = float4_t{0, 0, 0, 0};
       }
-      acc[0] = float4_t{0, 0, 0, 0};
     };
-    Unit<FMT> w[R][1];
+    Unit<FMT> w[R][RT];
     Acts x[R];
     if constexpr (kInt4) load_meta(cur);
 #pragma unroll
@@ -833,14 +851,17 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        uint32_t mj[1][S];
+        uint32_t mj[RT][S];
         if constexpr (kInt4) {
 #pragma unroll
-          for (int g = 0; g < S; ++g)
-            mj[0][g] = (uint32_t)__builtin_amdgcn_ds_bpermute((nl * 4 + j) * 4, (int)m[g]);
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int g = 0; g < S; ++g)
+              mj[r][g] = (uint32_t)__builtin_amdgcn_ds_bpermute(((16 * r + nl) * R + j) * 4,
+                                                                (int)m[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (cur.g * R + j < ku) unit_mac<XDT, FMT, S, 1>(w[j], mj, x[j], acc);
+        if (cur.g * R + j < ku) unit_mac<XDT, FMT, S, RT>(w[j], mj, x[j], acc);
         __builtin_amdgcn_sched_barrier(0);
         load(nxt, j, w[j], x[j]);
       }
@@ -849,25 +870,48 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < a.t * 16; i += NW * 64) {
+  constexpr int BR = 16 * RT;
+  for (int i = tid; i < a.t * BR; i += NW * 64) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += ys[w * a.t * 16 + i];
-    const int64_t o = (int64_t)(i >> 4) * a.h + n0 + (i & 15);
-    if (a.ydt == WQ_F32) static_cast<float*>(a.y)[o] = v;
-    else if (a.ydt == WQ_BF16) static_cast<uint16_t*>(a.y)[o] = (uint16_t)pack2<WQ_BF16>(v, 0.0f);
-    else static_cast<uint16_t*>(a.y)[o] = (uint16_t)pack2<WQ_F16>(v, 0.0f);
+    for (int w = 0; w < NW; ++w) v += ys[w * a.t * BR + i];
+    const int64_t o = (int64_t)(i / BR) * a.h + n0 + i % BR;
+    if (gridDim.y > 1) a.part[(int64_t)blockIdx.y * a.t * a.h + o] = v;
+    else store_as(a.y, a.ydt, o, v);
   }
+}
+
+// y = the sum of the parts, in their order
+__global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__ part, int parts,
+                                                       int count, void* y, int ydt) {
+  const int i = (int)blockIdx.x * 256 + (int)threadIdx.x;
+  if (i >= count) return;
+  float v = part[i];
+  for (int p = 1; p < parts; ++p) v += part[(int64_t)p * count + i];
+  store_as(y, ydt, i, v);
 }
 
 // ------------------------------------------------------------------ launch
 constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK;
 
-template <int XDT, int FMT, int S>
-hipError_t down_launch(const MoeArgs& a, hipStream_t s) {
+// Parts of k in the down product with two row tiles per workgroup, as many as
+// fill the 256 CUs once, or 0: one row tile, all of k, no join.  Two tiles read
+// the intermediate once for both, which the L2 carries at several times the
+// codes' size: 64 tokens, 2 of 8 experts of 4096 x 14336 INT4 take 249 us (two
+// tiles, 2 parts), 262 (one tile), 322 (two tiles, one part); 24 tokens, 6 of
+// 64 FP8 experts of 2048 x 1024 94 us (two tiles, 4 parts) against 108.  For a
+// few choices the join costs more than that gives: one token, 8 of 64 INT4
+// experts, 24.6 us with one tile, 25.4 with two in 4 parts; 4 tokens 46.7
+// against 41.4.
+int down_parts(int64_t t, int64_t top_k, int64_t h) {
+  return t * top_k <= 8 ? 0 : (int)std::max<int64_t>(1, 256 * 32 / h);
+}
+
+template <int XDT, int FMT, int S, int RT>
+hipError_t down_launch(const MoeArgs& a, int parts, hipStream_t s) {
   constexpr int NW = 16;
-  constexpr int most = kDownTables + NW * kMaxT * 64;
-  auto* kern = &moe_down_kernel<XDT, FMT, S, NW>;
+  constexpr int most = kDownTables + NW * kMaxT * 64 * RT;
+  auto* kern = &moe_down_kernel<XDT, FMT, S, NW, RT>;
   static std::atomic<bool> ready{false};
   if (!ready.load(std::memory_order_acquire)) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -875,8 +919,13 @@ hipError_t down_launch(const MoeArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     ready.store(true, std::memory_order_release);
   }
-  const int bytes = kDownTables + NW * a.t * 64;
-  kern<<<dim3((unsigned)(a.h / 16)), NW * 64, bytes, s>>>(a);
+  const int bytes = kDownTables + NW * a.t * 64 * RT;
+  kern<<<dim3((unsigned)(a.h / (16 * RT)), (unsigned)parts), NW * 64, bytes, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  const int count = a.t * a.h;
+  moe_join_kernel<<<dim3((unsigned)((count + 255) / 256)), 256, 0, s>>>(a.part, parts, count, a.y,
+                                                                       a.ydt);
   return hipGetLastError();
 }
 
@@ -901,7 +950,9 @@ hipError_t moe_fmt(const MoeArgs& a, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return down_launch<XDT, FMT, S>(a, s);
+  const int parts = down_parts(a.t, a.top_k, a.h);
+  if (parts == 0) return down_launch<XDT, FMT, S, 1>(a, 1, s);
+  return down_launch<XDT, FMT, S, 2>(a, parts, s);
 }
 
 template <int XDT>
@@ -917,10 +968,10 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 }  // namespace
 
 // workspace: logits fp32 [t][e] | count | table | token of each row |
-// intermediate [t * top_k][i]
-size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t i) {
+// intermediate [t * top_k][i] | parts of y fp32 [parts][t][h]
+size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t h, int64_t i) {
   return up256((size_t)(t * e) * 4) + 256 + up256(kMaxChunks * sizeof(Chunk)) + kMaxT * kMaxK +
-         up256((size_t)(t * top_k * i) * 2);
+         up256((size_t)(t * top_k * i) * 2) + (size_t)down_parts(t, top_k, h) * t * h * 4;
 }
 
 hipError_t launch_moe(const MoeCall& c, hipStream_t s) {
@@ -940,6 +991,8 @@ hipError_t launch_moe(const MoeCall& c, hipStream_t s) {
   a.slot_tok = reinterpret_cast<uint8_t*>(p);
   p += kMaxT * kMaxK;
   a.mid = reinterpret_cast<uint16_t*>(p);
+  p += up256((size_t)(c.t * c.top_k * c.i) * 2);
+  a.part = reinterpret_cast<float*>(p);
   a.y = c.y;
   a.ids = c.ids;
   a.probs = c.probs;

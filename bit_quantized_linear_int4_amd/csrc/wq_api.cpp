@@ -479,7 +479,7 @@ size_t wq_moe_workspace(int64_t m, int32_t top_k, const wq_weight* gate, int64_t
     return 0;
   if (check_weight(gate, gate->fmt != WQ_FMT_FP8_BLOCK) != WQ_OK || gate->n % experts != 0)
     return 0;
-  return moe_ws_bytes(m, experts, top_k, gate->n / experts);
+  return moe_ws_bytes(m, experts, top_k, gate->k, gate->n / experts);
 }
 
 wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, const float* logits,
@@ -509,7 +509,7 @@ wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, cons
   if (!aligned(x, 16) || !aligned(router, 16) || !aligned(logits, 4) ||
       !aligned(y, dt_bytes(ydt)) || !aligned(ids, 4) || !aligned(probs, 4))
     return WQ_ERR_ALIGN;
-  if (workspace == nullptr || ws_bytes < moe_ws_bytes(m, experts, top_k, i))
+  if (workspace == nullptr || ws_bytes < moe_ws_bytes(m, experts, top_k, h, i))
     return WQ_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
   const MoeCall c{static_cast<const uint16_t*>(x), xdt, m, h, experts, i, top_k,
