@@ -25,7 +25,7 @@
 // is free as long as both operands agree: lane group g = lane / 16 takes the
 // 16-byte chunks g and g + 4.
 //
-//  * decode (m <= 16): HBM-bound.  A workgroup owns 16 features over all of k;
+//  * decode (m <= 64): HBM-bound.  A workgroup owns 16 features over all of k;
 //    its waves take the blocks of k in turn and add their totals in LDS in a
 //    fixed order.
 //  * gemm: MFMA-bound.  Tiles of BN features x BM tokens, both operands staged
@@ -130,56 +130,135 @@ __device__ __forceinline__ void store4(void* y, int64_t i, float4_t v, bool wide
 }
 
 // ------------------------------------------------------------------ decode
-template <int YDT, int NW>
+// s_waitcnt for all but the loads of the n newest blocks, `per` loads each
+template <int PER, int MAX>
+__device__ __forceinline__ void wait_blocks(int n) {
+  if constexpr (MAX == 0) {
+    vm_wait<0>();
+  } else {
+    if (n >= MAX) vm_wait<MAX * PER>();
+    else wait_blocks<PER, MAX - 1>(n);
+  }
+}
+
+// Up to 64 tokens.  A workgroup owns 16 features over all of k, a wave every
+// NW-th block of it.  Weights, activations (MT tiles of 16 tokens) and their
+// scales reach a ring of R blocks per wave in LDS by direct loads, so R blocks
+// per wave are in flight and a load's adjacent lanes take adjacent bytes, eight
+// lanes to a 128-byte row (loaded as the matrix instruction wants them,
+// adjacent lanes on different rows, each load takes four times as long to
+// address: 12.9 against 10.0 us for 16 x 4096 x 11008, 5.7 against 4.7 for one
+// token and 4096 x 4096).  MT = 0: a single token, whose 128 bytes come in one
+// 4-byte load per lane and whose scale is a scalar load.
+template <int MT>
+constexpr int decode_slot_bytes() {
+  return 16 * kF8Block + (MT == 0 ? 256 : MT * 16 * kF8Block + 256);
+}
+
+template <int YDT, int NW, int R, int MT>
 __global__ __launch_bounds__(NW * 64) void fp8_decode_kernel(Fp8Args a) {
-  constexpr int D = 4;                       // blocks of k in flight per wave
-  __shared__ float4_t red[NW][64];
+  constexpr bool ONE = MT == 0;
+  constexpr int T = ONE ? 1 : MT, TB = 16 * kF8Block;      // token tiles, bytes of a tile
+  constexpr int SLOT = decode_slot_bytes<MT>(), LPB = ONE ? 3 : 2 * MT + 3, SO = TB * (1 + T);
+  extern __shared__ uint4_t dsm[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int nl = lane & 15, kq = lane >> 4;
   const int n0 = (int)blockIdx.x * 16;
-  const uint8_t* const wrow = a.w + (int64_t)min(n0 + nl, a.n - 1) * a.k;
-  const int tok = min(nl, a.m - 1);
-  const uint8_t* const xrow = a.x + (int64_t)tok * a.k;
-  const float* const swr = a.sw + (int64_t)(n0 / kF8Block) * a.kb;
-  float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b0 = wave; b0 < a.kb; b0 += NW * D) {
-    uint4_t wv[D][2], xv[D][2];
-    float s[D];
+  char* const ring = reinterpret_cast<char*>(dsm) + wave * R * SLOT;
+  using cfloat = const __attribute__((address_space(4))) float;
+  cfloat* const swr = (cfloat*)(a.sw + (int64_t)(n0 / kF8Block) * a.kb);
+  const int nb = a.kb > wave ? (a.kb - wave + NW - 1) / NW : 0;    // blocks of this wave
+
+  // chunk (l & 7) ^ (row & 7) of row l / 8 goes to slot l & 7 of that row
+  const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
+  const uint8_t* const w0 = a.w + (int64_t)min(n0 + lr, a.n - 1) * a.k;
+  const uint8_t* const w1 = a.w + (int64_t)min(n0 + 8 + lr, a.n - 1) * a.k;
+  auto issue = [&](int i) {
+    const int b = wave + i * NW, c = b * kF8Block + lc;
+    char* const l = ring + (i % R) * SLOT;
+    const bool in = c < a.k;                 // chunks past k are zeros
+    lds_dma16(in ? w0 + c : (const void*)&kZero16, (lds_void_t*)l);
+    lds_dma16(in ? w1 + c : (const void*)&kZero16, (lds_void_t*)(l + 1024));
+    if constexpr (ONE) {
+      const int d = b * kF8Block + (lane & 31) * 4;
+      lds_dma4(d < a.k ? a.x + d : (const void*)&kZero16, (lds_void_t*)(l + TB));
+    } else {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int b = b0 + d * NW;
-      if (b >= a.kb) break;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = b * kF8Block + kq * 16 + j * 64;
-        const bool in = c < a.k;             // k is a multiple of 16
-        wv[d][j] = in ? *reinterpret_cast<const uint4_t*>(wrow + c) : uint4_t{0, 0, 0, 0};
-        xv[d][j] = in ? *reinterpret_cast<const uint4_t*>(xrow + c) : uint4_t{0, 0, 0, 0};
+      for (int t = 0; t < 2 * MT; ++t) {
+        const uint8_t* const xr = a.x + (int64_t)min(8 * t + lr, a.m - 1) * a.k;
+        lds_dma16(in ? xr + c : (const void*)&kZero16, (lds_void_t*)(l + TB + t * 1024));
       }
-      s[d] = a.sx[(int64_t)b * a.m + tok] * swr[b];
+      lds_dma4(a.sx + (int64_t)b * a.m + min(lane, a.m - 1), (lds_void_t*)(l + SO));
     }
+  };
+  for (int i = 0; i < min(R, nb); ++i) issue(i);
+  const int s0 = nl * kF8Block + (kq ^ (nl & 7)) * 16, s1 = nl * kF8Block + ((kq + 4) ^ (nl & 7)) * 16;
+  float4_t acc[T];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (b0 + d * NW >= a.kb) break;
-      Operand<YDT == WQ_F32> wa, xb;
-      wa.set(wv[d][0], wv[d][1]);
-      xb.set(xv[d][0], xv[d][1]);
+  for (int t = 0; t < T; ++t) acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < nb; ++i) {
+    const char* const l = ring + (i % R) * SLOT;
+    const int b = wave + i * NW;
+    float s = swr[b];
+    if constexpr (ONE) s *= ((cfloat*)a.sx)[b];
+    wait_blocks<LPB, R - 1>(nb - 1 - i);
+    asm volatile("" ::: "memory");
+    Operand<YDT == WQ_F32> wa;
+    wa.set(*reinterpret_cast<const uint4_t*>(l + s0), *reinterpret_cast<const uint4_t*>(l + s1));
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const char* const xl = l + TB * (1 + t);
+      Operand<YDT == WQ_F32> xb;
+      float st = s;
+      if constexpr (ONE) {
+        xb.set(*reinterpret_cast<const uint4_t*>(xl + kq * 16),
+               *reinterpret_cast<const uint4_t*>(xl + 64 + kq * 16));
+      } else {
+        xb.set(*reinterpret_cast<const uint4_t*>(xl + s0),
+               *reinterpret_cast<const uint4_t*>(xl + s1));
+        st *= *reinterpret_cast<const float*>(l + SO + (t * 16 + nl) * 4);
+      }
       const float4_t c = block_sum(wa, xb);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s[d], acc[e]);
+      for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(c[e], st, acc[t][e]);
+    }
+    // the operands are in registers: the slot is free
+    if (i + R < nb) {
+      lgkm_wait0();
+      issue(i + R);
     }
   }
-  red[wave][lane] = acc;
+  // the waves' totals, over the rings
   __syncthreads();
-  if (wave == 0) {
-    float4_t t = red[0][lane];
+  float4_t* const red = reinterpret_cast<float4_t*>(dsm);
 #pragma unroll
-    for (int w = 1; w < NW; ++w) t += red[w][lane];
-    const int n = n0 + kq * 4;
-    if (nl < a.m && n < a.n)
-      store4<YDT>(a.y, (int64_t)nl * a.n + n, t, (a.n & 3) == 0, a.n - n);
+  for (int t = 0; t < T; ++t) red[(wave * T + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  if (wave < T) {
+    float4_t v = red[wave * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[(w * T + wave) * 64 + lane];
+    const int n = n0 + kq * 4, m = wave * 16 + nl;
+    if (m < a.m && n < a.n)
+      store4<YDT>(a.y, (int64_t)m * a.n + n, v, (a.n & 3) == 0, a.n - n);
   }
+}
+
+template <int YDT, int NW, int R, int MT>
+hipError_t decode_launch(const Fp8Args& a, hipStream_t s) {
+  constexpr int bytes = NW * R * decode_slot_bytes<MT>();
+  static_assert(bytes >= NW * (MT == 0 ? 1 : MT) * 1024 && NW >= MT, "room for the totals");
+  auto* kern = &fp8_decode_kernel<YDT, NW, R, MT>;
+  static std::atomic<bool> ready{false};
+  if (!ready.load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    ready.store(true, std::memory_order_release);
+  }
+  kern<<<dim3((unsigned)((a.n + 15) / 16)), NW * 64, bytes, s>>>(a);
+  return hipGetLastError();
 }
 
 // -------------------------------------------------------------------- gemm
@@ -377,8 +456,19 @@ hipError_t gemm_launch(const Fp8Args& a, hipStream_t s) {
 template <int YDT>
 hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
   if (p.tile == 0) {
-    fp8_decode_kernel<YDT, 8><<<dim3((unsigned)((a.n + 15) / 16)), 512, 0, s>>>(a);
-    return hipGetLastError();
+    // 16 features per workgroup.  Up to 256 of them (n <= 4096) a CU holds one,
+    // which then needs all the waves it can have; with more, smaller
+    // workgroups leave room for several: one token 4096 x 4096 4.7 us with 16
+    // waves, 5.1 with 8 (14336 rows: 10.5 and 10.3); 8 tokens 5.0 and 5.8; 16
+    // tokens 11008 x 4096 11.8 and 10.2; 64 tokens 4096 x 4096 8.4 with 8
+    // waves, 10.6 with 4, 11008 x 4096 17.9 and 16.6.  32 tokens 4096 x 4096
+    // 6.6 us, 11.8 as split tiles.
+    const bool few = a.n <= 4096;
+    if (a.m == 1) return decode_launch<YDT, 16, 2, 0>(a, s);
+    if (a.m <= 16)
+      return few ? decode_launch<YDT, 16, 2, 1>(a, s) : decode_launch<YDT, 8, 2, 1>(a, s);
+    if (a.m <= 32) return decode_launch<YDT, 8, 1, 2>(a, s);
+    return few ? decode_launch<YDT, 8, 1, 4>(a, s) : decode_launch<YDT, 4, 2, 4>(a, s);
   }
   // the exact products need twice the operand registers: smaller wave tiles
   constexpr int TM2 = YDT == WQ_F32 ? 4 : 8;
@@ -397,7 +487,7 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k) {
   Fp8Plan p{};
   p.splits = 1;
   const int64_t kb = (k + kF8Block - 1) / kF8Block;
-  if (m <= 16) {
+  if (m <= 64) {
     p.tile = 0;
     return p;
   }

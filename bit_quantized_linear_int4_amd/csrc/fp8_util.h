@@ -91,6 +91,19 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t off) {
   return *(const __attribute__((address_space(1))) T*)((G)b + off);
 }
 
+// MFMA operands want lane 16 kq + nl to hold piece kq of row nl, but a load
+// whose adjacent lanes are on different lines takes 64 cycles to address
+// instead of 16 (a 16-byte load, four adjacent lanes on 64 contiguous bytes).
+// So rows are loaded with a row's four pieces in adjacent lanes, 4 nl + kq, and
+// this moves them: what lane 4 nl + kq holds, to lane 16 kq + nl.
+__device__ __forceinline__ uint4_t operand_order(uint4_t v) {
+  const int lane = (int)__lane_id(), from = ((lane & 15) * 4 + (lane >> 4)) * 4;
+  uint4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+  return r;
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);

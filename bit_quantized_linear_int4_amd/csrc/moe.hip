@@ -80,14 +80,6 @@ __device__ __forceinline__ float4_t mfma16(uint4_t a, uint4_t b, float4_t c) {
                                                   __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
 }
 
-// the 16 bytes that lane 4 nl + kq holds, in lane 16 kq + nl
-__device__ __forceinline__ uint4_t operand_order(uint4_t v) {
-  const int lane = (int)__lane_id(), from = ((lane & 15) * 4 + (lane >> 4)) * 4;
-  uint4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
-  return r;
-}
 // ------------------------------------------------------------------ router
 // logits of 16 experts x 16 tokens per workgroup, k split over 16 waves (exact
 // products, fp32 sums).  Bound by latency: every load of a wave is issued
@@ -290,12 +282,10 @@ __device__ void route(const MoeArgs& a, Routing& r) {
 // in lane (row nl, quarter kq):
 //   INT4 (S groups per unit): 16 bytes = codes [32 kq, 32 kq + 32) of the row.
 //   FP8: bytes [16 kq, +16) and [64 + 16 kq, +16).
-// It is loaded with a row's four pieces in adjacent lanes (lane 4 nl + kq):
-// a load whose adjacent lanes are on different lines takes 64 cycles to
-// address instead of 16, and that was what bound the kernels.  operand_order()
-// moves the pieces to their lanes when they are used; until then they are kept
-// as loaded, since arithmetic on a value right after its load would make the
-// wave wait for it there.
+// It is loaded with a row's four pieces in adjacent lanes (lane 4 nl + kq), and
+// operand_order() moves the pieces to their lanes when they are used; until
+// then they are kept as loaded, since arithmetic on a value right after its
+// load would make the wave wait for it there.
 template <int FMT>
 struct Unit {
   uint4_t c[FMT == WQ_FMT_FP8_BLOCK ? 2 : 1];

@@ -88,9 +88,9 @@ def test_linear_fp8_errors():
     assert call(**w(codes=P + 8)) == ALIGN and call(**w(scales=ODD)) == ALIGN
     # a split product needs its workspace
     big = desc(n=512, k=8192)
-    need = wq._load().wq_linear_fp8_workspace(64, ctypes.byref(big))
+    need = wq._load().wq_linear_fp8_workspace(100, ctypes.byref(big))
     assert 0 < need <= 64 << 20
-    split = dict(m=64, w=ctypes.byref(big))
+    split = dict(m=100, w=ctypes.byref(big))
     assert call(**split) == WS and call(**split, ws=P, ws_bytes=need - 1) == WS
     assert call(**split, ws=P + 128, ws_bytes=need) == ALIGN
     assert wq._load().wq_linear_fp8_workspace(0, ctypes.byref(big)) == 0

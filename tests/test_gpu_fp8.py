@@ -290,7 +290,7 @@ def test_streams_and_graph():
     """The norm, packer and products on a stream of their own and replayed from
     a graph, with other work between the replays."""
     say("fp8: stream and graph replay")
-    m, n, k = 40, 512, 4096
+    m, n, k = 100, 512, 4096
     st = torch.cuda.Stream()
     with torch.cuda.stream(st):
         x, r = rand((m, k), 41, "bf16").cuda(), rand((m, k), 42, "bf16").cuda()
