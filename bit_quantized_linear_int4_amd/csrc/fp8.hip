@@ -34,6 +34,7 @@
 //    k is split over workgroups whose fp32 totals a second kernel adds.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "fp8_util.h"
 
@@ -48,6 +49,7 @@ struct Fp8Args {
   void* y;                   // [m][n]
   float* part;               // split totals [splits][m][n], or nullptr
   int m, n, k, kb, splits;
+  int ld;                    // features of y
 };
 
 __device__ const uint4_t kZero16 = {0, 0, 0, 0};   // what chunks past k read
@@ -262,10 +264,10 @@ hipError_t decode_launch(const Fp8Args& a, hipStream_t s) {
 }
 
 // -------------------------------------------------------------------- gemm
-// direct global -> LDS load with a uniform base and a 32-bit lane offset
-__device__ __forceinline__ void lds_dma16_s(const void* base, uint32_t off, lds_void_t* lds) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(l)
+// direct global -> LDS load with a uniform base, a 32-bit lane offset and a
+// uniform address in LDS
+__device__ __forceinline__ void lds_dma16_s(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds)
                : "memory");
 }
 
@@ -286,17 +288,22 @@ constexpr int fp8_buf_bytes() {
   return (WN * TN + WM * TM) * 16 * kF8Block + WM * TM * 16 * 4;
 }
 
-// WN x WM waves, each TN x TM tiles of 16 features x 16 tokens
+// WN x WM waves, each TN x TM tiles of 16 features x 16 tokens.
 template <int YDT, int WN, int WM, int TN, int TM>
-__global__ __launch_bounds__(WN * WM * 64) void fp8_gemm_kernel(Fp8Args a, int tm, int tn) {
-  constexpr int NW = WN * WM;
+__global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int tn) {
+  constexpr bool EXACT = YDT == WQ_F32;
+  constexpr int NW = WN * WM, T = TN * TM;
   constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
   constexpr int BUF = fp8_buf_bytes<WN, WM, TN, TM>();
-  constexpr int WI = BN / 8 / NW, XI = BM / 8 / NW;      // direct loads per wave
-  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0, "whole loads");
+  constexpr int WI = BN / 8 / NW, XI = BM / 8 / NW;      // direct loads per wave and block,
+  constexpr int SL = BM / NW;                            // and tokens whose scales it brings
+  constexpr int L = 1 + WI + XI;
+  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && SL <= 64, "whole loads");
   static_assert(kF8Block % (TN * 16) == 0, "a wave's features share a scale block");
+  static_assert(TN == 4 && WI <= TN && TM % 2 == 0, "the loads fit between the products");
   extern __shared__ uint4_t dsm[];
   char* const lds = reinterpret_cast<char*>(dsm);
+  const uint32_t l0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
@@ -318,38 +325,28 @@ __global__ __launch_bounds__(WN * WM * 64) void fp8_gemm_kernel(Fp8Args a, int t
   uint32_t woff[WI], xoff[XI];
 #pragma unroll
   for (int i = 0; i < WI; ++i)
-    woff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.n - 1 - n0) * (uint32_t)a.k + lc;
+    woff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.n - 1 - n0) * (uint32_t)a.k;
 #pragma unroll
   for (int i = 0; i < XI; ++i)
-    xoff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.m - 1 - m0) * (uint32_t)a.k + lc;
-
-  auto issue = [&](int b, int buf) {
-    char* const wl = lds + buf * BUF;
-    char* const xl = wl + BN * kF8Block;
-    char* const sl = xl + BM * kF8Block;
-    const int kc = b * kF8Block;
-    if (kc + kF8Block <= a.k) {
-#pragma unroll
-      for (int i = 0; i < WI; ++i)
-        lds_dma16_s(wbase + kc, woff[i], (lds_void_t*)(wl + (i * NW + wave) * 1024));
-#pragma unroll
-      for (int i = 0; i < XI; ++i)
-        lds_dma16_s(xbase + kc, xoff[i], (lds_void_t*)(xl + (i * NW + wave) * 1024));
-    } else {                               // chunks past k are zeros in both
-      const bool past = kc + lc >= a.k;
-#pragma unroll
-      for (int i = 0; i < WI; ++i)
-        lds_dma16(past ? (const void*)&kZero16 : wbase + kc + woff[i],
-                  (lds_void_t*)(wl + (i * NW + wave) * 1024));
-#pragma unroll
-      for (int i = 0; i < XI; ++i)
-        lds_dma16(past ? (const void*)&kZero16 : xbase + kc + xoff[i],
-                  (lds_void_t*)(xl + (i * NW + wave) * 1024));
+    xoff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.m - 1 - m0) * (uint32_t)a.k;
+  const int ms = min(m0 + wave * SL + lane, a.m - 1);
+  // load i of the L of block b: weights, scales, activations.  A chunk past k is its row's first instead: the
+  // weight operands are cleared there, and a NaN code in a row of x has made
+  // its whole row of y NaN in any case.
+  auto load = [&](int b, int i) {
+    const int c = b * kF8Block + lc;
+    const uint32_t o = c < a.k ? c : 0;
+    const uint32_t buf = l0 + (b & 1) * BUF;
+    if (i == WI) {
+      if (lane < SL)
+        lds_dma4(a.sx + (int64_t)b * a.m + ms,
+                 (lds_void_t*)(lds + (b & 1) * BUF + (BN + BM) * kF8Block + wave * SL * 4));
+    } else if (i < WI) {
+      lds_dma16_s(wbase, woff[i] + o, buf + (i * NW + wave) * 1024);
+    } else {
+      lds_dma16_s(xbase, xoff[i - 1 - WI] + o,
+                  buf + BN * kF8Block + ((i - 1 - WI) * NW + wave) * 1024);
     }
-    // the tokens' scales of this block, by the first BM / 64 waves
-    if (wave < BM / 64)
-      lds_dma4(a.sx + (int64_t)b * a.m + min(m0 + wave * 64 + lane, a.m - 1),
-               (lds_void_t*)(sl + wave * 256));
   };
 
   // the weight scales of 64 blocks at a time, one per lane
@@ -365,40 +362,103 @@ __global__ __launch_bounds__(WN * WM * 64) void fp8_gemm_kernel(Fp8Args a, int t
 
   // slots of this lane's two chunks in its operand rows (row & 7 = nl & 7)
   const int s0 = (kq ^ (nl & 7)) * 16, s1 = ((kq + 4) ^ (nl & 7)) * 16;
-  if (b0 < b1) issue(b0, 0);
-  for (int b = b0; b < b1; ++b) {
-    const int buf = (b - b0) & 1;
-    if (((b - b0) & 63) == 0) swl = swr[min(b + lane, a.kb - 1)];
-    vm_wait<0>();
-    wg_barrier();
-    if (b + 1 < b1) issue(b + 1, buf ^ 1);
-    const char* const wl = lds + buf * BUF + (wn * TN * 16 + nl) * kF8Block;
-    const char* const xl = lds + buf * BUF + (BN + wm * TM * 16 + nl) * kF8Block;
-    const float* const sl =
-        reinterpret_cast<const float*>(lds + buf * BUF + (BN + BM) * kF8Block) + wm * TM * 16 + nl;
+  const int wo = (wn * TN * 16 + nl) * kF8Block;
+  const int xo = (BN + wm * TM * 16 + nl) * kF8Block;
+  const int so = (BN + BM) * kF8Block + (wm * TM * 16 + nl) * 4;
+  uint4_t wr[TN][2], xr[2][2];
+  float xs[2];
+  auto read_w = [&](int b, int i, bool tail) {
+    const char* const l = lds + (b & 1) * BUF + wo + i * 16 * kF8Block;
+    wr[i][0] = *reinterpret_cast<const uint4_t*>(l + s0);
+    wr[i][1] = *reinterpret_cast<const uint4_t*>(l + s1);
+    if (tail) {
+      if (b * kF8Block + kq * 16 >= a.k) wr[i][0] = uint4_t{0, 0, 0, 0};
+      if (b * kF8Block + kq * 16 + 64 >= a.k) wr[i][1] = uint4_t{0, 0, 0, 0};
+    }
+  };
+  auto read_x = [&](int b, int j) {
+    const char* const l = lds + (b & 1) * BUF;
+    xr[j & 1][0] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s0);
+    xr[j & 1][1] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s1);
+    xs[j & 1] = *reinterpret_cast<const float*>(l + so + j * 64);
+  };
+
+  float4_t ring[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  float sr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](int t) {                  // result t of a block to its total
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[t % TN][t / TN][e] = fmaf(ring[t & 3][e], sr[t & 3], acc[t % TN][t / TN][e]);
+    // the total is formed here: put off, the results would not fit
+    asm volatile("" : "+v"(acc[t % TN][t / TN]));
+  };
+  auto step = [&](int b, auto inner) __attribute__((always_inline)) {
+    constexpr bool IN = decltype(inner)::value;          // two more blocks follow
     const float sw =
         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), (b - b0) & 63));
-    Operand<YDT == WQ_F32> xb[TM];
-    float s[TM];
+    Operand<EXACT> w[TN], x;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      xb[j].set(*reinterpret_cast<const uint4_t*>(xl + j * 16 * kF8Block + s0),
-                *reinterpret_cast<const uint4_t*>(xl + j * 16 * kF8Block + s1));
-      s[j] = sl[j * 16] * sw;
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      Operand<YDT == WQ_F32> wa;
-      wa.set(*reinterpret_cast<const uint4_t*>(wl + i * 16 * kF8Block + s0),
-             *reinterpret_cast<const uint4_t*>(wl + i * 16 * kF8Block + s1));
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const float4_t c = block_sum(wa, xb[j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], s[j], acc[i][j][e]);
+    for (int t = 0; t < T; ++t) {
+      const int i = t % TN, j = t / TN;
+      if (t == T - TN) {
+        // the next block has arrived, and this one's last operand is read
+        if constexpr (IN) vm_wait<WI>();
+        else vm_wait<0>();
+        lgkm_wait0();
+        __builtin_amdgcn_sched_barrier(0);
+        wg_barrier();
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (t == TN) {
+        // every wave has this block's weights in registers
+        wg_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (i == 0) x.set(xr[j & 1][0], xr[j & 1][1]);
+      if (j == 0) w[i].set(wr[i][0], wr[i][1]);
+      ring[t & 3] = block_sum(w[i], x);
+      sr[t & 3] = xs[j & 1] * sw;
+      __builtin_amdgcn_sched_barrier(0);
+      add((t + T - 3) % T);
+      if (i == 0) read_x(j + 1 < TM ? b : b + 1, (j + 1) % TM);
+      if (j == TM - 1) read_w(b + 1, i, !IN && (b + 2) * kF8Block > a.k);
+      if (IN) {
+        if (t >= TN && t - TN < WI) load(b + 2, t - TN);
+        if (t >= T - TN) {
+#pragma unroll
+          for (int l = WI + t - (T - TN); l < L; l += TN) load(b + 2, l);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  swl = swr[min(b0 + lane, a.kb - 1)];
+  asm volatile("" : "+v"(swl));            // waited for before the direct loads
+#pragma unroll
+  for (int i = 0; i < L; ++i) load(b0, i);
+  if (b0 + 1 < b1) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(b0 + 1, i);
+    vm_wait<L>();
+  } else {
+    vm_wait<0>();
   }
+  wg_barrier();
+  read_x(b0, 0);
+#pragma unroll
+  for (int i = 0; i < TN; ++i) read_w(b0, i, (b0 + 1) * kF8Block > a.k);
+  int b = b0;
+  for (; b + 2 < b1; ++b) {
+    if (((b - b0) & 63) == 0 && b > b0) swl = swr[min(b + lane, a.kb - 1)];
+    step(b, std::true_type{});
+  }
+  for (; b < b1; ++b) {
+    if (((b - b0) & 63) == 0 && b > b0) swl = swr[min(b + lane, a.kb - 1)];
+    step(b, std::false_type{});
+  }
+  add(T - 3);
+  add(T - 2);
+  add(T - 1);
 
   void* const out = a.part != nullptr ? a.part + (int64_t)blockIdx.y * a.m * a.n : a.y;
 #pragma unroll
@@ -415,6 +475,281 @@ __global__ __launch_bounds__(WN * WM * 64) void fp8_gemm_kernel(Fp8Args a, int t
       }
     }
   }
+}
+
+// ------------------------------------------------------- gemm in two halves
+constexpr int kHalvesN = 256;
+constexpr int kCus = 256;
+template <int TM>
+constexpr int halves_buf_bytes() { return (kHalvesN + TM * 32) * kF8Block + TM * 32 * 4; }
+
+template <int YDT, int TM>
+__device__ __forceinline__ void halves_tiles(const Fp8Args& a, char* lds) {
+  constexpr int TN = 4, BN = kHalvesN, BM = TM * 32, NW = 8, H = TM / 2, T = TN * H;
+  constexpr int BUF = halves_buf_bytes<TM>();
+  constexpr int WI = BN / 8 / NW, XI = BM / 16 / NW;     // direct loads per wave; XI per half
+  static_assert(BM % (16 * NW) == 0 && T % 4 == 0, "whole loads, the ring goes on");
+  const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wn = wave & 3, wm = wave >> 2;
+  const int nl = lane & 15, kq = lane >> 4;
+  // as in fp8_gemm_kernel, with the weights' rows in the order below
+  int n0, m0;
+  const uint8_t *wbase, *xbase;
+  constexpr int SL = BM / NW;              // tokens whose scales a wave brings
+  const float* swr;
+  auto place = [&](int tile) __attribute__((always_inline)) {
+    int im, in;
+    tile_of_block(tile, tm * tn, tm, tn, im, in);
+    n0 = in * BN;
+    m0 = im * BM;
+    wbase = a.w + (int64_t)n0 * a.k;
+    xbase = a.x + (int64_t)m0 * a.k;
+    swr = a.sw + (int64_t)min((n0 + wn * TN * 16) / kF8Block, (a.n - 1) / kF8Block) * a.kb;
+  };
+  // Direct loads of 8 rows.  Their offsets are formed each time (rows of a tile
+  // are below 256: 24-bit products): kept, they would not fit the registers.
+  // A chunk past k is its row's first instead: the weight operands are cleared
+  // there, and a NaN code in a row of x has made its row of y NaN in any case.
+  const int lr = lane >> 3, lcx = ((lane & 7) ^ lr) * 16;
+  const int lcw = ((lane & 7) ^ ((lr & 3) | (wave & 1) << 2)) * 16;
+  auto offset = [&](int b, int row, int rows, int lc) {
+    int r = lr;
+    asm volatile("" : "+v"(r));
+    const int c = b * kF8Block + lc;
+    return __umul24(min(row + r, rows - 1), a.k) + (uint32_t)(c < a.k ? c : 0);
+  };
+  const uint32_t l0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)lds);
+  auto load_w = [&](int b, int i) {
+    int row = wave * 8;
+    asm volatile("" : "+s"(row));
+    row += i * NW * 8;
+    lds_dma16_s(wbase, offset(b, row, a.n - n0, lcw), l0 + (b & 1) * BUF + row * kF8Block);
+  };
+  const int xw = (wave / TM) * TM * 16 + (wave % TM) * 8;  // its 8 rows of a half's first
+  auto load_x = [&](int b, int h, int i) {
+    int row = xw;
+    asm volatile("" : "+s"(row));
+    row += i * NW * 16 + h * TM * 8;
+    lds_dma16_s(xbase, offset(b, row, a.m - m0, lcx),
+                l0 + (b & 1) * BUF + (BN + row) * kF8Block);
+  };
+  auto load_s = [&](int b) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    if (l < SL)
+      lds_dma4(a.sx + (int64_t)b * a.m + min(m0 + wave * SL + l, a.m - 1),
+               (lds_void_t*)(lds + (b & 1) * BUF + (BN + BM) * kF8Block + wave * SL * 4));
+  };
+  auto load_lo = [&](int b) {
+    load_s(b);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) load_x(b, 0, i);
+  };
+
+  using cfloat = const __attribute__((address_space(4))) float;
+  float4_t acc[TN][TM];
+  const int s0 = (kq ^ (nl & 7)) * 16, s1 = ((kq + 4) ^ (nl & 7)) * 16;
+  // Row nl of weight operand i is feature 32 (i / 2) + 8 (nl / 4) + 4 (i % 2) +
+  // nl % 4 of the wave's 64: a lane's results of two operands are then eight
+  // consecutive features, one 16-byte store.
+  const int wo = (wn * TN * 16 + ((nl >> 2) * 8 + (nl & 3))) * kF8Block;
+  auto wrow = [](int i) { return ((i >> 1) * 32 + (i & 1) * 4) * kF8Block; };
+  const int xo = (BN + wm * TM * 16 + nl) * kF8Block;
+  const int so = (BN + BM) * kF8Block + (wm * TM * 16 + nl) * 4;
+
+  float4_t ring[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  float sr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](int h, int t) {           // result t of half h to its total
+    const int i = t % TN, j = h * H + t / TN;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(ring[t & 3][e], sr[t & 3], acc[i][j][e]);
+    asm volatile("" : "+v"(acc[i][j]));
+  };
+  auto step = [&](int b, auto inner) {
+    constexpr bool IN = decltype(inner)::value;          // two more blocks follow
+    const char* const buf = lds + (b & 1) * BUF;
+    Operand<false> w[TN];
+    float s[TM];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // ---- operands
+      Operand<false> x[H];
+      float sw;
+      if (IN && h == 1) load_lo(b + 2);
+      if (h == 0) {
+        sw = ((cfloat*)swr)[b];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) s[j] = *reinterpret_cast<const float*>(buf + so + j * 64);
+        const bool p0 = b * kF8Block + kq * 16 >= a.k, p1 = b * kF8Block + kq * 16 + 64 >= a.k;
+        const bool tail = !IN && (b + 1) * kF8Block > a.k;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          uint4_t c0 = *reinterpret_cast<const uint4_t*>(buf + wo + wrow(i) + s0);
+          uint4_t c1 = *reinterpret_cast<const uint4_t*>(buf + wo + wrow(i) + s1);
+          if (tail) {
+            if (p0) c0 = uint4_t{0, 0, 0, 0};
+            if (p1) c1 = uint4_t{0, 0, 0, 0};
+          }
+          w[i].set(c0, c1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const int jj = h * H + j;
+        x[j].set(*reinterpret_cast<const uint4_t*>(buf + xo + jj * 16 * kF8Block + s0),
+                 *reinterpret_cast<const uint4_t*>(buf + xo + jj * 16 * kF8Block + s1));
+      }
+      if (h == 0) {
+        if constexpr (IN) vm_wait<1 + XI + WI>();
+        else vm_wait<0>();
+      } else {
+        if constexpr (IN) {
+          vm_wait<1 + 2 * XI>();
+        } else {
+          vm_wait<0>();
+        }
+      }
+      if (h == 0) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) s[j] *= sw;
+      }
+      lgkm_wait0();
+      __builtin_amdgcn_sched_barrier(0);
+      wg_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      // ---- products
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        ring[t & 3] = block_sum(w[t % TN], x[t / TN]);
+        sr[t & 3] = s[h * H + t / TN];
+        __builtin_amdgcn_sched_barrier(0);
+        add(t >= 3 ? h : h ^ 1, (t + T - 3) % T);
+        if (h == 0) {
+          if (t % 4 == 1 && t / 4 < XI && (IN || b + 1 < a.kb)) load_x(b + 1, 1, t / 4);
+        } else {
+          if (IN && t % (T / WI) == 1) load_w(b + 2, t / (T / WI));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      wg_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // the first block and the first parts of the second
+  auto begin = [&]() __attribute__((always_inline)) {
+    load_lo(0);
+#pragma unroll
+    for (int i = 0; i < WI; ++i) load_w(0, i);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) load_x(0, 1, i);
+    if (a.kb > 1) {
+      load_lo(1);
+#pragma unroll
+      for (int i = 0; i < WI; ++i) load_w(1, i);
+    }
+  };
+  const int tiles = tm * tn;
+  if ((int)blockIdx.x >= tiles) return;
+  place((int)blockIdx.x);
+  begin();
+  if (a.kb > 1) vm_wait<1 + XI + WI>();
+  else vm_wait<0>();
+  for (int tile = (int)blockIdx.x;;) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    wg_barrier();
+    if (wm == 1) wg_barrier();
+    int b = 0;
+    for (; b + 2 < a.kb; ++b) step(b, std::true_type{});
+    for (; b < a.kb; ++b) step(b, std::false_type{});
+    if (wm == 0) wg_barrier();
+    add(1, T - 3);
+    add(1, T - 2);
+    add(1, T - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ring[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      sr[i] = 0.0f;
+    }
+
+    // the next tile's first loads fly while this one's results are stored
+    const int ns = n0 + wn * TN * 16 + kq * 8, mst = m0 + wm * TM * 16 + nl;
+    const bool whole = m0 + BM <= a.m && n0 + BN <= a.n && (a.ld & 7) == 0;
+    tile += (int)gridDim.x;
+    const bool more = tile < tiles;
+    if (more) {
+      place(tile);
+      begin();
+    }
+    constexpr int NS = TN * TM / 2;      // stores of a whole tile
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int64_t o = (int64_t)(mst + j * 16) * a.ld + ns;
+#pragma unroll
+        for (int i = 0; i < TN; i += 2)
+          *reinterpret_cast<uint4_t*>(static_cast<uint16_t*>(a.y) + o + i * 16) =
+              uint4_t{pack2<YDT>(acc[i][j][0], acc[i][j][1]),
+                      pack2<YDT>(acc[i][j][2], acc[i][j][3]),
+                      pack2<YDT>(acc[i + 1][j][0], acc[i + 1][j][1]),
+                      pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const int m = mst + j * 16, n = ns + (i >> 1) * 32 + (i & 1) * 4;
+          if (m < a.m && n < a.n)
+            store4<YDT>(a.y, (int64_t)m * a.ld + n, acc[i][j], (a.ld & 3) == 0, a.n - n);
+        }
+      }
+    }
+    if (!more) break;
+    if (whole && a.kb > 1) vm_wait<1 + XI + WI + NS>();
+    else vm_wait<0>();
+  }
+}
+
+// the first f columns of 256 features as 256 x 256 tiles, the others as tiles of
+// 128 tokens
+template <int YDT>
+__global__ __launch_bounds__(512, 2) void fp8_halves_kernel(Fp8Args a, int f) {
+  extern __shared__ uint4_t dsm[];
+  char* const lds = reinterpret_cast<char*>(dsm);
+  Fp8Args p = a;
+  p.n = min(a.n, f * kHalvesN);
+  if (p.n > 0) halves_tiles<YDT, 8>(p, lds);
+  if (p.n < a.n) {
+    Fp8Args r = a;
+    r.n = a.n - p.n;
+    r.w += (int64_t)p.n * a.k;
+    r.sw += (int64_t)(p.n / kF8Block) * a.kb;
+    r.y = static_cast<uint16_t*>(a.y) + p.n;
+    halves_tiles<YDT, 4>(r, lds);
+  }
+}
+
+template <int YDT>
+hipError_t halves_launch(const Fp8Args& a, int f, hipStream_t s) {
+  constexpr int bytes = 2 * halves_buf_bytes<8>();
+  auto* kern = &fp8_halves_kernel<YDT>;
+  static std::atomic<bool> ready{false};
+  if (!ready.load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    ready.store(true, std::memory_order_release);
+  }
+  kern<<<kCus, 512, bytes, s>>>(a, f);
+  return hipGetLastError();
 }
 
 // y = the sum of the splits' totals, in their order
@@ -470,10 +805,11 @@ hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
     if (a.m <= 32) return decode_launch<YDT, 8, 1, 2>(a, s);
     return few ? decode_launch<YDT, 8, 1, 4>(a, s) : decode_launch<YDT, 4, 2, 4>(a, s);
   }
-  // the exact products need twice the operand registers: smaller wave tiles
-  constexpr int TM2 = YDT == WQ_F32 ? 4 : 8;
-  hipError_t e = p.tile == 2 ? gemm_launch<YDT, 4, 2, 4, TM2>(a, s)
-                             : gemm_launch<YDT, 2, 2, 4, 4>(a, s);
+  hipError_t e;
+  if constexpr (YDT != WQ_F32) {
+    if (p.tile == 2) return halves_launch<YDT>(a, p.full, s);
+  }
+  e = gemm_launch<YDT, 2, 2, 4, 4>(a, s);
   if (e != hipSuccess || a.part == nullptr) return e;
   const int64_t count = (int64_t)a.m * a.n;
   fp8_join_kernel<YDT><<<dim3((unsigned)((count + 1023) / 1024)), 256, 0, s>>>(a.part, a.splits,
@@ -491,8 +827,11 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k) {
     p.tile = 0;
     return p;
   }
-  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
-  p.tile = big >= 192 ? 2 : 1;
+  const int64_t tm = (m + 255) / 256, tn = (n + 255) / 256, big = tm * tn;
+  p.tile = big > kCus / 4 ? 2 : 1;
+  // whole rounds of 256 x 256 tiles, then half tiles if they fill one round
+  p.full = (int)(big / kCus * kCus / tm);
+  if ((tn - p.full) * ((m + 127) / 128) > kCus) p.full = (int)tn;
   if (p.tile == 1) {
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
     int64_t s = std::max<int64_t>(1, 512 / tiles);
@@ -511,7 +850,7 @@ hipError_t launch_linear_fp8(const uint8_t* x, const float* sx, int64_t m, const
   const Fp8Args a{x, sx, static_cast<const uint8_t*>(w->codes),
                   static_cast<const float*>(w->scales), y, plan.splits > 1 ? part : nullptr,
                   (int)m, (int)w->n, (int)w->k, (int)((w->k + kF8Block - 1) / kF8Block),
-                  plan.splits};
+                  plan.splits, (int)w->n};
   if (ydt == WQ_F32) return fp8_ydt<WQ_F32>(a, plan, s);
   if (ydt == WQ_BF16) return fp8_ydt<WQ_BF16>(a, plan, s);
   return fp8_ydt<WQ_F16>(a, plan, s);

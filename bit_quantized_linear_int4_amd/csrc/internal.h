@@ -178,6 +178,7 @@ hipError_t launch_quantize_fp8_block(const uint16_t* w, int dt, int64_t n, int64
 
 struct Fp8Plan {
   int tile;          // 0 = decode (m <= 64), 1 = 128 x 128 tiles, 2 = 256 x 256
+  int full;          // tile 2, 16-bit y: columns of 256 features as 256 x 256 tiles
   int splits;        // parts of k summed by a second kernel (1 = none)
   size_t ws_bytes;   // their fp32 totals
 };
