@@ -695,11 +695,11 @@ __device__ __forceinline__ void halves_tiles(const Fp8Args& a, char* lds) {
         const int64_t o = (int64_t)(mst + j * 16) * a.ld + ns;
 #pragma unroll
         for (int i = 0; i < TN; i += 2)
-          *reinterpret_cast<uint4_t*>(static_cast<uint16_t*>(a.y) + o + i * 16) =
-              uint4_t{pack2<YDT>(acc[i][j][0], acc[i][j][1]),
+          __builtin_nontemporal_store(
+              (uint4_t{pack2<YDT>(acc[i][j][0], acc[i][j][1]),
                       pack2<YDT>(acc[i][j][2], acc[i][j][3]),
                       pack2<YDT>(acc[i + 1][j][0], acc[i + 1][j][1]),
-                      pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])};
+                      pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])}), reinterpret_cast<uint4_t*>(static_cast<uint16_t*>(a.y) + o + i * 16));
       }
     } else {
 #pragma unroll
