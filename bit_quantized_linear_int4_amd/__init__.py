@@ -145,10 +145,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream, t):
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        if _raw_stream is None:
+            import torch
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(t.get_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -168,7 +174,7 @@ def _fail(what, msg, status=_ERR_SHAPE):
 
 
 def _nbytes(t):
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _dense(what, name, t, nbytes=None, shape=None):
@@ -587,15 +593,22 @@ def wq_linear_fp8_workspace(m, weight):
 
 def wq_linear_fp8(q, scales, weight, y, workspace=None, stream=None):
     what = "wq_linear_fp8"
-    m, ts = _check_linear(what, q, weight, [("y", y)])
-    _fp8_rows(what, q, scales, m, weight.k)
+    if q is None or q.dim() != 2:
+        _fail(what, "q must be a 2-D [rows][k] tensor")
+    m, k = q.shape
+    if k != weight.k:
+        _fail(what, f"q has k={k}, the weight k={weight.k}")
+    _fp8_rows(what, q, scales, m, k)
+    wt = _weight_tensors(what, weight)
+    _dense(what, "y", y, shape=(m, weight.n))
+    ws_bytes = 0
     if workspace is not None:
         _dense(what, "workspace", workspace)
-    _on_gpu(what, workspace, scales, *ts)
+        ws_bytes = workspace.nbytes
+    _on_gpu(what, q, scales, y, workspace, *wt)
     d = weight.descriptor()
-    ws_bytes = 0 if workspace is None else _nbytes(workspace)
-    st = _load().wq_linear_fp8(_ptr(q), _ptr(scales), m, ctypes.byref(d), _ptr(y), _dt(y),
-                               _ptr(workspace), ws_bytes, _stream(stream, q))
+    st = _load().wq_linear_fp8(q.data_ptr(), scales.data_ptr(), m, ctypes.byref(d), y.data_ptr(),
+                               _dt(y), _ptr(workspace), ws_bytes, _stream(stream, q))
     _check(st, what)
 
 
@@ -607,7 +620,6 @@ def wq_moe_workspace(m, top_k, gate, experts):
 def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, logits=None,
            ids=None, probs=None, stream=None):
     """`router` [experts][h] in x's dtype, or None with `logits` fp32 [m][experts]."""
-    import torch
     what = "wq_moe"
     m, h = _matrix(what, "x", x)
     if (router is None) == (logits is None):
@@ -619,7 +631,7 @@ def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, log
     else:
         _, experts = _matrix(what, "logits", logits)
         _dense(what, "logits", logits, shape=(m, experts))
-        if logits.dtype != torch.float32:
+        if _dt(logits) != F32:
             _fail(what, "logits must be float32", _ERR_UNSUP)
     ts = []
     for w in (gate, up, down):

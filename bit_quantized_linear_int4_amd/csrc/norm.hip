@@ -9,9 +9,9 @@
 // once and each output written once: the kernel is bound by HBM for many rows
 // and by the latency of one load, one barrier and one store for few.  bf16 with
 // a residual to FP8, 8192 rows of 8192: 84 us, 5600 GB/s (a copy of 1 GiB:
-// 5180); 1 row of 4096: 2.4 us, of which an empty launch is 2.
+// 5180); 1 row of 4096: 2.4 us, of 256: 2.0.
 // One row per workgroup, and outputs stored past the caches, which keeps them
-// for the inputs: with four rows per workgroup 92 us, with ordinary stores 95.
+// for the inputs: with four rows per workgroup 97 us, with ordinary stores 96.
 //
 // quantize_rows: the same scale and code for given rows, or for silu(x) * up
 // (what stands between the gate/up and the down product of an MLP); bound by
