@@ -327,3 +327,21 @@ def test_streams_and_graph():
             assert all(torch.equal(a, b) for a, b in zip((out, y, z, s, s2), ref))
             linear(q, s, w, "f32")
             st.synchronize()
+
+
+# more tiles than CUs, whole and cut tiles, one block of k, tiles of 128 tokens
+# after the last whole round and without one
+@pytest.mark.parametrize("m,n,k", [(4096, 5120, 256), (4100, 8196, 128), (2048, 4096, 400),
+                                   (8192, 4224, 384)])
+def test_linear_many_tiles(m, n, k):
+    say(f"fp8 linear m={m} n={n} k={k}")
+    q, s, w = make_linear(m, n, k, 37)
+    # a tile whose results are not finite leaves the next one of its workgroup alone
+    q.view(torch.uint8)[3, k - 1] = 0x7F
+    y = linear(q, s, w, "bf16")
+    torch.cuda.synchronize()
+    assert bool(y[3].isnan().all())
+    q.view(torch.uint8)[3, k - 1] = 0
+    y[3] = linear(q, s, w, "bf16")[3]
+    torch.cuda.synchronize()
+    check_linear(y, q, s, w, "bf16")
