@@ -177,6 +177,10 @@ def _nbytes(t):
     return t.nbytes
 
 
+def _has(t, nbytes):
+    return t is not None and t.nbytes == nbytes and t.is_contiguous()
+
+
 def _dense(what, name, t, nbytes=None, shape=None):
     """`t` is contiguous, with `shape` (if given) and exactly `nbytes` bytes
     (if given)."""
@@ -221,9 +225,11 @@ def _weight_tensors(what, w):
         if k % g:
             _fail(what, f"k={k} is not a multiple of the group {g}")
         ng = k // g
-        _dense(what, "codes", w.codes, n * k // 2)
-        _dense(what, "scales", w.scales, 2 * n * ng)
-        _dense(what, "zeros", w.zeros, n * ((ng + 1) // 2))
+        if not (_has(w.codes, n * k // 2) and _has(w.scales, 2 * n * ng)
+                and _has(w.zeros, n * ((ng + 1) // 2))):          # says which
+            _dense(what, "codes", w.codes, n * k // 2)
+            _dense(what, "scales", w.scales, 2 * n * ng)
+            _dense(what, "zeros", w.zeros, n * ((ng + 1) // 2))
         if w.perm is not None:
             _dense(what, "perm", w.perm, 4 * k)
     elif w.fmt in (FMT_NF4, FMT_FP4):

@@ -182,29 +182,37 @@ __device__ __forceinline__ void top_k_of(const float* l, int e, int top_k, int r
     if (key[r] != 0) sum += __expf(order_value(key[r]) - top);
   sum = sum64(sum);
   id = 0;
-  prob = 0.0f;
+  uint32_t mine = 0;                   // the key of this lane's choice
   for (int k = 0; k < top_k; ++k) {
     uint32_t m = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) m = max(m, key[r]);
     m = max64(m);
-    // lowest index among the largest: the largest of 0xFFFF - index
-    uint32_t at = 0;
+    int j = 0;                         // the lowest index among the largest
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-      if (key[r] == m) at = 0xFFFFu - (uint32_t)(lane + 64 * r);
-    const int j = 0xFFFF - (int)max64(at);
+    for (int r = R - 1; r >= 0; --r) {
+      const uint64_t on = __ballot(key[r] == m);
+      if (on != 0) j = 64 * r + __builtin_ctzll(on);
+    }
     if (lane == k) {
       id = j;
-      prob = __expf(order_value(m) - top);
+      mine = m;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (j == lane + 64 * r) key[r] = 0;
   }
-  const float total = renorm ? sum64(lane < top_k ? prob : 0.0f) : sum;
+  prob = lane < top_k ? __expf(order_value(mine) - top) : 0.0f;
+  const float total = renorm ? sum64(prob) : sum;
   // top is -inf only when every expert is masked
   prob = __float_as_uint(top) == 0xFF800000u ? 0.0f : __fdiv_rn(prob, total);
+}
+
+__device__ __forceinline__ void top_k_any(const MoeArgs& a, int t, int lane, int& id, float& p) {
+  const float* l = a.logits + (int64_t)t * a.e;
+  if (a.e <= 64) top_k_of<1>(l, a.e, a.top_k, a.renorm, lane, id, p);
+  else if (a.e <= 256) top_k_of<4>(l, a.e, a.top_k, a.renorm, lane, id, p);
+  else top_k_of<kMaxE / 64>(l, a.e, a.top_k, a.renorm, lane, id, p);
 }
 
 // Fills `r` for all tokens; every thread of the workgroup calls it.
@@ -212,14 +220,36 @@ template <int NW>
 __device__ void route(const MoeArgs& a, Routing& r) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (a.t == 1) {
+    // one token: each choice is an expert with that token, nothing to sort
+    // (one token, 8 of 64 experts: this and the sums cost 3.2 us by the way below)
+    if (wave == 0) {
+      int id;
+      float p;
+      top_k_any(a, 0, lane, id, p);
+      const bool on = lane < a.top_k && p != 0.0f;
+      const uint64_t live = __ballot(on);
+      const int at = __popcll(live & ((1ull << lane) - 1));
+      if (lane < a.top_k) {
+        r.ids[lane] = id;
+        r.probs[lane] = p;
+      }
+      if (on) {
+        r.act[at] = Active{id, at, 1, at};
+        r.act_of[at] = (uint16_t)at;
+        r.slot_prob[at] = p;
+        r.slot_tok[at] = 0;
+      }
+      if (lane == 0) r.count = r.chunks = __popcll(live);
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = tid; i < a.e; i += NW * 64) r.mask[i][0] = r.mask[i][1] = 0;
   for (int t = wave; t < a.t; t += NW) {
     int id;
     float p;
-    const float* l = a.logits + (int64_t)t * a.e;
-    if (a.e <= 64) top_k_of<1>(l, a.e, a.top_k, a.renorm, lane, id, p);
-    else if (a.e <= 256) top_k_of<4>(l, a.e, a.top_k, a.renorm, lane, id, p);
-    else top_k_of<kMaxE / 64>(l, a.e, a.top_k, a.renorm, lane, id, p);
+    top_k_any(a, t, lane, id, p);
     if (lane < a.top_k) {
       r.ids[t * a.top_k + lane] = id;
       r.probs[t * a.top_k + lane] = p;
@@ -517,10 +547,30 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
   __shared__ Routing r;
   __shared__ float4_t red[2][2][NW][64];
   __shared__ uint32_t meta[kInt4 ? 2 : 1][kInt4 ? 2 * GP * 16 : 1];
-  route<NW>(a, r);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nl = lane & 15, kq = lane >> 4;
+  const int nl = lane & 15, kq = lane >> 4, ku = a.h >> 7;
+  Acts x0, x1;                         // of the wave's two units
+  auto keep_acts = [&](int u) {        // units past the end of k add nothing
+    vm_wait<0>();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if (u >= ku) x0.f[f] = uint4_t{0, 0, 0, 0};
+      if (u + 1 >= ku) x1.f[f] = uint4_t{0, 0, 0, 0};
+      if constexpr (kInt4) {
+        x0.f[f] = pair_order(x0.f[f]);
+        x1.f[f] = pair_order(x1.f[f]);
+      }
+    }
+  };
+  // one token's activations do not depend on its choices
+  const bool one = a.t == 1 && passes == 1;
+  if (one) {
+    load_acts<FMT, S>(x0, a.x, 0, min(wave * 2, ku - 1), kq);
+    load_acts<FMT, S>(x1, a.x, 0, min(wave * 2 + 1, ku - 1), kq);
+  }
+  route<NW>(a, r);
+  if (one) keep_acts(wave * 2);
   const int nact = __builtin_amdgcn_readfirstlane(r.count);
   if (blockIdx.x == 0) {
     for (int i = tid; i < nact; i += NW * 64) {
@@ -540,7 +590,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
   // neighbours in it run on the same XCD: the chunks of one block are about
   // one workgroup each, next to each other, so the codes of a block come from
   // HBM for the first and from that XCD's L2 for the others.
-  const int tiles = a.i >> 4, ku = a.h >> 7, groups = ku * S;
+  const int tiles = a.i >> 4, groups = ku * S;
   const int steps = tiles * __builtin_amdgcn_readfirstlane(r.chunks), G = (int)gridDim.x;
   const int per = (steps + G - 1) / G;
   const int xcd = (int)blockIdx.x & 7;
@@ -570,7 +620,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     if (++p.st >= st1) {               // stays on the last tile
       --p.tile;
     } else if (p.tile + 1 == p.hi) {
-      p.fresh = true;
+      p.fresh = !one;
       if (16 * ++p.ch >= p.cnt) {
         p.ch = 0;
         p.lo = p.hi;
@@ -596,7 +646,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     p.hi = min(p.lo + per, tiles);
     p.ch = (in - p.lo * nch) / (p.hi - p.lo);
     p.tile = p.lo + (in - p.lo * nch) % (p.hi - p.lo);
-    p.fresh = true;
+    p.fresh = !one;
     return p;
   };
   auto unit_of = [&](const Pos& p) { return (p.pass * NW + wave) * 2; };
@@ -635,7 +685,6 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
   float4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   int flip = 0, rflip = 0;
   Pos cur = start();
-  Acts x0, x1;                         // of the wave's two units
   // a unit's registers take the next tile's as soon as it is multiplied
   Unit<FMT> w0[2], w1[2];
   if constexpr (kInt4) load_meta(cur);
@@ -648,26 +697,17 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     lgkm_wait0();
     wg_barrier();
   }
-  while (cur.st < st1) {
+  auto step = [&](auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;         // another step follows
     const int u = unit_of(cur);
     Pos nxt = cur;
-    advance(nxt);
+    if constexpr (MORE) advance(nxt);
     if (cur.fresh) {
       const uint32_t tok = r.slot_tok[cur.slot + min(16 * cur.ch + nl, cur.cnt - 1)];
       const uint32_t xo = tok * (uint32_t)(a.h * 2);
       load_acts<FMT, S>(x0, a.x, xo, min(u, ku - 1), kq);
       load_acts<FMT, S>(x1, a.x, xo, min(u + 1, ku - 1), kq);
-      vm_wait<0>();
-      // units past the end of k add nothing
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (u >= ku) x0.f[f] = uint4_t{0, 0, 0, 0};
-        if (u + 1 >= ku) x1.f[f] = uint4_t{0, 0, 0, 0};
-        if constexpr (kInt4) {
-          x0.f[f] = pair_order(x0.f[f]);
-          x1.f[f] = pair_order(x1.f[f]);
-        }
-      }
+      keep_acts(u);
     }
     // the words of unit j of both matrices
     auto read_meta = [&](int j, uint32_t (&m)[2][S]) {
@@ -679,7 +719,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
             m[i][g] = meta[flip][(i * GP + (2 * wave + j) * S + g) * 16 + nl];
       }
     };
-    if constexpr (kInt4) load_meta(nxt);
+    if constexpr (kInt4 && MORE) load_meta(nxt);
     uint32_t m[2][S];
     read_meta(0, m);
     // the barriers keep the compiler from unpacking everything at once, which
@@ -687,13 +727,15 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     __builtin_amdgcn_sched_barrier(0);
     unit_mac<XDT, FMT, S, 2>(w0, m, x0, acc);
     __builtin_amdgcn_sched_barrier(0);
-    load(nxt, 0, w0);
+    if constexpr (MORE) load(nxt, 0, w0);
     read_meta(1, m);
     __builtin_amdgcn_sched_barrier(0);
     unit_mac<XDT, FMT, S, 2>(w1, m, x1, acc);
     __builtin_amdgcn_sched_barrier(0);
-    load(nxt, 1, w1);
-    if constexpr (kInt4) keep_meta(nxt, flip ^ 1);
+    if constexpr (MORE) {
+      load(nxt, 1, w1);
+      if constexpr (kInt4) keep_meta(nxt, flip ^ 1);
+    }
     const bool last = cur.pass + 1 == passes;
     // the buffers of the step before are free: every wave has passed the
     // barrier after its last read of them
@@ -728,6 +770,15 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     }
     flip ^= 1;
     cur = nxt;
+  };
+  // The last step loads nothing ahead and so waits for nothing (one token, 8 of
+  // 64 experts of 2048 x 1024: 1 us of 22); four groups per unit leave no
+  // registers for a second copy of the step.
+  if constexpr (S == 4) {
+    while (cur.st < st1) step(std::true_type{});
+  } else {
+    while (cur.st + 1 < st1 || cur.pass + 1 < passes) step(std::true_type{});
+    step(std::false_type{});
   }
 }
 
@@ -848,9 +899,10 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
       // in this order, as the loop waits for them
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int st = s0; st < s1; ++st) {
+    auto step = [&](auto more) __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value;       // another group follows
       Pos nxt = cur;
-      if (st + 1 < s1 && ++nxt.g == kg) {
+      if (MORE && ++nxt.g == kg) {
         nxt.g = 0;
         ++nxt.ci;
         enter(nxt);
@@ -858,7 +910,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
       uint32_t m[S];
       if constexpr (kInt4) {
         words(cur, m);
-        load_meta(nxt);
+        if constexpr (MORE) load_meta(nxt);
       }
 #pragma unroll
       for (int j = 0; j < R; ++j) {
@@ -874,11 +926,13 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
         __builtin_amdgcn_sched_barrier(0);
         if (cur.g * R + j < ku) unit_mac<XDT, FMT, S, RT>(w[j], mj, x[j], acc);
         __builtin_amdgcn_sched_barrier(0);
-        load(nxt, j, w[j], x[j]);
+        if constexpr (MORE) load(nxt, j, w[j], x[j]);
       }
-      if (nxt.ci != cur.ci || st + 1 == s1) flush(cur);
+      if (!MORE || nxt.ci != cur.ci) flush(cur);
       cur = nxt;
-    }
+    };
+    for (int st = s0; st + 1 < s1; ++st) step(std::true_type{});
+    step(std::false_type{});
   }
   __syncthreads();
   constexpr int BR = 16 * RT;
