@@ -283,30 +283,26 @@ __device__ __forceinline__ void tile_of_block(int bid, int T, int tm, int tn, in
   in = w / gm;
 }
 
-template <int WN, int WM, int TN, int TM>
-constexpr int fp8_buf_bytes() {
-  return (WN * TN + WM * TM) * 16 * kF8Block + WM * TM * 16 * 4;
-}
+// 2 x 2 waves, each 64 features x TM tiles of 16 tokens
+constexpr int kTileN = 128;
+template <int TM>
+constexpr int fp8_buf_bytes() { return (kTileN + TM * 32) * kF8Block + TM * 32 * 4; }
 
-// WN x WM waves, each TN x TM tiles of 16 features x 16 tokens.
-template <int YDT, int WN, int WM, int TN, int TM>
-__global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int tn) {
+template <int YDT, int TM, int NB>
+__global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int tn) {
   constexpr bool EXACT = YDT == WQ_F32;
-  constexpr int NW = WN * WM, T = TN * TM;
-  constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-  constexpr int BUF = fp8_buf_bytes<WN, WM, TN, TM>();
+  constexpr int NW = 4, TN = 4, T = TN * TM, BN = kTileN, BM = TM * 32;
+  constexpr int BUF = fp8_buf_bytes<TM>();
   constexpr int WI = BN / 8 / NW, XI = BM / 8 / NW;      // direct loads per wave and block,
   constexpr int SL = BM / NW;                            // and tokens whose scales it brings
   constexpr int L = 1 + WI + XI;
-  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && SL <= 64, "whole loads");
-  static_assert(kF8Block % (TN * 16) == 0, "a wave's features share a scale block");
-  static_assert(TN == 4 && WI <= TN && TM % 2 == 0, "the loads fit between the products");
+  static_assert(TM % 2 == 0 && TM <= 4 && (NB - 1) * L <= 63, "counted loads");
   extern __shared__ uint4_t dsm[];
   char* const lds = reinterpret_cast<char*>(dsm);
   const uint32_t l0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wn = wave % WN, wm = wave / WN;
+  const int wn = wave & 1, wm = wave >> 1;
   const int nl = lane & 15, kq = lane >> 4;
   int im, in;
   tile_of_block((int)blockIdx.x, tm * tn, tm, tn, im, in);
@@ -315,11 +311,12 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, in
   const int per = (a.kb + a.splits - 1) / a.splits;
   const int b0 = (int)blockIdx.y * per, b1 = min(b0 + per, a.kb);
 
-  // lane l of a load brings chunk (l & 7) ^ (row & 7) of row l / 8 into slot
-  // l & 7 of that row, so the 8 rows of an operand read that share LDS banks
-  // hold the same chunk in 8 different slots.  Rows past the end read the last
-  // row; their results are not stored.
-  const int lr = lane >> 3, lc = ((lane & 7) ^ lr) * 16;
+  // Lane l of a load brings chunk (l & 7) ^ f of row l / 8 into slot l & 7 of
+  // that row, with f different for the 8 rows that an operand read takes at
+  // once, so that they hold the same chunk in 8 different slots.  Rows past the
+  // end read the last row; their results are not stored.
+  const int lr = lane >> 3, lcx = ((lane & 7) ^ lr) * 16;
+  const int lcw = EXACT ? lcx : ((lane & 7) ^ ((lr & 3) | (wave & 1) << 2)) * 16;
   const uint8_t* const wbase = a.w + (int64_t)n0 * a.k;
   const uint8_t* const xbase = a.x + (int64_t)m0 * a.k;
   uint32_t woff[WI], xoff[XI];
@@ -330,29 +327,30 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, in
   for (int i = 0; i < XI; ++i)
     xoff[i] = (uint32_t)min((i * NW + wave) * 8 + lr, a.m - 1 - m0) * (uint32_t)a.k;
   const int ms = min(m0 + wave * SL + lane, a.m - 1);
-  // load i of the L of block b: weights, scales, activations.  A chunk past k is its row's first instead: the
-  // weight operands are cleared there, and a NaN code in a row of x has made
-  // its whole row of y NaN in any case.
-  auto load = [&](int b, int i) {
+  // Load i of the L of block b into the buffer at `buf`.  A chunk past k is its
+  // row's first instead: the weight operands are cleared there, and a NaN code
+  // in a row of x has made its whole row of y NaN in any case.
+  auto chunk = [&](int b, int lc) {
     const int c = b * kF8Block + lc;
-    const uint32_t o = c < a.k ? c : 0;
-    const uint32_t buf = l0 + (b & 1) * BUF;
-    if (i == WI) {
-      if (lane < SL)
-        lds_dma4(a.sx + (int64_t)b * a.m + ms,
-                 (lds_void_t*)(lds + (b & 1) * BUF + (BN + BM) * kF8Block + wave * SL * 4));
-    } else if (i < WI) {
-      lds_dma16_s(wbase, woff[i] + o, buf + (i * NW + wave) * 1024);
-    } else {
-      lds_dma16_s(xbase, xoff[i - 1 - WI] + o,
-                  buf + BN * kF8Block + ((i - 1 - WI) * NW + wave) * 1024);
+    return (uint32_t)(c < a.k ? c : 0);
+  };
+  auto load = [&](int b, uint32_t buf, int i) __attribute__((always_inline)) {
+    if (i < WI) {
+      lds_dma16_s(wbase, woff[i] + chunk(b, lcw), l0 + buf + (i * NW + wave) * 1024);
+    } else if (i < WI + XI) {
+      lds_dma16_s(xbase, xoff[i - WI] + chunk(b, lcx),
+                  l0 + buf + BN * kF8Block + ((i - WI) * NW + wave) * 1024);
+    } else if (lane < SL) {
+      lds_dma4(a.sx + (int64_t)b * a.m + ms,
+               (lds_void_t*)(lds + buf + (BN + BM) * kF8Block + wave * SL * 4));
     }
   };
 
   // the weight scales of 64 blocks at a time, one per lane
   const int nbw = min((n0 + wn * TN * 16) / kF8Block, (a.n - 1) / kF8Block);
   const float* const swr = a.sw + (int64_t)nbw * a.kb;
-  float swl = 0.0f;
+  float swl = swr[min(b0 + lane, a.kb - 1)];
+  asm volatile("" : "+v"(swl));            // waited for before the direct loads
 
   float4_t acc[TN][TM];
 #pragma unroll
@@ -360,15 +358,19 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, in
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // slots of this lane's two chunks in its operand rows (row & 7 = nl & 7)
+  // Slots of this lane's two chunks in its operand rows.  Row nl of weight
+  // operand i is feature 32 (i / 2) + 8 (nl / 4) + 4 (i % 2) + nl % 4 of the
+  // wave's 64 (16-bit y): a lane's results of two operands are then eight
+  // consecutive features, one 16-byte store.  fp32 y: 16 i + nl.
   const int s0 = (kq ^ (nl & 7)) * 16, s1 = ((kq + 4) ^ (nl & 7)) * 16;
-  const int wo = (wn * TN * 16 + nl) * kF8Block;
+  const int wo = (wn * TN * 16 + (EXACT ? nl : (nl >> 2) * 8 + (nl & 3))) * kF8Block;
+  auto wrow = [](int i) { return EXACT ? i * 16 : (i >> 1) * 32 + (i & 1) * 4; };
   const int xo = (BN + wm * TM * 16 + nl) * kF8Block;
   const int so = (BN + BM) * kF8Block + (wm * TM * 16 + nl) * 4;
-  uint4_t wr[TN][2], xr[2][2];
-  float xs[2];
-  auto read_w = [&](int b, int i, bool tail) {
-    const char* const l = lds + (b & 1) * BUF + wo + i * 16 * kF8Block;
+  uint4_t wr[TN][2], xr[TM][2];
+  float xs[TM];
+  auto read_w = [&](int b, uint32_t buf, int i, bool tail) __attribute__((always_inline)) {
+    const char* const l = lds + buf + wo + wrow(i) * kF8Block;
     wr[i][0] = *reinterpret_cast<const uint4_t*>(l + s0);
     wr[i][1] = *reinterpret_cast<const uint4_t*>(l + s1);
     if (tail) {
@@ -376,102 +378,123 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void fp8_gemm_kernel(Fp8Args a, in
       if (b * kF8Block + kq * 16 + 64 >= a.k) wr[i][1] = uint4_t{0, 0, 0, 0};
     }
   };
-  auto read_x = [&](int b, int j) {
-    const char* const l = lds + (b & 1) * BUF;
-    xr[j & 1][0] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s0);
-    xr[j & 1][1] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s1);
-    xs[j & 1] = *reinterpret_cast<const float*>(l + so + j * 64);
+  auto read_x = [&](uint32_t buf, int j) __attribute__((always_inline)) {
+    const char* const l = lds + buf;
+    xr[j][0] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s0);
+    xr[j][1] = *reinterpret_cast<const uint4_t*>(l + xo + j * 16 * kF8Block + s1);
+    xs[j] = *reinterpret_cast<const float*>(l + so + j * 64);
   };
 
   float4_t ring[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
   float sr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](int t) {                  // result t of a block to its total
+  auto add = [&](int t) __attribute__((always_inline)) {  // result t of a block to its total
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       acc[t % TN][t / TN][e] = fmaf(ring[t & 3][e], sr[t & 3], acc[t % TN][t / TN][e]);
     // the total is formed here: put off, the results would not fit
     asm volatile("" : "+v"(acc[t % TN][t / TN]));
   };
+  uint32_t cb = 0;                         // buffer of the block
   auto step = [&](int b, auto inner) __attribute__((always_inline)) {
-    constexpr bool IN = decltype(inner)::value;          // two more blocks follow
+    constexpr bool IN = decltype(inner)::value;          // NB more blocks follow
     const float sw =
         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), (b - b0) & 63));
+    const uint32_t nb = cb + BUF == NB * BUF ? 0 : cb + BUF;
     Operand<EXACT> w[TN], x;
+    float s;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int i = t % TN, j = t / TN;
-      if (t == T - TN) {
-        // the next block has arrived, and this one's last operand is read
-        if constexpr (IN) vm_wait<WI>();
-        else vm_wait<0>();
+      if (t == TN) {
+        // every operand of this block is in registers, and the next has arrived
+        if constexpr (IN) vm_wait<(NB - 2) * L>();
+        else wait_blocks<L, NB - 2>(min(max(b1 - 2 - b, 0), NB - 2));
         lgkm_wait0();
         __builtin_amdgcn_sched_barrier(0);
         wg_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (t == TN) {
-        // every wave has this block's weights in registers
-        wg_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+      if (i == 0) {
+        x.set(xr[j][0], xr[j][1]);
+        s = xs[j] * sw;
       }
-      if (i == 0) x.set(xr[j & 1][0], xr[j & 1][1]);
       if (j == 0) w[i].set(wr[i][0], wr[i][1]);
       ring[t & 3] = block_sum(w[i], x);
-      sr[t & 3] = xs[j & 1] * sw;
+      sr[t & 3] = s;
       __builtin_amdgcn_sched_barrier(0);
       add((t + T - 3) % T);
-      if (i == 0) read_x(j + 1 < TM ? b : b + 1, (j + 1) % TM);
-      if (j == TM - 1) read_w(b + 1, i, !IN && (b + 2) * kF8Block > a.k);
-      if (IN) {
-        if (t >= TN && t - TN < WI) load(b + 2, t - TN);
-        if (t >= T - TN) {
+      // an operand's registers take the next block's after its last product
+      if (i == 0 && j > 0) read_x(nb, j - 1);
+      if (j == TM - 1) read_w(b + 1, nb, i, !IN && (b + 2) * kF8Block > a.k);
+      if (t == T - 1) read_x(nb, j);
+      if (IN && t >= TN) {
 #pragma unroll
-          for (int l = WI + t - (T - TN); l < L; l += TN) load(b + 2, l);
-        }
+        for (int l = t - TN; l < L; l += T - TN) load(b + NB, cb, l);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    cb = nb;
   };
-  swl = swr[min(b0 + lane, a.kb - 1)];
-  asm volatile("" : "+v"(swl));            // waited for before the direct loads
 #pragma unroll
-  for (int i = 0; i < L; ++i) load(b0, i);
-  if (b0 + 1 < b1) {
+  for (int d = 0; d < NB; ++d)
+    if (b0 + d < b1) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) load(b0 + 1, i);
-    vm_wait<L>();
-  } else {
-    vm_wait<0>();
-  }
+      for (int i = 0; i < L; ++i) load(b0 + d, d * BUF, i);
+    }
+  wait_blocks<L, NB - 1>(min(b1 - 1 - b0, NB - 1));
   wg_barrier();
-  read_x(b0, 0);
 #pragma unroll
-  for (int i = 0; i < TN; ++i) read_w(b0, i, (b0 + 1) * kF8Block > a.k);
+  for (int j = 0; j < TM; ++j) read_x(0, j);
+#pragma unroll
+  for (int i = 0; i < TN; ++i) read_w(b0, 0, i, (b0 + 1) * kF8Block > a.k);
+  auto scales = [&](int b) {
+    if (((b - b0) & 63) == 0 && b > b0) {
+      swl = swr[min(b + lane, a.kb - 1)];
+      asm volatile("" : "+v"(swl));        // waited for here, not in every block
+    }
+  };
   int b = b0;
-  for (; b + 2 < b1; ++b) {
-    if (((b - b0) & 63) == 0 && b > b0) swl = swr[min(b + lane, a.kb - 1)];
+  for (; b + NB < b1; ++b) {
+    scales(b);
     step(b, std::true_type{});
   }
   for (; b < b1; ++b) {
-    if (((b - b0) & 63) == 0 && b > b0) swl = swr[min(b + lane, a.kb - 1)];
+    scales(b);
     step(b, std::false_type{});
   }
   add(T - 3);
   add(T - 2);
   add(T - 1);
 
-  void* const out = a.part != nullptr ? a.part + (int64_t)blockIdx.y * a.m * a.n : a.y;
+  const int ns = n0 + wn * TN * 16 + kq * (EXACT ? 4 : 8), mst = m0 + wm * TM * 16 + nl;
+  const bool wide = (a.n & (EXACT ? 3 : 7)) == 0;
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    const int m = m0 + (wm * TM + j) * 16 + nl;
+    const int m = mst + j * 16;
+    if (m >= a.m) continue;
+    if (a.part != nullptr) {
+      float* const out = a.part + ((int64_t)blockIdx.y * a.m + m) * a.n;
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int n = n0 + (wn * TN + i) * 16 + kq * 4;
-      if (m < a.m && n < a.n) {
-        const int64_t o = (int64_t)m * a.n + n;
-        const bool wide = (a.n & 3) == 0;
-        if (a.part != nullptr) store4<WQ_F32>(out, o, acc[i][j], wide, a.n - n);
-        else store4<YDT>(out, o, acc[i][j], wide, a.n - n);
+      for (int i = 0; i < TN; ++i) {
+        const int n = ns + wrow(i);
+        if (n < a.n) store4<WQ_F32>(out, n, acc[i][j], (a.n & 3) == 0, a.n - n);
+      }
+    } else if (!EXACT && wide) {
+#pragma unroll
+      for (int i = 0; i < TN; i += 2)
+        if (ns + i * 16 < a.n)
+          *reinterpret_cast<uint4_t*>(static_cast<uint16_t*>(a.y) + (int64_t)m * a.n + ns +
+                                      i * 16) =
+              uint4_t{pack2<YDT>(acc[i][j][0], acc[i][j][1]),
+                      pack2<YDT>(acc[i][j][2], acc[i][j][3]),
+                      pack2<YDT>(acc[i + 1][j][0], acc[i + 1][j][1]),
+                      pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const int n = ns + wrow(i);
+        if (n < a.n)
+          store4<YDT>(a.y, (int64_t)m * a.n + n, acc[i][j], (a.n & 3) == 0, a.n - n);
       }
     }
   }
@@ -771,11 +794,10 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
   }
 }
 
-template <int YDT, int WN, int WM, int TN, int TM>
+template <int YDT, int TM, int NB>
 hipError_t gemm_launch(const Fp8Args& a, hipStream_t s) {
-  constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-  constexpr int bytes = 2 * fp8_buf_bytes<WN, WM, TN, TM>();
-  auto* kern = &fp8_gemm_kernel<YDT, WN, WM, TN, TM>;
+  constexpr int bytes = NB * fp8_buf_bytes<TM>();
+  auto* kern = &fp8_gemm_kernel<YDT, TM, NB>;
   static std::atomic<bool> ready{false};
   if (!ready.load(std::memory_order_acquire)) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -783,8 +805,8 @@ hipError_t gemm_launch(const Fp8Args& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     ready.store(true, std::memory_order_release);
   }
-  const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
-  kern<<<dim3((unsigned)(tm * tn), (unsigned)a.splits), WN * WM * 64, bytes, s>>>(a, tm, tn);
+  const int tm = (a.m + TM * 32 - 1) / (TM * 32), tn = (a.n + kTileN - 1) / kTileN;
+  kern<<<dim3((unsigned)(tm * tn), (unsigned)a.splits), 256, bytes, s>>>(a, tm, tn);
   return hipGetLastError();
 }
 
@@ -806,10 +828,12 @@ hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
     return few ? decode_launch<YDT, 8, 1, 4>(a, s) : decode_launch<YDT, 4, 2, 4>(a, s);
   }
   hipError_t e;
-  if constexpr (YDT != WQ_F32) {
-    if (p.tile == 2) return halves_launch<YDT>(a, p.full, s);
+  if constexpr (YDT == WQ_F32) {
+    e = gemm_launch<YDT, 4, 2>(a, s);
+  } else {
+    if (p.tile == 3) return halves_launch<YDT>(a, p.full, s);
+    e = p.tile == 1 ? gemm_launch<YDT, 2, 6>(a, s) : gemm_launch<YDT, 4, 2>(a, s);
   }
-  e = gemm_launch<YDT, 2, 2, 4, 4>(a, s);
   if (e != hipSuccess || a.part == nullptr) return e;
   const int64_t count = (int64_t)a.m * a.n;
   fp8_join_kernel<YDT><<<dim3((unsigned)((count + 1023) / 1024)), 256, 0, s>>>(a.part, a.splits,
@@ -819,29 +843,35 @@ hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
 
 }  // namespace
 
-Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k) {
+Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int ydt) {
   Fp8Plan p{};
   p.splits = 1;
   const int64_t kb = (k + kF8Block - 1) / kF8Block;
-  if (m <= 64) {
-    p.tile = 0;
-    return p;
-  }
-  const int64_t tm = (m + 255) / 256, tn = (n + 255) / 256, big = tm * tn;
-  p.tile = big > kCus / 4 ? 2 : 1;
-  // whole rounds of 256 x 256 tiles, then half tiles if they fill one round
-  p.full = (int)(big / kCus * kCus / tm);
-  if ((tn - p.full) * ((m + 127) / 128) > kCus) p.full = (int)tn;
-  if (p.tile == 1) {
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-    int64_t s = std::max<int64_t>(1, 512 / tiles);
+  if (m <= 64) return p;
+  const int64_t tn = (n + 127) / 128, t64 = (m + 63) / 64 * tn, t128 = (m + 127) / 128 * tn;
+  // One round of tiles if 256 workgroups hold them, the smaller the better:
+  // 512 tokens 4096 x 4096 20.0 us in 64 x 128 (tokens x features), 23.7 in
+  // 128 x 128 tiles; 1000 tokens 35.3 and 27.8 us.  Past that the large tiles
+  // (1536 tokens, 384 tiles of 128 x 128: 36 and 38 us).  The exact products
+  // are bound by converting the operands, which small tiles share less.
+  const bool exact = ydt == WQ_F32;
+  p.tile = !exact && t64 <= kCus ? 1 : exact || t128 <= kCus ? 2 : 3;
+  if (p.tile < 3) {
+    // few tiles: k in parts of at least four blocks
+    const int64_t tiles = p.tile == 1 ? t64 : t128;
+    int64_t s = std::max<int64_t>(1, kCus / tiles);
     s = std::min<int64_t>(s, std::max<int64_t>(1, kb / 4));
     while (s > 1 && s * m * n * 4 > ((int64_t)64 << 20)) --s;
     // no empty split
     const int64_t per = (kb + s - 1) / s;
     p.splits = (int)((kb + per - 1) / per);
+    p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
+  } else {
+    // whole rounds of 256 x 256 tiles, then half tiles if they fill one round
+    const int64_t tm = (m + 255) / 256, tc = (n + 255) / 256;
+    p.full = (int)(tm * tc / kCus * kCus / tm);
+    if ((tc - p.full) * ((m + 127) / 128) > kCus) p.full = (int)tc;
   }
-  p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
   return p;
 }
 

@@ -177,12 +177,13 @@ hipError_t launch_quantize_fp8_block(const uint16_t* w, int dt, int64_t n, int64
                                      float* scales, hipStream_t s);
 
 struct Fp8Plan {
-  int tile;          // 0 = decode (m <= 64), 1 = 128 x 128 tiles, 2 = 256 x 256
-  int full;          // tile 2, 16-bit y: columns of 256 features as 256 x 256 tiles
+  int tile;          // 0 = decode (m <= 64); tokens x features: 1 = 64 x 128,
+                     // 2 = 128 x 128, 3 = 256 x 256
+  int full;          // tile 3: columns of 256 features that whole tiles take
   int splits;        // parts of k summed by a second kernel (1 = none)
   size_t ws_bytes;   // their fp32 totals
 };
-Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k);
+Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int ydt);
 hipError_t launch_linear_fp8(const uint8_t* x, const float* sx, int64_t m, const wq_weight* w,
                              void* y, int ydt, const Fp8Plan& plan, float* part, hipStream_t s);
 

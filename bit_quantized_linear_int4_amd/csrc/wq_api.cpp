@@ -2,6 +2,7 @@
 //
 // Every check runs before the first HIP call, so an error other than
 // WQ_ERR_HIP means nothing was enqueued.  No C++ exception crosses the ABI.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -452,7 +453,9 @@ wq_status wq_quantize_fp8_block(const void* w, int32_t wdt, int64_t n, int64_t k
 size_t wq_linear_fp8_workspace(int64_t m, const wq_weight* w) {
   if (check_weight(w, false) != WQ_OK || w->fmt != WQ_FMT_FP8_BLOCK) return 0;
   if (!sizes_ok(m, w->k) || m > kMaxElems / w->n) return 0;
-  return plan_fp8(m, w->n, w->k).ws_bytes;
+  // enough for every type of y
+  return std::max(plan_fp8(m, w->n, w->k, WQ_F32).ws_bytes,
+                  plan_fp8(m, w->n, w->k, WQ_F16).ws_bytes);
 }
 
 wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_weight* w,
@@ -463,7 +466,7 @@ wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_
   if (w->fmt != WQ_FMT_FP8_BLOCK || !is_out(ydt)) return WQ_ERR_UNSUPPORTED;
   if (!sizes_ok(m, w->k) || m > kMaxElems / w->n) return WQ_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(y, 16)) return WQ_ERR_ALIGN;
-  const Fp8Plan plan = plan_fp8(m, w->n, w->k);
+  const Fp8Plan plan = plan_fp8(m, w->n, w->k, ydt);
   if (plan.ws_bytes > 0) {
     if (workspace == nullptr || ws_bytes < plan.ws_bytes) return WQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
