@@ -15,23 +15,28 @@
 // v_mfma_f32_16x16x32_bf16 per block, 1e-8 on the same codes, at half the
 // matrix rate.
 //
-// Operands:  The weights
-// are the A operand (16 output features), the activations the B operand (16
-// tokens): a lane then holds four consecutive features of ONE token, whose
-// scale product sx * sw is one value per lane and instruction group, and which
-// store as one 8- or 16-byte piece of a row of y.
+// Operands: the weights are the A operand (16 output features), the activations
+// the B operand (16 tokens): a lane then holds four consecutive features of ONE
+// token, whose scale product sx * sw is one value per lane and instruction
+// group, and which store as one piece of a row of y.
 //
 // Which bytes of a block a lane feeds into the K positions of the instruction
 // is free as long as both operands agree: lane group g = lane / 16 takes the
 // 16-byte chunks g and g + 4.
 //
-//  * decode (m <= 64): HBM-bound.  A workgroup owns 16 features over all of k;
-//    its waves take the blocks of k in turn and add their totals in LDS in a
-//    fixed order.
-//  * gemm: MFMA-bound.  Tiles of BN features x BM tokens, both operands staged
-//    128 bytes of k at a time by direct global -> LDS loads into two buffers,
-//    one barrier per block of k.  Where the tiles are too few to fill the GPU,
-//    k is split over workgroups whose fp32 totals a second kernel adds.
+// Four schedules, chosen in plan_fp8; all bring both operands into LDS by direct
+// loads, 128 bytes of k at a time:
+//  * decode, up to 64 tokens: bound by HBM (one token 14336 x 4000 5.5 TB/s).  A
+//    workgroup owns 16 features over all of k; its waves take the blocks of k in
+//    turn and add their totals in LDS in a fixed order.
+//  * tiles of 64 or 128 tokens x 128 features (fp8_gemm_kernel): bound by
+//    latency, the chain of a block's loads, operand reads and products (512
+//    tokens 4096 x 4096 19 us, of which the products are 4).  Where the tiles
+//    are too few to fill the GPU, k is split over workgroups whose fp32 totals
+//    a second kernel adds.
+//  * tiles of 256 x 256 (fp8_halves_kernel): bound by the matrix cores and by
+//    what their operands cost (4096 tokens 14336 x 4096 214 us, 2250 TFLOP/s; a
+//    library product without block scales 205 us).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -263,7 +268,7 @@ hipError_t decode_launch(const Fp8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// -------------------------------------------------------------------- gemm
+// ------------------------------------------------------------------- tiles
 // direct global -> LDS load with a uniform base, a 32-bit lane offset and a
 // uniform address in LDS
 __device__ __forceinline__ void lds_dma16_s(const void* base, uint32_t off, uint32_t lds) {
@@ -283,7 +288,20 @@ __device__ __forceinline__ void tile_of_block(int bid, int T, int tm, int tn, in
   in = w / gm;
 }
 
-// 2 x 2 waves, each 64 features x TM tiles of 16 tokens
+// 2 x 2 waves, each 64 features x TM tiles of 16 tokens.  A wave holds a whole
+// block's operands in registers and reads each one's successor from LDS right
+// after its last product, so one barrier per block, early in it, frees the
+// block's buffer for the loads of NB blocks later and finds the next block
+// arrived.  The scaled additions of a result wait until three more matrix
+// instructions are issued.
+//
+// Nothing between two blocks may make the compiler wait for all loads: a load of
+// scales under a branch without its own wait did, in every block, and cost more
+// than the products (512 tokens 4096 x 4096 24 us as split tiles, then 19).
+// Blocks in flight: 64 x 128 tiles take NB = 6 (150 KB, one workgroup per CU),
+// 128 x 128 tiles two with two workgroups per CU (1000 tokens 4096 x 4096 28.3
+// us, NB = 4 with one workgroup 27.8; the exact products, which need the second
+// wave to convert operands under the products, 41.8 and 44.2).
 constexpr int kTileN = 128;
 template <int TM>
 constexpr int fp8_buf_bytes() { return (kTileN + TM * 32) * kF8Block + TM * 32 * 4; }
@@ -500,7 +518,31 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int
   }
 }
 
-// ------------------------------------------------------- gemm in two halves
+// ------------------------------------------------------ tiles in two halves
+// 256 features x 32 TM tokens, 8 waves of 64 features x 16 TM tokens.  Waves 0-3
+// and 4-7 (one of each per SIMD) are half a step apart: while one half reads its
+// operands from LDS the other multiplies, and a barrier swaps them.  A step takes
+// a block of k in two parts: all weights and the first half of the tokens, then
+// the second half.  So the matrix cores always have a wave with all its operands
+// in registers, LDS reads and their latency hide under its products, and a wave
+// needs registers for half the tokens' operands only.
+//
+// LDS holds two blocks.  The weights, scales and first tokens of a block are read
+// in its first part, so their space takes the block after next from the second
+// part on; the other tokens' space follows in the next block's first part.  Every
+// load thus has about three parts to arrive, counted exactly (vm_wait), and
+// half of them are issued between products, where the load unit is idle.
+//
+// Workgroups are persistent (one per CU) and start the next tile's loads before
+// they store a tile, which goes past the caches: y would push the operands out of
+// L2.  The last round, if at most half the tiles are left, is made of tiles of
+// half the tokens.
+//
+// 4096 tokens 14336 x 4096, us: both halves in step, one barrier per block 294;
+// halves alternating 246; loads between products 228; wide stores 222; one
+// launch with persistent workgroups 217; stores past the caches 214.  Marginal
+// cost of a block per CU 1.37 us, 64 instructions per SIMD: 1.1 us at the 35
+// cycles that one takes with its additions.
 constexpr int kHalvesN = 256;
 constexpr int kCus = 256;
 template <int TM>
@@ -847,14 +889,18 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int ydt) {
   Fp8Plan p{};
   p.splits = 1;
   const int64_t kb = (k + kF8Block - 1) / kF8Block;
-  if (m <= 64) return p;
+  const bool exact = ydt == WQ_F32;
+  // Few tokens: the weights stream past them (tile 0).  From 33 tokens on that
+  // costs more than tiles once a CU has several of its workgroups: 64 tokens
+  // 8192 x 4096 14.0 us against 14.6 in tiles, 11008 x 4096 18.6 and 15.4,
+  // 14336 x 4096 24.1 and 17.7; fp32 y 22.8 and 24.4, 29.7 and 25.8.
+  if (m <= 32 || (m <= 64 && n <= (exact ? 12288 : 8192))) return p;
   const int64_t tn = (n + 127) / 128, t64 = (m + 63) / 64 * tn, t128 = (m + 127) / 128 * tn;
   // One round of tiles if 256 workgroups hold them, the smaller the better:
   // 512 tokens 4096 x 4096 20.0 us in 64 x 128 (tokens x features), 23.7 in
   // 128 x 128 tiles; 1000 tokens 35.3 and 27.8 us.  Past that the large tiles
   // (1536 tokens, 384 tiles of 128 x 128: 36 and 38 us).  The exact products
   // are bound by converting the operands, which small tiles share less.
-  const bool exact = ydt == WQ_F32;
   p.tile = !exact && t64 <= kCus ? 1 : exact || t128 <= kCus ? 2 : 3;
   if (p.tile < 3) {
     // few tiles: k in parts of at least four blocks

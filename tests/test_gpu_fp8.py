@@ -345,3 +345,25 @@ def test_linear_many_tiles(m, n, k):
     y[3] = linear(q, s, w, "bf16")[3]
     torch.cuda.synchronize()
     check_linear(y, q, s, w, "bf16")
+
+
+# tiles of 64 and of 128 tokens, whole and split over k, cut at every side
+@pytest.mark.parametrize("ydt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(40, 9001, 400), (64, 12301, 272), (65, 130, 2048),
+                                   (150, 1000, 4112), (300, 8000, 208), (1000, 4000, 1296)])
+def test_linear_tiles(m, n, k, ydt):
+    say(f"fp8 linear m={m} n={n} k={k} y={ydt}")
+    q, s, w = make_linear(m, n, k, 39)
+    y = linear(q, s, w, ydt)
+    torch.cuda.synchronize()
+    check_linear(y, q, s, w, ydt)
+    assert torch.equal(y, linear(q, s, w, ydt))
+
+
+def test_linear_more_blocks_than_a_wave_has_lanes():
+    """k of 70 blocks: the weight scales come 64 at a time."""
+    for m, ydt in ((100, "bf16"), (200, "f32"), (1, "f32"), (4100, "f16")):
+        q, s, w = make_linear(m, 4200 if m > 1000 else 136, 8832, 47)
+        y = linear(q, s, w, ydt)
+        torch.cuda.synchronize()
+        check_linear(y, q, s, w, ydt)
