@@ -856,18 +856,21 @@ template <int YDT>
 hipError_t fp8_ydt(Fp8Args a, const Fp8Plan& p, hipStream_t s) {
   if (p.tile == 0) {
     // 16 features per workgroup.  Up to 256 of them (n <= 4096) a CU holds one,
-    // which then needs all the waves it can have; with more, smaller
-    // workgroups leave room for several: one token 4096 x 4096 4.7 us with 16
+    // which then needs all the waves it can have; with more, several should fit
+    // a CU, whose LDS their rings share: one token 4096 x 4096 4.7 us with 16
     // waves, 5.1 with 8 (14336 rows: 10.5 and 10.3); 8 tokens 5.0 and 5.8; 16
-    // tokens 11008 x 4096 11.8 and 10.2; 64 tokens 4096 x 4096 8.4 with 8
-    // waves, 10.6 with 4, 11008 x 4096 17.9 and 16.6.  32 tokens 4096 x 4096
-    // 6.6 us, 11.8 as split tiles.
+    // tokens 11008 x 4096 11.8 and 10.2; 64 tokens 4096 x 4096 8.0 with 8, 8.7
+    // with 5 waves, 5000 x 4096 12.2 and 11.0.  The exact products convert every
+    // operand and want more waves: fp32 y 14336 x 4096 22.5 with 7, 26.8 with 5.
+    // 40 tokens as three tiles of 16 14336 x 4096 16.8, as four 17.7.
     const bool few = a.n <= 4096;
     if (a.m == 1) return decode_launch<YDT, 16, 2, 0>(a, s);
     if (a.m <= 16)
       return few ? decode_launch<YDT, 16, 2, 1>(a, s) : decode_launch<YDT, 8, 2, 1>(a, s);
     if (a.m <= 32) return decode_launch<YDT, 8, 1, 2>(a, s);
-    return few ? decode_launch<YDT, 8, 1, 4>(a, s) : decode_launch<YDT, 4, 2, 4>(a, s);
+    if (a.m <= 48) return decode_launch<YDT, 8, 1, 3>(a, s);
+    return few ? decode_launch<YDT, 8, 1, 4>(a, s)
+               : decode_launch<YDT, YDT == WQ_F32 ? 7 : 5, 1, 4>(a, s);
   }
   hipError_t e;
   if constexpr (YDT == WQ_F32) {
@@ -890,11 +893,12 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int ydt) {
   p.splits = 1;
   const int64_t kb = (k + kF8Block - 1) / kF8Block;
   const bool exact = ydt == WQ_F32;
-  // Few tokens: the weights stream past them (tile 0).  From 33 tokens on that
-  // costs more than tiles once a CU has several of its workgroups: 64 tokens
-  // 8192 x 4096 14.0 us against 14.6 in tiles, 11008 x 4096 18.6 and 15.4,
-  // 14336 x 4096 24.1 and 17.7; fp32 y 22.8 and 24.4, 29.7 and 25.8.
-  if (m <= 32 || (m <= 64 && n <= (exact ? 12288 : 8192))) return p;
+  // Few tokens: the weights stream past them (tile 0).  From 33 tokens on and
+  // with many features tiles take less, except where they convert operands: 40
+  // tokens 11008 x 4096 13.7 us against 14.6 in tiles, 14336 x 4096 16.8 and
+  // 16.3; 64 tokens 8192 x 4096 12.6 and 14.6, 14336 x 4096 20.0 and 17.8; fp32
+  // y 22.5 and 26.0.
+  if (m <= 32 || (m <= 64 && (exact || n <= (m <= 48 ? 12288 : 8192)))) return p;
   const int64_t tn = (n + 127) / 128, t64 = (m + 63) / 64 * tn, t128 = (m + 127) / 128 * tn;
   // One round of tiles if 256 workgroups hold them, the smaller the better:
   // 512 tokens 4096 x 4096 20.0 us in 64 x 128 (tokens x features), 23.7 in

@@ -349,7 +349,8 @@ def test_linear_many_tiles(m, n, k):
 
 # tiles of 64 and of 128 tokens, whole and split over k, cut at every side
 @pytest.mark.parametrize("ydt", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("m,n,k", [(40, 9001, 400), (64, 12301, 272), (65, 130, 2048),
+@pytest.mark.parametrize("m,n,k", [(40, 12301, 400), (64, 8201, 272), (33, 515, 1040),
+                                   (49, 4200, 656), (65, 130, 2048),
                                    (150, 1000, 4112), (300, 8000, 208), (1000, 4000, 1296)])
 def test_linear_tiles(m, n, k, ydt):
     say(f"fp8 linear m={m} n={n} k={k} y={ydt}")
