@@ -398,8 +398,8 @@ wq_status wq_quantize_fp8_block(const void* w, int32_t wdt, int64_t n, int64_t k
                                 float* scales, void* stream);
 
 /*
- * Scratch bytes of wq_linear_fp8 for this (m, weight) pair, at most 64 MiB:
- * fp32 totals of the parts k is split into where the output tiles alone do
+ * Scratch bytes of wq_linear_fp8 for this (m, weight) pair and any ydt, at most
+ * 64 MiB: fp32 totals of the parts k is split into where the output tiles alone do
  * not fill the GPU, 0 elsewhere (and for invalid arguments).
  */
 size_t wq_linear_fp8_workspace(int64_t m, const wq_weight* w);
@@ -407,9 +407,10 @@ size_t wq_linear_fp8_workspace(int64_t m, const wq_weight* w);
 /*
  * FP8 linear with block scales:
  *   y[i][j] = sum_b sx[b][i] * sw[j/128][b] * sum_{c in block b} q[i][c] * codes[j][c]
- * Every sum over a block of 128 is one matrix instruction into fp32; the
- * scaled sums are added in fp32, in an order fixed by the sizes (results are
- * deterministic), and rounded once to ydt.
+ * A sum over a block of 128 is formed by the FP8 matrix instructions, good to
+ * 2^-12 of the sum of its magnitudes, for a 16-bit y, and from exact products
+ * in fp32 for an fp32 y; the scaled sums are added in fp32, in an order fixed
+ * by the sizes (results are deterministic), and rounded once to ydt.
  * q: E4M3 [m][k], 16-byte aligned; scales fp32 [ceil(k/128)][m] (as
  * wq_add_rmsnorm and wq_quantize_fp8_rows write them); w: fmt FP8_BLOCK, any n;
  * y: ydt in {F16, BF16, F32} [m][n], 16-byte aligned.  workspace: at least
