@@ -532,53 +532,83 @@ def _rows(what, name, t):
     return m, k, ld
 
 
-def _fp8_rows(what, q, scales, m, k):
-    _dense(what, "q", q, m * k, (m, k))
-    _dense(what, "scales", scales, 4 * m * (-(-k // 128)), (-(-k // 128), m))
+# The operators below are called once per layer and token, where the host's time
+# counts: every check of a tensor is one call.
+def _need(what, name, t, shape, size, dev):
+    """`t` is contiguous, of `shape`, `size` bytes per element and on `dev`."""
+    if t is None or t.shape != shape or t.element_size() != size or not t.is_contiguous():
+        n = size
+        for d in shape:
+            n *= d
+        _dense(what, name, t, n, shape)              # says what differs
+    if t.get_device() != dev:
+        _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+
+
+def _like(what, name, t, shape, dtype, dev):
+    if t is None or t.shape != shape or not t.is_contiguous():
+        _dense(what, name, t, shape=shape)
+    if t.dtype != dtype:
+        _fail(what, f"{name} has dtype {t.dtype}, x {dtype}", _ERR_UNSUP)
+    if t.get_device() != dev:
+        _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+
+
+def _fp8_rows(what, q, scales, m, k, dev):
+    _need(what, "q", q, (m, k), 1, dev)
+    _need(what, "scales", scales, ((k + 127) // 128, m), 4, dev)
+
+
+def _device(what, t):
+    dev = t.get_device()                             # -1 for a CPU tensor
+    if dev < 0:
+        _fail(what, "tensors must be GPU tensors", _ERR_UNSUP)
+    return dev
 
 
 def wq_add_rmsnorm(x, gain, eps, residual=None, residual_out=None, y=None, q=None, scales=None,
                    stream=None):
     what = "wq_add_rmsnorm"
     m, k, ldx = _rows(what, "x", x)
-    dt = _dt(x)
-    ldr = k
-    _dense(what, "gain", gain, shape=(k,))
-    same = [("gain", gain)]
+    dt, dtype, ldr, r, ro = _dt(x), x.dtype, k, None, None
+    if dt == F32:
+        _fail(what, f"x has dtype {dtype}", _ERR_UNSUP)
+    dev = x.get_device()
+    _like(what, "gain", gain, (k,), dtype, dev)
     if residual is not None or residual_out is not None:
         mr, kr, ldr = _rows(what, "residual", residual)
         if (mr, kr) != (m, k) or _rows(what, "residual_out", residual_out) != (m, k, ldr):
             _fail(what, "residual and residual_out must have x's shape and equal strides")
-        same += [("residual", residual), ("residual_out", residual_out)]
+        if residual.dtype != dtype or residual_out.dtype != dtype:
+            _fail(what, f"residual and residual_out must be {dtype}, as x", _ERR_UNSUP)
+        if residual.get_device() != dev or residual_out.get_device() != dev:
+            _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+        r, ro = residual.data_ptr(), residual_out.data_ptr()
     if y is not None:
-        _dense(what, "y", y, shape=(m, k))
-        same.append(("y", y))
-    for name, t in same:
-        if t.dtype != x.dtype:
-            _fail(what, f"{name} has dtype {t.dtype}, x {x.dtype}", _ERR_UNSUP)
+        _like(what, "y", y, (m, k), dtype, dev)
     if q is not None or scales is not None:
-        _fp8_rows(what, q, scales, m, k)
+        _fp8_rows(what, q, scales, m, k, dev)
     elif y is None:
         _fail(what, "y or q is required")
-    _on_gpu(what, x, gain, residual, residual_out, y, q, scales)
-    st = _load().wq_add_rmsnorm(_ptr(x), dt, m, k, ldx, _ptr(residual), _ptr(residual_out), ldr,
-                                _ptr(gain), eps, _ptr(y), _ptr(q), _ptr(scales),
-                                _stream(stream, x))
-    _check(st, what)
+    _device(what, x)
+    st = _load().wq_add_rmsnorm(x.data_ptr(), dt, m, k, ldx, r, ro, ldr, gain.data_ptr(), eps,
+                                _ptr(y), _ptr(q), _ptr(scales), _stream(stream, x))
+    if st != 0:
+        _check(st, what)
 
 
 def wq_quantize_fp8_rows(x, q, scales, up=None, stream=None):
     what = "wq_quantize_fp8_rows"
     m, k = _matrix(what, "x", x)
+    dev = x.get_device()
     if up is not None:
-        _dense(what, "up", up, shape=(m, k))
-        if up.dtype != x.dtype:
-            _fail(what, f"up has dtype {up.dtype}, x {x.dtype}", _ERR_UNSUP)
-    _fp8_rows(what, q, scales, m, k)
-    _on_gpu(what, x, up, q, scales)
-    st = _load().wq_quantize_fp8_rows(_ptr(x), _ptr(up), _dt(x), m, k, _ptr(q), _ptr(scales),
-                                      _stream(stream, x))
-    _check(st, what)
+        _like(what, "up", up, (m, k), x.dtype, dev)
+    _fp8_rows(what, q, scales, m, k, dev)
+    _device(what, x)
+    st = _load().wq_quantize_fp8_rows(x.data_ptr(), _ptr(up), _dt(x), m, k, q.data_ptr(),
+                                      scales.data_ptr(), _stream(stream, x))
+    if st != 0:
+        _check(st, what)
 
 
 def wq_quantize_fp8_block(w, codes, scales, stream=None):
@@ -604,18 +634,21 @@ def wq_linear_fp8(q, scales, weight, y, workspace=None, stream=None):
     m, k = q.shape
     if k != weight.k:
         _fail(what, f"q has k={k}, the weight k={weight.k}")
-    _fp8_rows(what, q, scales, m, k)
+    dev = q.get_device()
+    _fp8_rows(what, q, scales, m, k, dev)
     wt = _weight_tensors(what, weight)
-    _dense(what, "y", y, shape=(m, weight.n))
-    ws_bytes = 0
+    ydt = _dt(y)
+    _need(what, "y", y, (m, weight.n), 4 if ydt == F32 else 2, dev)
+    ws, ws_bytes = None, 0
     if workspace is not None:
         _dense(what, "workspace", workspace)
-        ws_bytes = workspace.nbytes
-    _on_gpu(what, q, scales, y, workspace, *wt)
-    d = weight.descriptor()
-    st = _load().wq_linear_fp8(q.data_ptr(), scales.data_ptr(), m, ctypes.byref(d), y.data_ptr(),
-                               _dt(y), _ptr(workspace), ws_bytes, _stream(stream, q))
-    _check(st, what)
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _on_gpu(what, q, workspace, *wt)
+    st = _load().wq_linear_fp8(q.data_ptr(), scales.data_ptr(), m,
+                               ctypes.byref(weight.descriptor()), y.data_ptr(), ydt, ws, ws_bytes,
+                               _stream(stream, q))
+    if st != 0:
+        _check(st, what)
 
 
 def wq_moe_workspace(m, top_k, gate, experts):
