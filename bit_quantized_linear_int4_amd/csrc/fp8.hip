@@ -778,6 +778,8 @@ __device__ __forceinline__ void halves_tiles(const Fp8Args& a, char* lds) {
       }
     }
     if (!more) break;
+    // NS stores, one instruction each, are newer than the loads
+    asm volatile("" ::: "memory");
     if (whole && a.kb > 1) vm_wait<1 + XI + WI + NS>();
     else vm_wait<0>();
   }
