@@ -200,7 +200,8 @@ __global__ __launch_bounds__(NW * 64) void fp8_decode_kernel(Fp8Args a) {
     }
   };
   for (int i = 0; i < min(R, nb); ++i) issue(i);
-  const int s0 = nl * kF8Block + (kq ^ (nl & 7)) * 16, s1 = nl * kF8Block + ((kq + 4) ^ (nl & 7)) * 16;
+  const int s0 = nl * kF8Block + (kq ^ (nl & 7)) * 16;
+  const int s1 = nl * kF8Block + ((kq + 4) ^ (nl & 7)) * 16;
   float4_t acc[T];
 #pragma unroll
   for (int t = 0; t < T; ++t) acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -757,14 +758,15 @@ __device__ __forceinline__ void halves_tiles(const Fp8Args& a, char* lds) {
     if (whole) {
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const int64_t o = (int64_t)(mst + j * 16) * a.ld + ns;
+        uint16_t* const o = static_cast<uint16_t*>(a.y) + (int64_t)(mst + j * 16) * a.ld + ns;
 #pragma unroll
-        for (int i = 0; i < TN; i += 2)
-          __builtin_nontemporal_store(
-              (uint4_t{pack2<YDT>(acc[i][j][0], acc[i][j][1]),
-                      pack2<YDT>(acc[i][j][2], acc[i][j][3]),
-                      pack2<YDT>(acc[i + 1][j][0], acc[i + 1][j][1]),
-                      pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])}), reinterpret_cast<uint4_t*>(static_cast<uint16_t*>(a.y) + o + i * 16));
+        for (int i = 0; i < TN; i += 2) {
+          const uint4_t v = {pack2<YDT>(acc[i][j][0], acc[i][j][1]),
+                             pack2<YDT>(acc[i][j][2], acc[i][j][3]),
+                             pack2<YDT>(acc[i + 1][j][0], acc[i + 1][j][1]),
+                             pack2<YDT>(acc[i + 1][j][2], acc[i + 1][j][3])};
+          __builtin_nontemporal_store(v, reinterpret_cast<uint4_t*>(o + i * 16));
+        }
       }
     } else {
 #pragma unroll

@@ -12,10 +12,18 @@
 //                 walks units of 16 gate rows and the same 16 up rows of one
 //                 expert; its waves split k.  It stores
 //                 a = round16(p * silu(g) * u) for every token of the expert.
-//   3. down       a workgroup owns 16 rows of y over all active experts, whose
-//                 columns form one long k that its waves split; nothing leaves
-//                 the workgroup but y, and the order of the sum is fixed.
+//   3. down       a workgroup owns 16 or 32 rows of y over all active experts,
+//                 whose columns form one long k that its waves, and with more
+//                 than a few choices several workgroups, split; the order of
+//                 the sum is fixed.  Parts of k are added by a fourth launch.
 // The first workgroup of 2 leaves the routing (experts, rows, tokens) for 3.
+//
+// One MI355X, us: one token, 8 of 64 INT4 experts of 2048 x 1024 18.6 (25 MB, 5
+// at the rate of a copy; three dependent launches); 24 tokens, 6 of 64 FP8 84
+// (365 MB, 70); 64 tokens, 2 of 8 INT4 of 4096 x 14336 244 (735 MB, 142).  The
+// last is not bound by HBM: an expert with more than 16 tokens is read (in 2.
+// from L2) and unpacked twice, and a step (a tile, 16 tokens) of gate/up takes
+// the 3 us that its loads, one step ahead, need.
 //
 // The multiply runs on v_mfma_f32_16x16x32 with up to 16 tokens as the A
 // operand and 16 weight rows as the B operand.  INT4 codes are not rounded to
@@ -85,7 +93,7 @@ __device__ __forceinline__ float4_t mfma16(uint4_t a, uint4_t b, float4_t c) {
 // products, fp32 sums).  Bound by latency: every load of a wave is issued
 // before its first use for h up to 4096 (one memory round trip), with one wave
 // per expert and four tokens it was a chain of them (24 tokens, 64 experts,
-// h = 2048: 9.9 against 4.3 us; one token 5.4 against 4.2).
+// h = 2048: 9.9 against 4.6 us; one token 5.4 against 3.8).
 template <int XDT>
 __global__ __launch_bounds__(1024) void moe_router_kernel(MoeArgs a) {
   constexpr int NW = 16;
@@ -132,8 +140,10 @@ __global__ __launch_bounds__(1024) void moe_router_kernel(MoeArgs a) {
 // ----------------------------------------------------------------- routing
 __device__ __forceinline__ uint32_t max64(uint32_t v) {
   const int s = (int)max16(v);
-  return max(max((uint32_t)__builtin_amdgcn_readlane(s, 0), (uint32_t)__builtin_amdgcn_readlane(s, 16)),
-             max((uint32_t)__builtin_amdgcn_readlane(s, 32), (uint32_t)__builtin_amdgcn_readlane(s, 48)));
+  return max(max((uint32_t)__builtin_amdgcn_readlane(s, 0),
+                 (uint32_t)__builtin_amdgcn_readlane(s, 16)),
+             max((uint32_t)__builtin_amdgcn_readlane(s, 32),
+                 (uint32_t)__builtin_amdgcn_readlane(s, 48)));
 }
 
 // fp32 -> uint32 in the same order; NaN above everything, never 0, and -0
@@ -437,7 +447,8 @@ __device__ __forceinline__ uint4_t quarter_transpose(uint4_t v) {
 // [operand f][quarter kq][row][8 values], the 8 values in pair order for INT4.
 // One operand load of a wave is then cnt * 64 contiguous bytes, adjacent lanes
 // 16 bytes apart (with adjacent lanes on different lines a load takes four
-// times as long to address), and needs no reordering.  Element offset of value k of row j from the chunk's begin:
+// times as long to address), and needs no reordering.  Element offset of value
+// k of row j from the chunk's begin:
 template <int FMT, int S>
 __device__ __forceinline__ int64_t mid_offset(int k, int j, int cnt) {
   const int q = k & 127, e = k & 7;
@@ -962,12 +973,12 @@ constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK;
 // Parts of k in the down product with two row tiles per workgroup, as many as
 // fill the 256 CUs once, or 0: one row tile, all of k, no join.  Two tiles read
 // the intermediate once for both, which the L2 carries at several times the
-// codes' size: 64 tokens, 2 of 8 experts of 4096 x 14336 INT4 take 249 us (two
-// tiles, 2 parts), 262 (one tile), 322 (two tiles, one part); 24 tokens, 6 of
-// 64 FP8 experts of 2048 x 1024 94 us (two tiles, 4 parts) against 108.  For a
+// codes' size: 64 tokens, 2 of 8 experts of 4096 x 14336 INT4 take 244 us (two
+// tiles, 2 parts), 257 (one tile), 320 (two tiles, one part); 24 tokens, 6 of
+// 64 FP8 experts of 2048 x 1024 85 us (two tiles, 4 parts) against 98.  For a
 // few choices the join costs more than that gives: one token, 8 of 64 INT4
-// experts, 24.6 us with one tile, 25.4 with two in 4 parts; 4 tokens 46.7
-// against 41.4.
+// experts, 18.9 us with one tile, 20.5 with two in 4 parts; 4 tokens 39.2
+// against 34.9.
 int down_parts(int64_t t, int64_t top_k, int64_t h) {
   return t * top_k <= 8 ? 0 : (int)std::max<int64_t>(1, 256 * 32 / h);
 }
@@ -1002,8 +1013,10 @@ hipError_t moe_fmt(const MoeArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // 8 waves and two workgroups per CU where they cover k in one pass, else 16
-  // waves and one
+  // 8 waves and two workgroups per CU, which are seldom at the same point of a
+  // step, where they cover k in one pass; else 16 waves and one: 16 tokens, 8 of
+  // 64 INT4 experts, h = 2048, 62.8 us with 8 waves, 75.4 with 16; 64 tokens, 2
+  // of 8, h = 4096, 365 with 8 (two passes), 244 with 16
   const int64_t units = (int64_t)std::min(a.e, a.t * a.top_k) * (a.i / 16);
   if (a.h <= 8 * 256) {
     const unsigned grid = (unsigned)std::min<int64_t>(units, 512);
