@@ -173,15 +173,15 @@ struct Routing {
 // expert (logit -inf) has probability 0 and comes last; with every expert
 // masked all probabilities are 0.  A NaN or +inf logit makes the token's
 // probabilities NaN; the ids stay valid.
+// Lane l holds logits l, l + 64, ...
 template <int R>
-__device__ __forceinline__ void top_k_of(const float* l, int e, int top_k, int renorm, int lane,
-                                         int& id, float& prob) {
+__device__ __forceinline__ void top_k_of(const float (&l)[R], int e, int top_k, int renorm,
+                                         int lane, int& id, float& prob) {
   uint32_t key[R];
   uint32_t best = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int j = lane + 64 * r;
-    key[r] = j < e ? order_key(l[j]) : 0u;
+    key[r] = lane + 64 * r < e ? order_key(l[r]) : 0u;
     best = max(best, key[r]);
   }
   best = max64(best);
@@ -218,11 +218,36 @@ __device__ __forceinline__ void top_k_of(const float* l, int e, int top_k, int r
   prob = __float_as_uint(top) == 0xFF800000u ? 0.0f : __fdiv_rn(prob, total);
 }
 
-__device__ __forceinline__ void top_k_any(const MoeArgs& a, int t, int lane, int& id, float& p) {
-  const float* l = a.logits + (int64_t)t * a.e;
-  if (a.e <= 64) top_k_of<1>(l, a.e, a.top_k, a.renorm, lane, id, p);
-  else if (a.e <= 256) top_k_of<4>(l, a.e, a.top_k, a.renorm, lane, id, p);
-  else top_k_of<kMaxE / 64>(l, a.e, a.top_k, a.renorm, lane, id, p);
+// The top_k of tokens wave, wave + NW, ... into `r`, the next one's logits loaded
+// while one is sorted; lane j gets choice j of the last.
+template <int NW, int R>
+__device__ __forceinline__ void top_k_all(const MoeArgs& a, Routing& r, int wave, int lane,
+                                          int& id, float& p) {
+  auto load = [&](int t, float (&l)[R]) {
+    const float* const row = a.logits + (int64_t)min(t, a.t - 1) * a.e;
+#pragma unroll
+    for (int i = 0; i < R; ++i) l[i] = row[min(lane + 64 * i, a.e - 1)];
+  };
+  float l[R];
+  load(wave, l);
+  for (int t = wave; t < a.t; t += NW) {
+    float next[R];
+    load(t + NW, next);
+    top_k_of<R>(l, a.e, a.top_k, a.renorm, lane, id, p);
+    if (lane < a.top_k) {
+      r.ids[t * a.top_k + lane] = id;
+      r.probs[t * a.top_k + lane] = p;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) l[i] = next[i];
+  }
+}
+template <int NW>
+__device__ __forceinline__ void top_k_any(const MoeArgs& a, Routing& r, int wave, int lane,
+                                          int& id, float& p) {
+  if (a.e <= 64) top_k_all<NW, 1>(a, r, wave, lane, id, p);
+  else if (a.e <= 256) top_k_all<NW, 4>(a, r, wave, lane, id, p);
+  else top_k_all<NW, kMaxE / 64>(a, r, wave, lane, id, p);
 }
 
 // Fills `r` for all tokens; every thread of the workgroup calls it.
@@ -234,16 +259,12 @@ __device__ void route(const MoeArgs& a, Routing& r) {
     // one token: each choice is an expert with that token, nothing to sort
     // (one token, 8 of 64 experts: this and the sums cost 3.2 us by the way below)
     if (wave == 0) {
-      int id;
-      float p;
-      top_k_any(a, 0, lane, id, p);
+      int id = 0;
+      float p = 0.0f;
+      top_k_any<NW>(a, r, 0, lane, id, p);
       const bool on = lane < a.top_k && p != 0.0f;
       const uint64_t live = __ballot(on);
       const int at = __popcll(live & ((1ull << lane) - 1));
-      if (lane < a.top_k) {
-        r.ids[lane] = id;
-        r.probs[lane] = p;
-      }
       if (on) {
         r.act[at] = Active{id, at, 1, at};
         r.act_of[at] = (uint16_t)at;
@@ -256,15 +277,9 @@ __device__ void route(const MoeArgs& a, Routing& r) {
     return;
   }
   for (int i = tid; i < a.e; i += NW * 64) r.mask[i][0] = r.mask[i][1] = 0;
-  for (int t = wave; t < a.t; t += NW) {
-    int id;
-    float p;
-    top_k_any(a, t, lane, id, p);
-    if (lane < a.top_k) {
-      r.ids[t * a.top_k + lane] = id;
-      r.probs[t * a.top_k + lane] = p;
-    }
-  }
+  int id;
+  float p;
+  top_k_any<NW>(a, r, wave, lane, id, p);
   __syncthreads();
   const int picks = a.t * a.top_k;
   for (int i = tid; i < picks; i += NW * 64) {
