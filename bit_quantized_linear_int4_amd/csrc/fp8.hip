@@ -821,15 +821,25 @@ hipError_t halves_launch(const Fp8Args& a, int f, hipStream_t s) {
   return hipGetLastError();
 }
 
-// y = the sum of the splits' totals, in their order
+// y = the sum of the splits' totals, in their order; four are loaded before the
+// first is added, so their latencies do not add up
 template <int YDT>
 __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ part, int splits,
                                                        int64_t count, void* y) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= count) return;
   if (i + 4 <= count && (count & 3) == 0) {
-    float4_t t = *reinterpret_cast<const float4_t*>(part + i);
-    for (int s = 1; s < splits; ++s) t += *reinterpret_cast<const float4_t*>(part + s * count + i);
+    float4_t t = {0.0f, 0.0f, 0.0f, 0.0f};
+    int s = 0;
+    for (; s + 4 <= splits; s += 4) {
+      float4_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = *reinterpret_cast<const float4_t*>(part + (s + j) * count + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t += v[j];
+    }
+    for (; s < splits; ++s) t += *reinterpret_cast<const float4_t*>(part + s * count + i);
     store4<YDT>(y, i, t, true, 4);
   } else {
     for (int64_t e = i; e < min(i + 4, count); ++e) {

@@ -972,13 +972,22 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   }
 }
 
-// y = the sum of the parts, in their order
+// y = the sum of the parts, in their order; four are loaded before the first is
+// added, so their latencies do not add up
 __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__ part, int parts,
                                                        int count, void* y, int ydt) {
   const int i = (int)blockIdx.x * 256 + (int)threadIdx.x;
   if (i >= count) return;
-  float v = part[i];
-  for (int p = 1; p < parts; ++p) v += part[(int64_t)p * count + i];
+  float v = 0.0f;
+  int p = 0;
+  for (; p + 4 <= parts; p += 4) {
+    float t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = part[(int64_t)(p + j) * count + i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v += t[j];
+  }
+  for (; p < parts; ++p) v += part[(int64_t)p * count + i];
   store_as(y, ydt, i, v);
 }
 
