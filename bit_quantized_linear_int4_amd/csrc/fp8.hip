@@ -87,17 +87,19 @@ struct Operand<false> {
 template <>
 struct Operand<true> {
   uint4_t v[4];
+  __device__ __forceinline__ void piece(int f, uint4_t a, uint4_t b) {
+    const uint32_t c[2] = {f < 2 ? a[2 * f] : b[2 * f - 4], f < 2 ? a[2 * f + 1] : b[2 * f - 3]};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t lo, hi;
+      fp8_to_bf16(c[i], lo, hi);
+      v[f][2 * i] = lo;
+      v[f][2 * i + 1] = hi;
+    }
+  }
   __device__ __forceinline__ void set(uint4_t a, uint4_t b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t lo, hi;
-      fp8_to_bf16(a[i], lo, hi);
-      v[i >> 1][2 * (i & 1)] = lo;
-      v[i >> 1][2 * (i & 1) + 1] = hi;
-      fp8_to_bf16(b[i], lo, hi);
-      v[2 + (i >> 1)][2 * (i & 1)] = lo;
-      v[2 + (i >> 1)][2 * (i & 1) + 1] = hi;
-    }
+    for (int f = 0; f < 4; ++f) piece(f, a, b);
   }
 };
 
@@ -414,12 +416,12 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int
     asm volatile("" : "+v"(acc[t % TN][t / TN]));
   };
   uint32_t cb = 0;                         // buffer of the block
+  Operand<EXACT> w[TN], x[2];
   auto step = [&](int b, auto inner) __attribute__((always_inline)) {
     constexpr bool IN = decltype(inner)::value;          // NB more blocks follow
     const float sw =
         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(swl), (b - b0) & 63));
     const uint32_t nb = cb + BUF == NB * BUF ? 0 : cb + BUF;
-    Operand<EXACT> w[TN], x;
     float s;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
@@ -433,14 +435,20 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int
         wg_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (i == 0) {
-        x.set(xr[j][0], xr[j][1]);
-        s = xs[j] * sw;
+      if (i == 0) s = xs[j] * sw;
+      if constexpr (EXACT) {
+        // the conversions of the next operands run under the products
+        ring[t & 3] = block_sum(w[i], x[j & 1]);
+        x[(j + 1) & 1].piece(i, xr[(j + 1) % TM][0], xr[(j + 1) % TM][1]);
+        if (j == 0 && i + 1 < TN) w[i + 1].set(wr[i + 1][0], wr[i + 1][1]);
+        if (t == T - 1) w[0].set(wr[0][0], wr[0][1]);
+      } else {
+        if (i == 0) x[0].set(xr[j][0], xr[j][1]);
+        if (j == 0) w[i].set(wr[i][0], wr[i][1]);
+        ring[t & 3] = block_sum(w[i], x[0]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (j == 0) w[i].set(wr[i][0], wr[i][1]);
-      ring[t & 3] = block_sum(w[i], x);
       sr[t & 3] = s;
-      __builtin_amdgcn_sched_barrier(0);
       add((t + T - 3) % T);
       // an operand's registers take the next block's after its last product
       if (i == 0 && j > 0) read_x(nb, j - 1);
@@ -466,6 +474,10 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8Args a, int tm, int
   for (int j = 0; j < TM; ++j) read_x(0, j);
 #pragma unroll
   for (int i = 0; i < TN; ++i) read_w(b0, 0, i, (b0 + 1) * kF8Block > a.k);
+  if constexpr (EXACT) {
+    x[0].set(xr[0][0], xr[0][1]);
+    w[0].set(wr[0][0], wr[0][1]);
+  }
   auto scales = [&](int b) {
     if (((b - b0) & 63) == 0 && b > b0) {
       swl = swr[min(b + lane, a.kb - 1)];
