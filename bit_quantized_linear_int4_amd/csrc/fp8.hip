@@ -260,13 +260,9 @@ hipError_t decode_launch(const Fp8Args& a, hipStream_t s) {
   constexpr int bytes = NW * R * decode_slot_bytes<MT>();
   static_assert(bytes >= NW * (MT == 0 ? 1 : MT) * 1024 && NW >= MT, "room for the totals");
   auto* kern = &fp8_decode_kernel<YDT, NW, R, MT>;
-  static std::atomic<bool> ready{false};
-  if (!ready.load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    ready.store(true, std::memory_order_release);
-  }
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), bytes, done);
+  if (e != hipSuccess) return e;
   kern<<<dim3((unsigned)((a.n + 15) / 16)), NW * 64, bytes, s>>>(a);
   return hipGetLastError();
 }
@@ -822,13 +818,9 @@ template <int YDT>
 hipError_t halves_launch(const Fp8Args& a, int f, hipStream_t s) {
   constexpr int bytes = 2 * halves_buf_bytes<8>();
   auto* kern = &fp8_halves_kernel<YDT>;
-  static std::atomic<bool> ready{false};
-  if (!ready.load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    ready.store(true, std::memory_order_release);
-  }
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), bytes, done);
+  if (e != hipSuccess) return e;
   kern<<<kCus, 512, bytes, s>>>(a, f);
   return hipGetLastError();
 }
@@ -866,13 +858,9 @@ template <int YDT, int TM, int NB>
 hipError_t gemm_launch(const Fp8Args& a, hipStream_t s) {
   constexpr int bytes = NB * fp8_buf_bytes<TM>();
   auto* kern = &fp8_gemm_kernel<YDT, TM, NB>;
-  static std::atomic<bool> ready{false};
-  if (!ready.load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    ready.store(true, std::memory_order_release);
-  }
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), bytes, done);
+  if (e != hipSuccess) return e;
   const int tm = (a.m + TM * 32 - 1) / (TM * 32), tn = (a.n + kTileN - 1) / kTileN;
   kern<<<dim3((unsigned)(tm * tn), (unsigned)a.splits), 256, bytes, s>>>(a, tm, tn);
   return hipGetLastError();

@@ -2,6 +2,8 @@
 // vector access, E4M3 scales and conversions, reductions inside a wave.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace wq {
@@ -132,6 +134,19 @@ __device__ __forceinline__ float sum64(float v) {
           __int_as_float(__builtin_amdgcn_readlane(s, 16))) +
          (__int_as_float(__builtin_amdgcn_readlane(s, 32)) +
           __int_as_float(__builtin_amdgcn_readlane(s, 48)));
+}
+
+// Lets `kern` take `bytes` of dynamic LDS on the current device, once per device
+// and kernel (`done`: a bit per device).
+inline hipError_t allow_lds(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return hipSuccess;
+  e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // v / (1 + exp(-v)) with the hardware exponential and reciprocal (about 1e-6

@@ -1012,16 +1012,12 @@ hipError_t down_launch(const MoeArgs& a, int parts, hipStream_t s) {
   constexpr int NW = 16;
   constexpr int most = kDownTables + NW * kMaxT * 64 * RT;
   auto* kern = &moe_down_kernel<XDT, FMT, S, NW, RT>;
-  static std::atomic<bool> ready{false};
-  if (!ready.load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != hipSuccess) return e;
-    ready.store(true, std::memory_order_release);
-  }
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), most, done);
+  if (e != hipSuccess) return e;
   const int bytes = kDownTables + NW * a.t * 64 * RT;
   kern<<<dim3((unsigned)(a.h / (16 * RT)), (unsigned)parts), NW * 64, bytes, s>>>(a);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || parts == 1) return e;
   const int count = a.t * a.h;
   moe_join_kernel<<<dim3((unsigned)((count + 255) / 256)), 256, 0, s>>>(a.part, parts, count, a.y,
