@@ -236,3 +236,18 @@ def test_stream_and_graph():
             assert torch.equal(y, ref)
             x2 = x * 2
             st.synchronize()
+
+
+# k past what 8 waves, and past what 16 waves, hold in one pass; a long k of the
+# down product; one token, some and more than a chunk of an expert
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("t,e,top_k,h,i", [(1, 3, 2, 2304, 128), (20, 2, 1, 2176, 256),
+                                           (1, 2, 2, 4224, 128), (5, 3, 2, 8320, 128),
+                                           (40, 2, 2, 128, 4224)])
+def test_long_k(t, e, top_k, h, i, fmt, group):
+    say(f"moe t={t} e={e} k={top_k} h={h} i={i} {fmt} g{group}")
+    ex = Experts(e, h, i, fmt, group, 90)
+    x = rand((t, h), 91, "bf16", 0.5).cuda()
+    logits = rand((t, e), 92, "f32", 2.0)
+    got = run(x, ex, top_k, logits=logits.cuda(), ydt="f32")
+    check(x, ex, logits.double().numpy(), top_k, "bf16", got, True, "f32")
