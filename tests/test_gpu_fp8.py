@@ -368,3 +368,24 @@ def test_linear_more_blocks_than_a_wave_has_lanes():
         y = linear(q, s, w, ydt)
         torch.cuda.synchronize()
         check_linear(y, q, s, w, ydt)
+
+
+# rows of every workgroup size, few and many of them
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,k", [(3, 512), (3, 1544), (600, 1544), (513, 2600), (515, 8000),
+                                 (514, 4104), (512, 4096), (2, 8192), (520, 9000)])
+def test_norm_sizes(m, k, dtype):
+    say(f"norm m={m} k={k} {dtype}")
+    x, r = rand((m, k), 51, dtype, outliers=2).cuda(), rand((m, k), 52, dtype, 3.0).cuda()
+    g = (1 + 0.2 * rand((k,), 53, "f32")).to(TD[dtype]).cuda()
+    tol = (k / 256 + 40) * 2.0 ** -24
+    out, y = torch.empty_like(x), torch.empty_like(x)
+    q, s = wq.alloc_fp8_rows(m, k)
+    wq.wq_add_rmsnorm(x, g, 1e-5, residual=r, residual_out=out, y=y, q=q, scales=s)
+    torch.cuda.synchronize()
+    _, v = fp8.add_rmsnorm(x.double().cpu().numpy(), g.double().cpu().numpy(), 1e-5,
+                           r.double().cpu().numpy())
+    assert torch.equal(out, (x.float() + r.float()).to(x.dtype))
+    err = np.abs(y.double().cpu().numpy() - v)
+    assert np.all(err <= (ULP[dtype] * (1 + 1e-3) + tol) * np.abs(v) + TINY[dtype])
+    check_codes(q, s, v, tol)
