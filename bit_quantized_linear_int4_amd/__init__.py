@@ -576,9 +576,12 @@ def wq_add_rmsnorm(x, gain, eps, residual=None, residual_out=None, y=None, q=Non
     dev = x.get_device()
     _like(what, "gain", gain, (k,), dtype, dev)
     if residual is not None or residual_out is not None:
-        mr, kr, ldr = _rows(what, "residual", residual)
-        if (mr, kr) != (m, k) or _rows(what, "residual_out", residual_out) != (m, k, ldr):
-            _fail(what, "residual and residual_out must have x's shape and equal strides")
+        if not (residual is not None and residual_out is not None
+                and residual.shape == x.shape and residual_out.shape == x.shape
+                and residual.is_contiguous() and residual_out.is_contiguous()):
+            mr, kr, ldr = _rows(what, "residual", residual)
+            if (mr, kr) != (m, k) or _rows(what, "residual_out", residual_out) != (m, k, ldr):
+                _fail(what, "residual and residual_out must have x's shape and equal strides")
         if residual.dtype != dtype or residual_out.dtype != dtype:
             _fail(what, f"residual and residual_out must be {dtype}, as x", _ERR_UNSUP)
         if residual.get_device() != dev or residual_out.get_device() != dev:
