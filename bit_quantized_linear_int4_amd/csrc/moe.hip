@@ -11,12 +11,15 @@
 //                 (a few hundred logits: cheaper than one more launch), then
 //                 walks units of 16 gate rows and the same 16 up rows of one
 //                 expert; its waves split k.  It stores
-//                 a = round16(p * silu(g) * u) for every token of the expert.
+//                 a = round16(silu(g) * u) for every token of the expert.
 //   3. down       a workgroup owns 16 or 32 rows of y over all active experts,
 //                 whose columns form one long k that its waves, and with more
 //                 than a few choices several workgroups, split; the order of
 //                 the sum is fixed.  Parts of k are added by a fourth launch.
-// The first workgroup of 2 leaves the routing (experts, rows, tokens) for 3.
+// The first workgroup of 2 leaves the routing (experts, rows, tokens, their p)
+// for 3, which multiplies an expert's sums by p in fp32: a share of one in
+// several hundred experts, multiplied in before the rounding to fp16, would
+// push a among the subnormals and cost most of its bits.
 //
 // One MI355X, us: one token, 8 of 64 INT4 experts of 2048 x 1024 18.6 (25 MB, 5
 // at the rate of a copy; three dependent launches); 24 tokens, 6 of 64 FP8 84
@@ -64,6 +67,7 @@ struct MoeArgs {
   int32_t* count;            // of chunks
   Chunk* table;
   uint8_t* slot_tok;         // [t * top_k] token of a row of the intermediate
+  float* slot_prob;          // [t * top_k] and its p
   uint16_t* mid;             // [t * top_k][i]
   float* part;               // [parts][t][h]
   void* y;                   // [t][h]
@@ -607,6 +611,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
     if (tid == 0) *a.count = r.chunks;
     for (int i = tid; i < a.t * a.top_k; i += NW * 64) {
       a.slot_tok[i] = r.slot_tok[i];
+      a.slot_prob[i] = r.slot_prob[i];
       if (a.ids != nullptr) a.ids[i] = r.ids[i];
       if (a.probs != nullptr) a.probs[i] = r.probs[i];
     }
@@ -789,7 +794,7 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
           const int sl = cur.slot + c0;
           a.mid[(int64_t)sl * a.i +
                 mid_offset<FMT, S>(cur.tile * 16 + n, j, min(16, cur.cnt - c0))] =
-              (uint16_t)pack2<XDT>(silu(g) * v * r.slot_prob[sl + j], 0.0f);
+              (uint16_t)pack2<XDT>(silu(g) * v, 0.0f);
         }
       }
       rflip ^= 1;
@@ -813,8 +818,8 @@ __global__ __launch_bounds__(NW * 64, 4) void moe_gate_up_kernel(MoeArgs a, int 
 // 16 tokens of one expert) form one k of chunks * i values, in groups of R
 // units; its gridDim.y parts go to as many workgroups, and of a part each wave
 // takes a contiguous piece.  A wave's sums over one chunk (a row of the MFMA
-// result per token) go into the wave's own rows of y in LDS when the chunk
-// ends, so no two waves touch the same value and the order is fixed.  R units
+// result per token), times the token's p, go into the wave's own rows of y in
+// LDS when the chunk ends, so no two waves touch the same value and the order is fixed.  R units
 // per wave are in flight, and 16 waves share the CU.
 //
 // INT4: one load of scales and one of zero points serves the R x RT units of a
@@ -827,7 +832,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   extern __shared__ uint4_t dsm[];
   Chunk* const chunk = reinterpret_cast<Chunk*>(dsm);                  // [kMaxChunks]
   uint8_t* const tok = reinterpret_cast<uint8_t*>(chunk + kMaxChunks); // [kMaxT * kMaxK]
-  float* const ys = reinterpret_cast<float*>(tok + kMaxT * kMaxK);     // [NW][t][16 RT]
+  float* const prob = reinterpret_cast<float*>(tok + kMaxT * kMaxK);   // [kMaxT * kMaxK]
+  float* const ys = prob + kMaxT * kMaxK;                              // [NW][t][16 RT]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
@@ -836,7 +842,10 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
   const int most = min(a.e, a.t * a.top_k) + a.t * a.top_k / 16;
   for (int i = tid; i < most; i += NW * 64) chunk[i] = a.table[i];
   const int chunks = *a.count;
-  for (int i = tid; i < a.t * a.top_k; i += NW * 64) tok[i] = a.slot_tok[i];
+  for (int i = tid; i < a.t * a.top_k; i += NW * 64) {
+    tok[i] = a.slot_tok[i];
+    prob[i] = a.slot_prob[i];
+  }
   for (int i = tid; i < NW * a.t * 16 * RT; i += NW * 64) ys[i] = 0.0f;
   __syncthreads();
   const int ku = a.i >> 7, kg = (ku + R - 1) / R, n0 = (int)blockIdx.x * 16 * RT;
@@ -907,14 +916,17 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a) {
     for (int r = 0; r < RT; ++r) acc[r] = float4_t{0, 0, 0, 0};
     auto flush = [&](const Pos& p) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int e = 0; e < 4; ++e) {
+        const int j = 4 * kq + e;
+        if (j < p.cnt) {
+          float* const o = yw + tok[p.slot + j] * RT * 16 + nl;
+          const float pr = prob[p.slot + j];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 4 * kq + e;
-          if (j < p.cnt) yw[(tok[p.slot + j] * RT + r) * 16 + nl] += acc[r][e];
+          for (int r = 0; r < RT; ++r) o[r * 16] = fmaf(acc[r][e], pr, o[r * 16]);
         }
-        acc[r] = float4_t{0, 0, 0, 0};
       }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = float4_t{0, 0, 0, 0};
     };
     Unit<FMT> w[R][RT];
     Acts x[R];
@@ -992,7 +1004,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float* __restrict__
 }
 
 // ------------------------------------------------------------------ launch
-constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK;
+constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK * 5;
 
 // Parts of k in the down product with two row tiles per workgroup, as many as
 // fill the 256 CUs once, or 0: one row tile, all of k, no join.  Two tiles read
@@ -1065,10 +1077,10 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
 
-// workspace: logits fp32 [t][e] | count | table | token of each row |
+// workspace: logits fp32 [t][e] | count | table | token of each row | its p |
 // intermediate [t * top_k][i] | parts of y fp32 [parts][t][h]
 size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t h, int64_t i) {
-  return up256((size_t)(t * e) * 4) + 256 + up256(kMaxChunks * sizeof(Chunk)) + kMaxT * kMaxK +
+  return up256((size_t)(t * e) * 4) + 256 + up256(kMaxChunks * sizeof(Chunk)) + kMaxT * kMaxK * 5 +
          up256((size_t)(t * top_k * i) * 2) + (size_t)down_parts(t, top_k, h) * t * h * 4;
 }
 
@@ -1088,6 +1100,8 @@ hipError_t launch_moe(const MoeCall& c, hipStream_t s) {
   p += up256(kMaxChunks * sizeof(Chunk));
   a.slot_tok = reinterpret_cast<uint8_t*>(p);
   p += kMaxT * kMaxK;
+  a.slot_prob = reinterpret_cast<float*>(p);
+  p += kMaxT * kMaxK * 4;
   a.mid = reinterpret_cast<uint16_t*>(p);
   p += up256((size_t)(c.t * c.top_k * c.i) * 2);
   a.part = reinterpret_cast<float*>(p);

@@ -425,9 +425,10 @@ wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_
  *   l = x . router^T (fp32), or the caller's `logits`
  *   p = softmax(l); the top_k experts of the largest l, ties to the lowest
  *   index; renormalize != 0: their p divided by their sum
- *   a = round16(p_j * silu(x . gate_e^T) * (x . up_e^T))
- *   y = sum_j a . down_e^T
- * with fp32 sums; a is rounded to xdt (as any 16-bit model keeps it), y to ydt.
+ *   a = round16(silu(x . gate_e^T) * (x . up_e^T))
+ *   y = sum_j p_j * (a . down_e^T)
+ * with fp32 sums; a is rounded to xdt (as any 16-bit model keeps it: in fp16 it
+ * is infinite from 65520 on), y to ydt.
  * The order of every sum is fixed by the sizes and the routing: results are
  * deterministic.  INT4 weights enter as (q - z) * s, unrounded.
  *

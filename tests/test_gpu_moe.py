@@ -251,3 +251,52 @@ def test_long_k(t, e, top_k, h, i, fmt, group):
     logits = rand((t, e), 92, "f32", 2.0)
     got = run(x, ex, top_k, logits=logits.cuda(), ydt="f32")
     check(x, ex, logits.double().numpy(), top_k, "bf16", got, True, "f32")
+
+
+def spread_bound(x, ids, probs, ex, xdt):
+    """How far y may be off before its own rounding when the gated product is
+    rounded by itself and its share multiplies the sums: every term, the half
+    subnormal step of the intermediate too, comes times p."""
+    x64 = x.double().cpu().numpy()
+    out = np.zeros((x64.shape[0], ex.h))
+    cg, cd = (32 + ex.h / 128) * 2.0 ** -24, (32 + 16 * ex.i / 128) * 2.0 ** -24
+    for t in range(out.shape[0]):
+        for e, p in zip(ids[t], probs[t]):
+            if p == 0:
+                continue
+            g, u = ex.val[0][e] @ x64[t], ex.val[1][e] @ x64[t]
+            dg, du = (cg * (ex.mag[j][e] @ np.abs(x64[t])) for j in (0, 1))
+            sl = g / (1 + np.exp(-g))
+            a = np.abs(sl * u)
+            da = 1.1 * np.abs(u) * dg + np.abs(sl) * du + dg * du + 2.0 ** -18 * a
+            da += ULP[xdt] * (a + da) + (2.0 ** -25 if xdt == "f16" else 0)
+            out[t] += p * (np.abs(ex.val[2][e]) @ da + cd * (ex.mag[2][e] @ (a + da)))
+    return out
+
+
+# Small shares of small values: the gated product is near fp16's smallest normal
+# value, and a share multiplied in before it is rounded to fp16 leaves three bits
+# of it.  The most experts and choices there are.
+@pytest.mark.parametrize("fmt,group", [("int4", 128), ("fp8", 128)])
+@pytest.mark.parametrize("t", [1, 5, 64])
+def test_small_shares_of_small_values(t, fmt, group):
+    say(f"moe small shares t={t} {fmt}")
+    e, top_k, h, i = 512, 16, 128, 128
+    ex = Experts(e, h, i, fmt, group, 110)
+    x = rand((t, h), 111, "f16", 0.02).cuda()
+    logits = rand((t, e), 112, "f32", 0.1)
+    y, ids, probs = run(x, ex, top_k, logits=logits.cuda(), renorm=False)
+    rid, rp = moe.route(logits.double().numpy(), top_k, False)
+    assert np.array_equal(ids, rid) and rp.max() < 4 / e
+    assert np.all(np.abs(probs - rp) <= 2.0 ** -18 * rp)
+    ref = moe.experts(x.double().cpu().numpy(), rid, rp, *ex.val)
+    # the shares' own error, 2^-18, of sums no larger than those of magnitudes
+    tol = spread_bound(x, rid, rp, ex, "f16")
+    big = np.zeros_like(ref)
+    for j in range(top_k):
+        part = np.zeros_like(rp)
+        part[:, j] = rp[:, j]
+        big += np.abs(moe.experts(x.double().cpu().numpy(), rid, part, *ex.val))
+    err = np.abs(y.double().cpu().numpy() - ref)
+    lim = (tol + 2.0 ** -18 * big) * (1 + 1e-3) + ULP["f32"] * np.abs(ref)
+    assert np.all(err <= lim), f"worst {np.max(err / lim):.3g} of the bound"
