@@ -139,6 +139,21 @@ def _dt(t):
     return d
 
 
+_TYPES = None
+
+
+def _types():
+    """The dtypes that E4M3 codes, fp32 values, fp16 scales and int32 values may
+    come in.  Bytes and 16-bit integers are taken as the bits of a format; another
+    float format of the same size would be read as wrong numbers."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = ((torch.float8_e4m3fn, torch.uint8), (torch.float32,),
+                  (torch.float16, torch.int16, torch.uint16), (torch.int32,))
+    return _TYPES
+
+
 # Addresses and streams go to ctypes as plain integers (its void* arguments
 # take them), which costs less than wrapping each one.
 def _ptr(t):
@@ -192,6 +207,11 @@ def _dense(what, name, t, nbytes=None, shape=None):
         _fail(what, f"{name} is not contiguous")
     if nbytes is not None and _nbytes(t) != nbytes:
         _fail(what, f"{name} holds {_nbytes(t)} bytes, expected {nbytes}")
+
+
+def _typed(what, name, t, types):
+    if t.dtype not in types:
+        _fail(what, f"{name} has dtype {t.dtype}, expected {types[0]}", _ERR_UNSUP)
 
 
 def _on_gpu(what, *ts):
@@ -250,8 +270,11 @@ def _weight_tensors(what, w):
         _dense(what, "codes", w.codes, n * k)
         _dense(what, "scales", w.scales, 4 * n)
     elif w.fmt == FMT_FP8_BLOCK:
+        e4m3, f32, _, _ = _types()
         _dense(what, "codes", w.codes, n * k)
+        _typed(what, "codes", w.codes, e4m3)
         _dense(what, "scales", w.scales, 4 * (-(-n // 128)) * (-(-k // 128)))
+        _typed(what, "scales", w.scales, f32)
     else:
         _fail(what, f"unknown weight format {w.fmt}", _ERR_UNSUP)
     return [w.codes, w.scales, w.zeros, w.scales2, w.perm]
@@ -534,13 +557,14 @@ def _rows(what, name, t):
 
 # The operators below are called once per layer and token, where the host's time
 # counts: every check of a tensor is one call.
-def _need(what, name, t, shape, size, dev):
-    """`t` is contiguous, of `shape`, `size` bytes per element and on `dev`."""
-    if t is None or t.shape != shape or t.element_size() != size or not t.is_contiguous():
-        n = size
+def _need(what, name, t, shape, types, dev):
+    """`t` is contiguous, of `shape`, of one of `types` and on `dev`."""
+    if t is None or t.shape != shape or t.dtype not in types or not t.is_contiguous():
+        n = types[0].itemsize
         for d in shape:
             n *= d
         _dense(what, name, t, n, shape)              # says what differs
+        _typed(what, name, t, types)
     if t.get_device() != dev:
         _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
 
@@ -555,8 +579,9 @@ def _like(what, name, t, shape, dtype, dev):
 
 
 def _fp8_rows(what, q, scales, m, k, dev):
-    _need(what, "q", q, (m, k), 1, dev)
-    _need(what, "scales", scales, ((k + 127) // 128, m), 4, dev)
+    e4m3, f32, _, _ = _types()
+    _need(what, "q", q, (m, k), e4m3, dev)
+    _need(what, "scales", scales, ((k + 127) // 128, m), f32, dev)
 
 
 def _device(what, t):
@@ -617,8 +642,11 @@ def wq_quantize_fp8_rows(x, q, scales, up=None, stream=None):
 def wq_quantize_fp8_block(w, codes, scales, stream=None):
     what = "wq_quantize_fp8_block"
     n, k = _matrix(what, "w", w)
+    e4m3, f32, _, _ = _types()
     _dense(what, "codes", codes, n * k)
+    _typed(what, "codes", codes, e4m3)
     _dense(what, "scales", scales, 4 * (-(-n // 128)) * (-(-k // 128)))
+    _typed(what, "scales", scales, f32)
     _on_gpu(what, w, codes, scales)
     st = _load().wq_quantize_fp8_block(_ptr(w), _dt(w), n, k, _ptr(codes), _ptr(scales),
                                        _stream(stream, w))
@@ -640,8 +668,10 @@ def wq_linear_fp8(q, scales, weight, y, workspace=None, stream=None):
     dev = q.get_device()
     _fp8_rows(what, q, scales, m, k, dev)
     wt = _weight_tensors(what, weight)
+    if y is None:
+        _fail(what, "y is required")
     ydt = _dt(y)
-    _need(what, "y", y, (m, weight.n), 4 if ydt == F32 else 2, dev)
+    _need(what, "y", y, (m, weight.n), (y.dtype,), dev)
     ws, ws_bytes = None, 0
     if workspace is not None:
         _dense(what, "workspace", workspace)
@@ -676,8 +706,11 @@ def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, log
         if _dt(logits) != F32:
             _fail(what, "logits must be float32", _ERR_UNSUP)
     ts = []
+    _, f32, f16, i32 = _types()
     for w in (gate, up, down):
         ts += _weight_tensors(what, w)
+        if w.fmt == FMT_INT4_ASYM:
+            _typed(what, "scales", w.scales, f16)
     i = down.k
     if (gate.n, gate.k) != (experts * i, h) or (up.n, up.k) != (experts * i, h) or (
             down.n != experts * h):
@@ -686,8 +719,10 @@ def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, log
     _dense(what, "y", y, shape=(m, h))
     if ids is not None:
         _dense(what, "ids", ids, 4 * m * top_k, (m, top_k))
+        _typed(what, "ids", ids, i32)
     if probs is not None:
         _dense(what, "probs", probs, 4 * m * top_k, (m, top_k))
+        _typed(what, "probs", probs, f32)
     _dense(what, "workspace", workspace)
     _on_gpu(what, x, router, logits, y, ids, probs, workspace, *ts)
     dg, du, dd = gate.descriptor(), up.descriptor(), down.descriptor()

@@ -231,3 +231,80 @@ def test_moe_binding():
     assert status(f, x, r, 2, g, u, d, y, ws, ids=torch.zeros((3, 3), dtype=torch.int32)) == SHAPE
     assert status(f, x, None, 2, g, u, d, y, ws, logits=torch.zeros((2, 4))) == SHAPE
     assert status(f, x, None, 2, g, u, d, y, ws, logits=torch.zeros((3, 4)).double()) == UNSUP
+
+
+# ------------------------------------------- types of the same size, on CPU tensors
+def refusal(fn, *a, **kw):
+    with pytest.raises(wq.WqError) as e:
+        fn(*a, **kw)
+    return e.value.status, str(e.value)
+
+
+def refused_type(fn, *a, **kw):
+    st, msg = refusal(fn, *a, **kw)
+    return st == UNSUP and "dtype" in msg
+
+
+def well_formed(fn, *a, **kw):
+    st, msg = refusal(fn, *a, **kw)
+    return st == UNSUP and "GPU" in msg
+
+
+OTHER8 = (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int8)
+
+
+def test_rows_of_other_types():
+    x, g = torch.zeros((4, 256), dtype=H), torch.zeros(256, dtype=H)
+    q, s = wq.alloc_fp8_rows(4, 256, device="cpu")
+    for call in (lambda q, s: (wq.wq_add_rmsnorm, x, g, 1e-5, None, None, None, q, s),
+                 lambda q, s: (wq.wq_quantize_fp8_rows, x, q, s)):
+        assert well_formed(*call(q, s)) and well_formed(*call(q.view(torch.uint8), s))
+        for dt in OTHER8:
+            assert refused_type(*call(q.view(dt), s))
+        assert refused_type(*call(q, s.view(torch.int32)))
+
+
+def test_fp8_weights_of_other_types():
+    w = wq.alloc_fp8(300, 256, device="cpu")
+    w16, y = torch.zeros((300, 256), dtype=H), torch.zeros((4, 300), dtype=H)
+    q, s = wq.alloc_fp8_rows(4, 256, device="cpu")
+    f, pack = wq.wq_linear_fp8, wq.wq_quantize_fp8_block
+    raw = wq.QuantizedWeight(wq.FMT_FP8_BLOCK, 300, 256, 128, w.codes.view(torch.uint8), w.scales)
+    assert well_formed(f, q, s, w, y) and well_formed(f, q.view(torch.uint8), s, raw, y)
+    assert well_formed(pack, w16, w.codes, w.scales) and well_formed(pack, w16, raw.codes, w.scales)
+    assert well_formed(wq.wq_dequantize, w, w16)
+    for dt in OTHER8:
+        assert refused_type(f, q.view(dt), s, w, y)
+        bad = wq.QuantizedWeight(wq.FMT_FP8_BLOCK, 300, 256, 128, w.codes.view(dt), w.scales)
+        assert refused_type(f, q, s, bad, y) and refused_type(wq.wq_dequantize, bad, w16)
+        assert refused_type(pack, w16, bad.codes, w.scales)
+    bad = wq.QuantizedWeight(wq.FMT_FP8_BLOCK, 300, 256, 128, w.codes, w.scales.view(torch.int32))
+    assert refused_type(f, q, s, bad, y) and refused_type(pack, w16, w.codes, bad.scales)
+    assert refused_type(f, q, s.view(torch.int32), w, y)
+    assert refused_type(f, q, s, w, y.view(torch.int16))
+    assert status(f, q, s, w, None) == SHAPE
+
+
+@pytest.mark.parametrize("fmt", ["int4", "fp8"])
+def test_experts_of_other_types(fmt):
+    x, r = torch.zeros((3, 256), dtype=H), torch.zeros((4, 256), dtype=H)
+    alloc = wq.alloc_int4 if fmt == "int4" else wq.alloc_fp8
+    g, u, d = (alloc(n, k, device="cpu") for n, k in ((512, 256), (512, 256), (1024, 128)))
+    ws, y = torch.zeros(1024, dtype=torch.uint8), torch.zeros((3, 256), dtype=H)
+    ids, probs = torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2))
+
+    def call(**kw):
+        a = dict(x=x, router=r, top_k=2, gate=g, up=u, down=d, y=y, workspace=ws, ids=ids,
+                 probs=probs)
+        return (lambda: wq.wq_moe(**{**a, **kw}),)
+
+    assert well_formed(*call())
+    assert refused_type(*call(ids=probs)) and refused_type(*call(probs=ids))
+    for name, w in (("gate", g), ("up", u), ("down", d)):
+        bad = w.clone()
+        bad.scales = w.scales.view(torch.bfloat16 if fmt == "int4" else torch.int32)
+        assert refused_type(*call(**{name: bad}))
+        if fmt == "fp8":
+            bad = w.clone()
+            bad.codes = w.codes.view(torch.float8_e5m2)
+            assert refused_type(*call(**{name: bad}))
