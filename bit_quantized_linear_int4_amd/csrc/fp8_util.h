@@ -66,16 +66,49 @@ __device__ __forceinline__ uint32_t pack4_fp8(float a, float b, float c, float d
 
 // The scale of a block whose largest magnitude has the fp32 bits `bits`
 // (sign cleared): amax / 448, 1 for a block of zeros, and never below the
-// smallest normal fp32 value, so that 1 / s stays finite and |v| * (1 / s)
-// at most 448.  The bits of an infinity or a NaN compare above every finite
-// magnitude, so a block that holds one gets that as its scale, and what is
+// smallest normal fp32 value, so that 1 / s stays finite and |v| / s at most
+// 448 (and a rounding).  The bits of an infinity or a NaN compare above every
+// finite magnitude, so a block that holds one gets that as its scale, and what is
 // read back from it is not finite either.
+// The quotient is that of an fp32 division: a product with 1 / 448 and its
+// residual; a / 448 is never within a fourteenth of a step of a midpoint.
 __device__ __forceinline__ float fp8_scale(uint32_t bits) {
   const float a = __uint_as_float(bits);
-  const float s = __fdiv_rn(a, kF8Max);
-  constexpr float kTiny = 1.17549435e-38f;
+  constexpr float kInv = 1.0f / kF8Max, kTiny = 0x1p-126f;
+  const float q = a * kInv;
+  const float s = bits < 0x7F800000u ? fmaf(fmaf(-q, kF8Max, a), kInv, q) : a;
   if (s < kTiny) return a == 0.0f ? 1.0f : kTiny;
   return s;
+}
+
+// Codes of v / s, rounded as an fp32 division rounds it, with one reciprocal for a
+// whole block: q = v * (1 / s) gains its residual v - q * s times 1 / s, which
+// leaves at most 2^-21 of an fp32 step.  A code could then change only next to one
+// of its midpoints, for scales within 13 steps of a 4-bit value, and for those the
+// reciprocal's own residual is enough (q alone changes one code in about a
+// million).  A small scale and its values are scaled up together, so that no
+// residual is subnormal; the residual's sign is taken such that a zero keeps its
+// own.  An infinite scale gives 0 for finite values, a NaN one NaN.
+// Against q alone: norm of 8192 rows of 8192 85.1 us either way, 1 row of 4096
+// 2.49 and 2.44, gated rows 2048 of 14336 28.9 either way.
+__device__ __forceinline__ uint2_t fp8_codes(float s, const float (&v)[8]) {
+  float a[8], q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = v[i];
+  if (s < 0x1p-64f) {
+    s *= 0x1p64f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= 0x1p64f;
+  }
+  const float d = __float_as_uint(s) == 0x7F800000u ? 0.0f : s;
+  float inv = __builtin_amdgcn_rcpf(s);                  // within one step
+  inv = fmaf(fmaf(-d, inv, 1.0f), inv, inv);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = a[i] * inv;
+    q[i] = fmaf(-fmaf(q[i], d, -a[i]), inv, q[i]);
+  }
+  return uint2_t{pack4_fp8(q[0], q[1], q[2], q[3]), pack4_fp8(q[4], q[5], q[6], q[7])};
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

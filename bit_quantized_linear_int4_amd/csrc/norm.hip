@@ -85,11 +85,8 @@ __device__ __forceinline__ void norm_store(const NormArgs& a, int64_t row, int c
 #pragma unroll
     for (int i = 0; i < 8; ++i) big = max(big, abs_bits(v[i]));
     const float s = fp8_scale(max16(live ? big : 0u));
-    const float inv = __fdiv_rn(1.0f, s);
     if (live) {
-      put(a.q + row * a.k + c * 8,
-          uint2_t{pack4_fp8(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                  pack4_fp8(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)});
+      put(a.q + row * a.k + c * 8, fp8_codes(s, v));
       if ((c & 15) == 0) a.scales[(int64_t)(c >> 4) * a.m + row] = s;
     }
   }
@@ -205,11 +202,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) big = max(big, abs_bits(v[u][i]));
     const float s = fp8_scale(max16(big));
-    const float inv = __fdiv_rn(1.0f, s);
     if (live[u]) {
-      put(a.q + row * a.k + c,
-          uint2_t{pack4_fp8(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv),
-                  pack4_fp8(v[u][4] * inv, v[u][5] * inv, v[u][6] * inv, v[u][7] * inv)});
+      put(a.q + row * a.k + c, fp8_codes(s, v[u]));
       if (l == 0) a.scales[(int64_t)b * a.m + row] = s;
     }
   }
@@ -249,16 +243,10 @@ __global__ __launch_bounds__(256) void quantize_block_kernel(const uint16_t* __r
   __syncthreads();
   big = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
   const float s = fp8_scale(big);
-  const float inv = __fdiv_rn(1.0f, s);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t row = nb * kF8Block + j * 16 + sub;
-    if (row < n && c < k) {
-      const uint2_t o = {
-          pack4_fp8(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
-          pack4_fp8(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv)};
-      *reinterpret_cast<uint2_t*>(q + row * k + c) = o;
-    }
+    if (row < n && c < k) *reinterpret_cast<uint2_t*>(q + row * k + c) = fp8_codes(s, v[j]);
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }

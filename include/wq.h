@@ -355,7 +355,7 @@ wq_status wq_scale_columns(const void* src, int32_t dt, int64_t rows, int64_t k,
  *   y = round16(v)
  *   per block b of 128 consecutive values (the last may be shorter):
  *     s = max|v| / 448 (1.0 if 0; at least 2^-126),
- *     q = E4M3(v * (1 / s)), scales[b][row] = s
+ *     q = E4M3(v / s), the fp32 quotient rounded to nearest, scales[b][row] = s
  *
  * x, residual, residual_out, gain, y: dt in {WQ_F16, WQ_BF16}; x [m] rows of
  * k, ldx elements apart; residual and residual_out [m] rows ldr apart; gain
@@ -390,7 +390,7 @@ wq_status wq_quantize_fp8_rows(const void* x, const void* up, int32_t dt, int64_
 
 /*
  * Quantize a weight to WQ_FMT_FP8_BLOCK: per block of 128 x 128
- *   s = max|w| / 448 (1.0 if 0; at least 2^-126), q = E4M3(w * (1 / s)).
+ *   s = max|w| / 448 (1.0 if 0; at least 2^-126), q = E4M3(w / s).
  * w: wdt in {WQ_F16, WQ_BF16} [n][k], 16-byte aligned, k % 16 == 0; codes E4M3
  * [n][k], 16-byte aligned; scales fp32 [ceil(n/128)][ceil(k/128)].
  */

@@ -8,8 +8,8 @@ FP8 deployment and its E4M3 layout; the scale granularities are readings):
   * weights: one fp32 scale per block of 128 x 128;
   * s = max|v| / 448 (fp32 division), 1 for a block of zeros, at least the
     smallest normal fp32 value 2^-126;
-  * code = E4M3(v * (1 / s)): the fp32 reciprocal, the fp32 product, one
-    rounding to nearest, ties to even.
+  * code = E4M3(v / s): the fp32 division, then one rounding to nearest, ties
+    to even.
 
 Norm and gated product are defined in fp64.
 """
@@ -65,8 +65,7 @@ def scale_of(amax32):
 
 
 def _codes(v, s):
-    inv = (np.float32(1) / s).astype(np.float32)
-    return encode((v * inv).astype(np.float32))
+    return encode((v / s).astype(np.float32))
 
 
 def quantize_rows(v32):

@@ -389,3 +389,57 @@ def test_norm_sizes(m, k, dtype):
     err = np.abs(y.double().cpu().numpy() - v)
     assert np.all(err <= (ULP[dtype] * (1 + 1e-3) + tol) * np.abs(v) + TINY[dtype])
     check_codes(q, s, v, tol)
+
+
+def quotient_rows(dtype, seed):
+    """A row of 128 for each 16-bit mantissa of the largest value, with values
+    whose quotient by the scale is next to a midpoint of two codes in front, at
+    many magnitudes of the whole row."""
+    mant, exps = {"f16": (1024, (-12, -3, 0, 7)), "bf16": (128, (-130, -122, -80, -64, 0, 60, 119))}[
+        dtype]
+    lat = np.concatenate([(1 + np.arange(mant) / mant) * 2.0 ** -e for e in range(10)])
+    lat = lat.astype(np.float32)
+    r = np.random.default_rng(seed)
+    rows = []
+    for a in (1 + np.arange(mant) / mant).astype(np.float32):
+        s = np.float32(a / np.float32(448))
+        v = lat[lat <= a]
+        hard = v[fp8.encode(v * (np.float32(1) / s)) != fp8.encode(v / s)][:60]
+        row = np.concatenate([[a], hard, -hard, r.choice(v, 128)])[:128]
+        rows += [row * np.float32(2.0 ** e) for e in exps]
+    return torch.from_numpy(np.array(rows, np.float32)).to(TD[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_codes_are_of_the_quotient(dtype):
+    say(f"codes of the fp32 quotient, {dtype}")
+    x = quotient_rows(dtype, 14)
+    m, k = x.shape
+    codes, scales = fp8.quantize_rows(x.float().numpy())
+    # the values do tell a product with the reciprocal from the quotient
+    inv = (np.float32(1) / scales[0])[:, None]
+    with np.errstate(over="ignore"):
+        assert (fp8.encode(x.float().numpy() * inv) != codes).sum() > 100
+    q, s = wq.alloc_fp8_rows(m, k)
+    wq.wq_quantize_fp8_rows(x.cuda(), q, s)
+    torch.cuda.synchronize()
+    assert np.array_equal(s.cpu().numpy(), scales) and np.array_equal(bits(q), codes)
+    # the norm of rows of ones is 1: it leaves the gains, in fp32 as they are
+    for row in x[x.abs().max(1).values < 1e4][::97]:
+        one = torch.ones((3, k), dtype=x.dtype)
+        one[1] = -1
+        q3, s3 = wq.alloc_fp8_rows(3, k)
+        wq.wq_add_rmsnorm(one.cuda(), row.cuda(), 0.0, q=q3, scales=s3)
+        torch.cuda.synchronize()
+        codes, scales = fp8.quantize_rows(one.float().numpy() * row.float().numpy())
+        assert np.array_equal(s3.cpu().numpy(), scales) and np.array_equal(bits(q3), codes)
+    # and one row of a weight block, zeros below
+    for row in x[::53]:
+        w16 = torch.zeros((2, k), dtype=x.dtype)
+        w16[1] = row
+        w = wq.alloc_fp8(2, k)
+        wq.wq_quantize_fp8_block(w16.cuda(), w.codes, w.scales)
+        torch.cuda.synchronize()
+        codes, scales = fp8.quantize_block(w16.float().numpy())
+        assert np.array_equal(w.scales.cpu().numpy(), scales)
+        assert np.array_equal(bits(w.codes), codes)

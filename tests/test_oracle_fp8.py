@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from exact_fp import FP32, exact, rn
 from oracle import fp8, moe
 
 
@@ -113,3 +114,92 @@ def test_experts_against_loops(renorm):
                     uv = sum(u[ex, c, q] * x[a, q] for q in range(h))
                     s += p[a, j] * d[ex, o, c] * gv / (1 + math.exp(-gv)) * uv
             assert abs(s - y[a, o]) <= 1e-12 * (1 + abs(s))
+
+
+def row_of(v):
+    """[v] as the rows of a block 128 wide, zeros behind."""
+    out = np.zeros((1, 128), np.float32)
+    out[0, :len(v)] = v
+    return out
+
+
+# The code is that of the fp32 quotient v / s; v times the reciprocal of s gives
+# the neighbouring one here.
+@pytest.mark.parametrize("amax,v,code", [(1.078125, 0.80859375, 122), (1.0234375, 0.767578125, 122),
+                                         (1.03125, 1.5735626220703125e-05, 4)])
+def test_codes_are_of_the_quotient(amax, v, code):
+    a, x = np.float32(amax), np.float32(v)
+    s = np.float32(a / np.float32(448))
+    near = np.float32(float(rn(exact(x) / exact(s), FP32)))
+    assert fp8.encode(near) == code
+    assert fp8.encode(np.float32(x * (np.float32(1) / s))) != code
+    codes, _ = fp8.quantize_rows(row_of([a, x, -x]))
+    assert codes[0, :3].tolist() == [126, code, code | 128]
+    codes, _ = fp8.quantize_block(row_of([a, x, -x]).astype(np.float16).repeat(2, 0))
+    assert codes[1, :3].tolist() == [126, code, code | 128]
+
+
+def fma(a, b, c):
+    """fp32 fused multiply-add of scalars, rounded once."""
+    v = exact(a) * exact(b) + exact(c)
+    if v == 0:
+        return np.float32(float(a) * float(b) + float(c))    # the sign of zero
+    return np.float32(float(rn(v, FP32)))
+
+
+def corrected(v, s, inv):
+    """v / s as the packers divide in fp32: v * inv and its residual times inv."""
+    q = v * inv
+    return fma(-fma(q, s, -v), inv, q)
+
+
+def reciprocals(s):
+    """1 / s from a reciprocal up to one step off, with its residual added."""
+    near = np.float32(1) / s
+    for start in (near, np.nextafter(near, np.float32(0)), np.nextafter(near, 2 * near)):
+        yield fma(fma(-s, start, np.float32(1)), start, start)
+
+
+def test_a_corrected_quotient_has_the_codes_of_the_division():
+    """v * inv is off by at most 2.5 steps even if inv is off by one; with its
+    residual times inv, 2^-21 of a step is left.  That can change an fp32 rounding
+    only next to a midpoint of two fp32 values, and a code only where that midpoint
+    is half a step from a midpoint of two codes (5 bits).  With integers A / B of 24
+    bits that takes B within 13 of a multiple of 2^20: those scales, each with the
+    values around every midpoint."""
+    n = 0
+    for c in range(8, 17):
+        for delta in range(-14, 15):
+            B = (c << 20) + delta
+            if B < 1 << 23 or B >= 1 << 24:
+                continue
+            s = np.float32(B)
+            for j in range(17, 32, 2):
+                for A in range(B * j // 32 - 2, B * j // 32 + 4):
+                    v = np.float32(A)
+                    code = fp8.encode(np.float32(v / s))
+                    for inv in reciprocals(s):
+                        assert fp8.encode(corrected(v, s, inv)) == code, (A, B)
+                        n += 1
+    assert n > 30000
+    r = np.random.default_rng(8)
+    v = np.float32(r.uniform(1, 2, 1000))
+    s = np.float32(r.uniform(1, 2, 1000) * 2.0 ** -4)
+    for a, b in zip(v, s):
+        for inv in reciprocals(b):
+            assert fp8.encode(corrected(a, b, inv)) == fp8.encode(a / b)
+    for zero in (np.float32(0.0), np.float32(-0.0)):
+        for inv in reciprocals(np.float32(3)):
+            assert np.signbit(corrected(zero, np.float32(3), inv)) == np.signbit(zero)
+
+
+def test_a_corrected_scale_is_the_division():
+    """a * (1 / 448) and its residual, for every mantissa; fp64 holds each step but
+    the last sum, which is rounded far from a midpoint."""
+    inv = np.float32(1) / np.float32(448)
+    for part in np.split(np.arange(1 << 23, 1 << 24), 8):
+        a = part.astype(np.float32)
+        q = a * inv
+        r = (a.astype(np.float64) - q.astype(np.float64) * 448).astype(np.float32)
+        got = (r.astype(np.float64) * np.float64(inv) + q).astype(np.float32)
+        assert np.array_equal(got, a / np.float32(448))
