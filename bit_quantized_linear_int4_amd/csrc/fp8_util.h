@@ -182,8 +182,13 @@ inline hipError_t allow_lds(const void* kern, int bytes, std::atomic<uint64_t>& 
   return e;
 }
 
-// v / (1 + exp(-v)) with the hardware exponential and reciprocal (about 1e-6
-// relative for |v| up to 20; exp overflow gives the limit 0)
+// v / (1 + exp(-v)) with the hardware exponential and reciprocal; exp overflow
+// gives the limit 0.  The exponent v * log2(e) is rounded to fp32, which costs up to
+// |v| * 2^-24 of the value where v is negative: 1e-6 at -16 (57 * 2^-24 at most down
+// to -80), where an E4M3 or a 16-bit rounding of the result, 2^-4 to 2^-12 of it,
+// follows in every use.  With the exponent's rest added, good to 10 * 2^-24, the
+// gated packer, which the vector units bound as much as HBM does, takes 29.9 us
+// instead of 28.1 for 2048 rows of 14336 and 6.3 instead of 5.7 for 300.
 __device__ __forceinline__ float silu(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
