@@ -443,3 +443,56 @@ def test_codes_are_of_the_quotient(dtype):
         codes, scales = fp8.quantize_block(w16.float().numpy())
         assert np.array_equal(w.scales.cpu().numpy(), scales)
         assert np.array_equal(bits(w.codes), codes)
+
+
+# ------------------------------------------------- products without a tolerance
+def integer_linear(m, n, k, seed, pairs=False):
+    """Codes that are integers up to 4 and scales that are powers of two: every
+    product, and every sum of them in any order, is exact in fp32, so one lost,
+    doubled or misplaced code shows.  With `pairs`, each whole block also holds
+    448 * 448 and its negative."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(-4, 5, (m, k), generator=g).float()
+    w = torch.randint(-4, 5, (n, k), generator=g).float()
+    if pairs:
+        for b in range(k // 128):
+            i, j = (b * 128 + torch.randperm(128, generator=g)[:2]).tolist()
+            x[:, i], x[:, j], w[:, i], w[:, j] = 448.0, 448.0, 448.0, -448.0
+    kb, nb = -(-k // 128), -(-n // 128)
+    s = torch.exp2(torch.randint(-2, 3, (kb, m), generator=g).float())
+    e = torch.exp2(torch.randint(-2, 3, (nb, kb), generator=g).float())
+    f8 = torch.float8_e4m3fn
+    return (x.to(f8).cuda(), s.cuda(),
+            wq.QuantizedWeight(wq.FMT_FP8_BLOCK, n, k, 128, w.to(f8).cuda(), e.cuda()))
+
+
+# every schedule: one token, 1 to 4 tiles of 16 tokens with few and many features,
+# tiles of 64 and 128 tokens whole and split, 256 x 256 tiles with and without
+# tiles of 128 tokens after them
+EXACT = [(1, 300, 400), (1, 4500, 144), (7, 515, 2064), (16, 4200, 272), (31, 200, 1024),
+         (40, 5000, 400), (48, 12301, 400), (64, 200, 2064), (64, 8201, 272), (65, 257, 16),
+         (100, 136, 8832), (150, 1000, 4112), (300, 513, 1040), (512, 1030, 272),
+         (1000, 4000, 1296), (2049, 4100, 400), (4096, 5120, 272)]
+
+
+@pytest.mark.parametrize("ydt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", EXACT)
+def test_linear_of_integers_is_exact(m, n, k, ydt):
+    say(f"fp8 linear of integers m={m} n={n} k={k} y={ydt}")
+    q, s, w = integer_linear(m, n, k, 61)
+    ref = reference(q, s, w)[0]
+    assert float(ref.abs().max()) < 2.0 ** 15
+    y = linear(q, s, w, ydt)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref.float().to(TD[ydt]))
+
+
+@pytest.mark.parametrize("m,n,k", [c for c in EXACT if c[0] <= 1000])
+def test_linear_fp32_products_are_exact(m, n, k):
+    """What the FP8 matrix instructions drop beside 448 * 448 (products below 2)."""
+    say(f"fp8 linear, large pairs, m={m} n={n} k={k}")
+    q, s, w = integer_linear(m, n, k, 62, pairs=True)
+    ref = reference(q, s, w)[0]
+    y = linear(q, s, w, "f32")
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref.float())
