@@ -7,12 +7,14 @@
 // are added to the fp32 totals with one fused multiply-add each.
 //
 // The FP8 matrix instructions (all of them: 16x16x32, 16x16x128 and 32x32x64
-// give the same bits) drop bits below about 2^-16 of the largest products of
-// a sum: measured on N(0, 100) codes 1.5e-5 of the sum's size, 4.6e-5 with one
-// outlier per block.  That is far below the rounding of a 16-bit y (up to 2^-8
-// or 2^-11 of the value), so those outputs use it.  An fp32 y takes the exact
-// products instead: the codes converted to bf16 (exact) and four
-// v_mfma_f32_16x16x32_bf16 per block, 1e-8 on the same codes, at half the
+// give the same bits) cut every product towards zero at 2^-17 of the largest power
+// of two among a sum's products: measured on N(0, 100) codes 1.5e-5 of the sum's
+// size, 4.6e-5 with one outlier per block, and at worst 2^-10 of the largest
+// product (256 * 256 beside 127 products alike: 0.43 * 2^-16 of it each).  On
+// activations that is far below the rounding of a 16-bit y (up to 2^-8 or 2^-11 of
+// the value), and the worst is no larger than it, so those outputs use them.  An
+// fp32 y takes the exact products instead: the codes converted to bf16 (exact) and
+// four v_mfma_f32_16x16x32_bf16 per block, 1e-8 on the same codes, at half the
 // matrix rate.
 //
 // Operands: the weights are the A operand (16 output features), the activations

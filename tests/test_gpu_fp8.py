@@ -496,3 +496,54 @@ def test_linear_fp32_products_are_exact(m, n, k):
     y = linear(q, s, w, "f32")
     torch.cuda.synchronize()
     assert torch.equal(y, ref.float())
+
+
+def power(t):
+    """The power of two of a code, 2^-6 for smaller ones."""
+    return torch.exp2(torch.floor(torch.log2(t.double().abs().clamp(min=2.0 ** -6))))
+
+
+@pytest.mark.parametrize("ydt", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["one large", "all codes", "normal"])
+@pytest.mark.parametrize("m,n,k", [(1, 130, 400), (16, 300, 1040), (64, 200, 528), (150, 140, 656),
+                                   (300, 1000, 272), (2049, 4100, 144)])
+def test_linear_16_bit_bound(m, n, k, kind, ydt):
+    """Each product of a block is cut at 2^-17 of the largest power of two among the
+    block's products: 128 of them lose at most 2^-10 of it.  Then fp32 sums, and the
+    rounding of y."""
+    say(f"fp8 linear bound m={m} n={n} k={k} {kind} y={ydt}")
+    f8 = torch.float8_e4m3fn
+    g = torch.Generator().manual_seed(63)
+    if kind == "normal":
+        x, w = (torch.randn(r, k, generator=g).mul(100).clamp(-448, 448).to(f8) for r in (m, n))
+    else:
+        x, w = (torch.randint(0, 127, (r, k), generator=g, dtype=torch.uint8) for r in (m, n))
+        if kind == "one large":
+            # 256 * 256 beside products that are alike within a row and column
+            x[:], w[:] = x[:, :1], w[:, :1]
+            x[:, 5::128], w[:, 5::128] = 0x78, 0x78
+        else:
+            x |= torch.randint(0, 2, (m, k), generator=g, dtype=torch.uint8) << 7
+        x, w = x.view(f8), w.view(f8)
+    kb, nb = -(-k // 128), -(-n // 128)
+    q = x.cuda()
+    # y of every kind within 16 bits' range
+    s = (torch.rand((kb, m), generator=g) + 0.5).mul(2.0 ** -8).cuda()
+    w = wq.QuantizedWeight(wq.FMT_FP8_BLOCK, n, k, 128, w.cuda(),
+                           (torch.rand((nb, kb), generator=g) + 0.5).mul(2.0 ** -8).cuda())
+    ref, mag = reference(q, s, w)
+    tol = (kb + 16) * 2.0 ** -23 * mag
+    for b in range(kb):
+        c = slice(b * 128, (b + 1) * 128)
+        px, pw = power(q[:, c].float()), power(w.codes[:, c].float())
+        e = (s[b].double()[:, None] * w.scales[:, b].double().repeat_interleave(128)[:n]) * 2.0 ** -10
+        for r in range(0, m, 64):
+            u = torch.zeros((min(64, m - r), n), dtype=torch.float64, device="cuda")
+            for i in range(px.shape[1]):
+                u = torch.maximum(u, px[r:r + 64, i:i + 1] * pw[:, i])
+            tol[r:r + 64] += e[r:r + 64] * u
+    y = linear(q, s, w, ydt)
+    torch.cuda.synchronize()
+    err = (y.double() - ref).abs()
+    assert bool((err <= tol + ULP[ydt] * (1 + 1e-3) * (ref.abs() + tol) + TINY[ydt]).all()), (
+        f"worst {float((err / (tol + 1e-300)).max()):.3g} of the bound")
