@@ -300,3 +300,51 @@ def test_small_shares_of_small_values(t, fmt, group):
     err = np.abs(y.double().cpu().numpy() - ref)
     lim = (tol + 2.0 ** -18 * big) * (1 + 1e-3) + ULP["f32"] * np.abs(ref)
     assert np.all(err <= lim), f"worst {np.max(err / lim):.3g} of the bound"
+
+
+def spread(t, top_k, counts, seed):
+    """Logits fp32 [t][e] that route counts[e] tokens to expert e."""
+    left = np.array(counts)
+    assert left.sum() == t * top_k and left.max() <= t
+    r = np.random.default_rng(seed)
+    logits = r.uniform(-2, -1, (t, len(counts)))
+    for i in range(t):
+        pick = np.argsort(-left, kind="stable")[:top_k]
+        left[pick] -= 1
+        logits[i, pick] = r.uniform(1, 2, top_k)
+    assert not left.any()
+    return torch.from_numpy(logits.astype(np.float32))
+
+
+# The walk over the gate/up steps: from tile to tile, chunk (16 tokens) to chunk and
+# expert to expert within a workgroup, with a last block of tiles that is shorter than
+# the others; 8 and 16 waves, k in one pass and in two, grids as large as the tiles and
+# as large as the GPU holds.
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("t,top_k,counts,h,i,per", [
+    (50, 2, (20, 50, 30), 384, 128, 3), (50, 2, (20, 50, 30), 2176, 128, 3),
+    (50, 2, (20, 50, 30), 4224, 128, 3), (37, 1, (37,), 256, 128, 3), (33, 1, (33,), 2304, 128, 3),
+    (64, 3, (64, 40, 1, 33, 17, 16, 17, 4), 256, 1280, 3)])
+def test_steps(t, top_k, counts, h, i, per, fmt, group, xdt):
+    steps_case(t, top_k, counts, h, i, per, fmt, group, xdt)
+
+
+@pytest.mark.parametrize("fmt,group", [("int4", 128), ("int4", 32), ("fp8", 128)])
+def test_steps_of_large_experts(fmt, group):
+    steps_case(64, 2, (17, 64, 14, 33), 2176, 1664, 5, fmt, group, "bf16")
+
+
+def steps_case(t, top_k, counts, h, i, per, fmt, group, xdt):
+    say(f"moe steps t={t} {counts} h={h} i={i} {fmt} g{group} {xdt}")
+    e, tiles = len(counts), i // 16
+    chunks = sum((c + 15) // 16 for c in counts)
+    # as launched: workgroups, steps of each, and a block of tiles that is cut short
+    grid = min(min(e, t * top_k) * tiles, 512 if h <= 2048 else 256)
+    assert -(-tiles * chunks // grid) == per and per > 1 and tiles % per != 0
+    ex = Experts(e, h, i, fmt, group, 120)
+    x = rand((t, h), 121, xdt, 0.5).cuda()
+    logits = spread(t, top_k, counts, 122)
+    got = run(x, ex, top_k, logits=logits.cuda(), ydt="f32")
+    assert np.bincount(got[1].ravel(), minlength=e).tolist() == list(counts)
+    check(x, ex, logits.double().numpy(), top_k, xdt, got, True, "f32")
