@@ -43,3 +43,22 @@ def test_abi_checks_clean_under_asan_and_ubsan():
     assert r.returncode == 0, out[-4000:]
     assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
     assert " passed" in out
+
+
+@pytest.mark.skipif(not _have_hipcc(), reason="hipcc not available")
+def test_fp8_and_moe_checks_clean_under_asan_and_ubsan():
+    env = dict(os.environ)
+    env.update({
+        "WQ_LIBRARY": _build.build_host_sanitized(),
+        "LD_PRELOAD": _build.sanitizer_runtime(),
+        "ASAN_OPTIONS": "detect_leaks=0:halt_on_error=1",
+        "UBSAN_OPTIONS": "halt_on_error=1:print_stacktrace=1",
+    })
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "not gpu",
+         os.path.join(ROOT, "tests", "test_fp8_moe_checks.py")],
+        cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    out = r.stdout + r.stderr
+    assert r.returncode == 0, out[-4000:]
+    assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
+    assert " passed" in out and "skipped" not in out

@@ -66,3 +66,16 @@ def test_no_kernel_uses_scratch_or_spills(tmp_path):
            if v.get("private_segment_fixed_size", 0) or v.get("vgpr_spill_count", 0)
            or v.get("sgpr_spill_count", 0)}
     assert not bad, f"{len(bad)} kernels use scratch or spill, e.g. {sorted(bad)[:3]}"
+
+
+def test_fp8_norm_and_moe_kernels_do_not_spill_either(tmp_path):
+    kernels = kernel_metadata(tmp_path)
+    # the waits of the FP8 products count loads and stores: a spill would be one more
+    for fam in ("add_rmsnorm_kernel", "quantize_rows_kernel", "quantize_block_kernel",
+                "fp8_decode_kernel", "fp8_gemm_kernel", "fp8_halves_kernel", "fp8_join_kernel",
+                "moe_router_kernel", "moe_gate_up_kernel", "moe_down_kernel", "moe_join_kernel"):
+        mine = {k: v for k, v in kernels.items() if fam in k}
+        assert mine, fam
+        for k, v in mine.items():
+            assert v["private_segment_fixed_size"] == v["vgpr_spill_count"] == 0, k
+            assert v["sgpr_spill_count"] == 0, k
