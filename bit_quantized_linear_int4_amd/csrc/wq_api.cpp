@@ -480,8 +480,10 @@ size_t wq_moe_workspace(int64_t m, int32_t top_k, const wq_weight* gate, int64_t
   if (gate == nullptr || m < 1 || m > kMoeMaxTokens || experts < 1 || experts > kMoeMaxExperts ||
       top_k < 1 || top_k > kMoeMaxTopK || top_k > experts)
     return 0;
-  if (check_weight(gate, gate->fmt != WQ_FMT_FP8_BLOCK) != WQ_OK || gate->n % experts != 0)
+  if (check_weight(gate, gate->fmt != WQ_FMT_FP8_BLOCK) != WQ_OK || gate->perm != nullptr ||
+      (gate->fmt != WQ_FMT_INT4_ASYM && gate->fmt != WQ_FMT_FP8_BLOCK))
     return 0;
+  if (gate->k % 128 != 0 || gate->n % (experts * 128) != 0) return 0;
   return moe_ws_bytes(m, experts, top_k, gate->k, gate->n / experts);
 }
 

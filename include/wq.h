@@ -441,7 +441,7 @@ wq_status wq_linear_fp8(const void* q, const float* scales, int64_t m, const wq_
  * (equal groups) or FP8_BLOCK.  y: ydt in {F16, BF16, F32} [m][h].
  * ids: int32 [m][top_k] and probs: fp32 [m][top_k], NULL or written, in the
  * order of decreasing l.  workspace: at least wq_moe_workspace(m, top_k, gate,
- * experts) bytes, 256-byte aligned.
+ * experts) bytes, 256-byte aligned (0 for arguments that wq_moe refuses).
  * h and i multiples of 128; INT4 scales 8-byte and zeros 2-byte aligned;
  * experts <= 512; top_k <= min(experts, 16).
  *

@@ -308,3 +308,14 @@ def test_experts_of_other_types(fmt):
             bad = w.clone()
             bad.codes = w.codes.view(torch.float8_e5m2)
             assert refused_type(*call(**{name: bad}))
+
+
+@needs_lib
+def test_moe_workspace_of_weights_it_does_not_take():
+    """0, as the other workspace queries say for arguments that the call refuses."""
+    ask = wq._load().wq_moe_workspace
+    assert ask(4, 2, ctypes.byref(i4(n=512, k=256)), 4) > 0
+    assert ask(4, 2, ctypes.byref(desc(n=512, k=256)), 4) > 0
+    for bad in (i4(n=512, k=256, fmt=wq.FMT_NF4, zeros=None, group=64), i4(n=512, k=256, perm=P),
+                i4(n=512, k=192, group=64), desc(n=512, k=272), i4(n=256, k=256)):
+        assert ask(4, 2, ctypes.byref(bad), 4) == 0
