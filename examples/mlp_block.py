@@ -36,8 +36,8 @@ def pack_int4(w, group=128):
 
 
 class DenseMLP:
-    """gate, up [inner][hidden] and down [hidden][inner] in 16 bits, for up to
-    `tokens` rows."""
+    """gate, up [inner][hidden] and down [hidden][inner] in 16 bits, for `tokens`
+    rows a call."""
 
     def __init__(self, gain, gate, up, down, tokens, eps=1e-6):
         inner, hidden = gate.shape
@@ -64,7 +64,7 @@ class DenseMLP:
 
 class ExpertsMLP:
     """router [experts][hidden], gate and up [experts][inner][hidden], down
-    [experts][hidden][inner] in 16 bits, for `tokens` <= 64 rows."""
+    [experts][hidden][inner] in 16 bits, for `tokens` <= 64 rows a call."""
 
     def __init__(self, gain, router, gate, up, down, top_k, tokens, eps=1e-6):
         e, inner, hidden = gate.shape

@@ -381,9 +381,9 @@ wq_status wq_add_rmsnorm(const void* x, int32_t dt, int64_t m, int64_t k, int64_
  *   v = x, or silu(x) * up when up is given (silu(t) = t / (1 + exp(-t)), fp32),
  *   s, q as in wq_add_rmsnorm.
  * x, up: dt in {WQ_F16, WQ_BF16} [m][k], 16-byte aligned; q E4M3 [m][k], 8-byte
- * aligned; scales fp32 [ceil(k/128)][m]; k % 8 == 0.  A NaN or an infinity
- * makes the scale of its block one, and what q * s gives for that block is
- * not finite where the value was not.
+ * aligned; scales fp32 [ceil(k/128)][m]; k % 8 == 0.  A block with a NaN has a
+ * NaN scale, one with an infinity an infinite scale, and what q * s gives is not
+ * finite where the value was not.
  */
 wq_status wq_quantize_fp8_rows(const void* x, const void* up, int32_t dt, int64_t m, int64_t k,
                                void* q, float* scales, void* stream);
