@@ -21,12 +21,20 @@
 // several hundred experts, multiplied in before the rounding to fp16, would
 // push a among the subnormals and cost most of its bits.
 //
-// One MI355X, us: one token, 8 of 64 INT4 experts of 2048 x 1024 18.6 (25 MB, 5
-// at the rate of a copy; three dependent launches); 24 tokens, 6 of 64 FP8 84
-// (365 MB, 70); 64 tokens, 2 of 8 INT4 of 4096 x 14336 244 (735 MB, 142).  The
-// last is not bound by HBM: an expert with more than 16 tokens is read (in 2.
-// from L2) and unpacked twice, and a step (a tile, 16 tokens) of gate/up takes
-// the 3 us that its loads, one step ahead, need.
+// One MI355X, us: one token, 8 of 64 INT4 experts of 2048 x 1024 18.5 (25 MB, 5
+// at the rate of a copy; three dependent launches); 24 tokens, 6 of 64 FP8 82
+// (365 MB, 70); 64 tokens, 2 of 8 INT4 of 4096 x 14336 243 to 249 (735 MB, 142).
+// The last: an expert with more than 16 tokens is read and unpacked twice.  In 2.
+// its codes come from L2 the second time (495 MB fetched for 488), and a step (a
+// tile, 16 tokens) takes the 3 us that its loads, one step ahead, need.  In 3. the
+// two chunks of an expert are far apart in k, and both come from HBM (379 MB
+// fetched for 244).  Groups of 128, 64 and 32: one token 18.5, 19.3, 21.9; 24
+// tokens, 6 of 64 61.9, 63.7, 71.0; 64 tokens, 2 of 8 245, 259, 296.
+//
+// a is kept in the activations' type, which the matrix instructions of 3. take:
+// with y in the same type the error of y is the square root of two times that of
+// y's rounding alone (bf16 2.3e-3 against 1.7e-3); in two parts a would double 3.'s
+// products.
 //
 // The multiply runs on v_mfma_f32_16x16x32 with up to 16 tokens as the A
 // operand and 16 weight rows as the B operand.  INT4 codes are not rounded to
@@ -1009,12 +1017,11 @@ constexpr int kDownTables = kMaxChunks * (int)sizeof(Chunk) + kMaxT * kMaxK * 5;
 // Parts of k in the down product with two row tiles per workgroup, as many as
 // fill the 256 CUs once, or 0: one row tile, all of k, no join.  Two tiles read
 // the intermediate once for both, which the L2 carries at several times the
-// codes' size: 64 tokens, 2 of 8 experts of 4096 x 14336 INT4 take 244 us (two
-// tiles, 2 parts), 257 (one tile), 320 (two tiles, one part); 24 tokens, 6 of
-// 64 FP8 experts of 2048 x 1024 85 us (two tiles, 4 parts) against 98.  For a
-// few choices the join costs more than that gives: one token, 8 of 64 INT4
-// experts, 18.9 us with one tile, 20.5 with two in 4 parts; 4 tokens 39.2
-// against 34.9.
+// codes' size: 64 tokens, 2 of 8 experts of 4096 x 14336 INT4 take 247 us (two
+// tiles, 2 parts), 262 (one tile), 322 (two tiles, one part); 24 tokens, 6 of
+// 64 FP8 experts of 2048 x 1024 83 us (two tiles, 4 parts) against 98; 4 tokens, 8
+// of 64 INT4 34.2 against 39.6.  For a few choices the join costs more than that
+// gives: one token, 8 of 64 18.5 us with one tile, 19.5 with two in 4 parts.
 int down_parts(int64_t t, int64_t top_k, int64_t h) {
   return t * top_k <= 8 ? 0 : (int)std::max<int64_t>(1, 256 * 32 / h);
 }
@@ -1047,8 +1054,8 @@ hipError_t moe_fmt(const MoeArgs& a, hipStream_t s) {
   }
   // 8 waves and two workgroups per CU, which are seldom at the same point of a
   // step, where they cover k in one pass; else 16 waves and one: 16 tokens, 8 of
-  // 64 INT4 experts, h = 2048, 62.8 us with 8 waves, 75.4 with 16; 64 tokens, 2
-  // of 8, h = 4096, 365 with 8 (two passes), 244 with 16
+  // 64 INT4 experts, h = 2048, 61.0 us with 8 waves, 73.8 with 16; 64 tokens, 2
+  // of 8, h = 4096, 363 with 8 (two passes), 247 with 16
   const int64_t units = (int64_t)std::min(a.e, a.t * a.top_k) * (a.i / 16);
   if (a.h <= 8 * 256) {
     const unsigned grid = (unsigned)std::min<int64_t>(units, 512);

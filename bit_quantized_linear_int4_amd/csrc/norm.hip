@@ -8,16 +8,19 @@
 // stays in registers between the sum and the outputs, so each input is read
 // once and each output written once: the kernel is bound by HBM for many rows
 // and by the latency of one load, one barrier and one store for few.  bf16 with
-// a residual to FP8, 8192 rows of 8192: 84 us, 5600 GB/s (a copy of 1 GiB:
-// 5180); 1 row of 4096: 2.4 us, of 256: 2.0.
+// a residual to FP8, 8192 rows of 8192: 85 us, 5520 GB/s (a copy of 1 GiB: 5130
+// to 5180); 1 row of 4096: 2.5 us, of 256: 2.0.
 // One row per workgroup, and outputs stored past the caches, which keeps them
-// for the inputs: with four rows per workgroup 97 us, with ordinary stores 96.
+// for the inputs: with four rows per workgroup 97 us, with ordinary stores 96
+// (84 then for one row and these stores).
 //
 // quantize_rows: the same scale and code for given rows, or for silu(x) * up
 // (what stands between the gate/up and the down product of an MLP); bound by
-// HBM: 2048 rows of 14336, gated, 28 us, 5200 GB/s.
+// HBM and, gated, as much by the vector units: 2048 rows of 14336 28 to 29 us,
+// 5030 to 5270 GB/s.
 //
-// quantize_block: weights, one scale per 128 x 128 block.
+// quantize_block: weights, one scale per 128 x 128 block; once per weight: 14336
+// x 4096 41 us, 4300 GB/s, 28672 x 8192 132 us, 5350 GB/s.
 //
 // Scales of rows are stored [ceil(k / 128)][m]: the linear reads the scales of
 // all its tokens for one block of k at once, so they are contiguous.
@@ -163,7 +166,7 @@ struct RowsArgs {
 // 16 lanes per scale block; a workgroup takes RT rows x 16/RT blocks of k in
 // each of U rounds, so with RT = 16 the scales it writes are 64 contiguous
 // bytes per block of k.  Workgroups next to each other continue along k.  Two
-// rounds: 16 rows of 11008 2.7 us, 3.6 with four.
+// rounds: 16 rows of 11008 2.7 us, 3.8 with four.
 template <int DT, int RT, int U>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(RowsArgs a) {
   const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
@@ -261,9 +264,9 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t s) {
   const int nc = a.k / 8;
   // Up to two rows per CU the time is one chain of latencies (load, sum, store),
   // shortest with one chunk per thread; with more rows several workgroups share
-  // a CU, and smaller ones fit better: k = 8192, 1 row 2.9 us with 1024 threads
-  // and 3.5 with 256, 256 rows 3.9 and 4.5, 1024 rows 11.4 and 10.4, 2048 rows
-  // 21.1 and 19.9.
+  // a CU, and smaller ones fit better: k = 8192, 1 row 3.0 us with 1024 threads
+  // and 3.7 with 256, 256 rows 4.1 and 4.7, 1024 rows 11.7 and 10.6, 2048 rows
+  // 21.2 and 19.8.
   const bool few = a.m <= 512;
   if (nc <= 64) return norm_nt<DT, 64, 1>(a, s);
   if (nc <= 128) return norm_nt<DT, 128, 1>(a, s);
