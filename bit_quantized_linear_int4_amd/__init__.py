@@ -27,9 +27,11 @@ __all__ = [
     "FMT_FP8_BLOCK", "wq_add_rmsnorm", "wq_quantize_fp8_rows", "wq_quantize_fp8_block",
     "wq_linear_fp8_workspace", "wq_linear_fp8", "alloc_fp8", "alloc_fp8_rows",
     "wq_moe_workspace", "wq_moe",
+    "E4M3", "KVCache", "alloc_kv_cache", "wq_append_kv", "wq_attention_decode_workspace",
+    "wq_attention_decode", "wq_attention_prompt_workspace", "wq_attention_prompt",
 ]
 
-F16, BF16, F32 = 0, 1, 2
+F16, BF16, F32, E4M3 = 0, 1, 2, 3       # E4M3: key-value caches only
 FMT_INT4_ASYM, FMT_NF4, FMT_INT8_SYM_ROW, FMT_FP4, FMT_FP8_BLOCK = 0, 1, 2, 3, 4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -58,6 +60,17 @@ class _Weight(ctypes.Structure):
     ]
 
 
+class _Cache(ctypes.Structure):
+    _fields_ = [
+        ("dt", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+    ]
+
+
 def library_path():
     return _LIB_PATH
 
@@ -71,7 +84,7 @@ def _load():
                           "or python -m bit_quantized_linear_int4_amd._build")
     lib = ctypes.CDLL(_LIB_PATH)
     c_i32, c_i64, c_vp, c_f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
-    wp = ctypes.POINTER(_Weight)
+    wp, cp = ctypes.POINTER(_Weight), ctypes.POINTER(_Cache)
     sig = {
         "wq_quantize_groupwise": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i32, c_i32, c_i32,
                                           c_vp, c_vp, c_vp, c_vp]),
@@ -106,6 +119,16 @@ def _load():
         "wq_moe_workspace": (ctypes.c_size_t, [c_i64, c_i32, wp, c_i64]),
         "wq_moe": (c_i32, [c_vp, c_i32, c_i64, c_vp, c_vp, c_i64, c_i32, c_i32, wp, wp, wp, c_vp,
                            c_i32, c_vp, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+        "wq_append_kv": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                 c_vp, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp, cp, c_vp]),
+        "wq_attention_decode_workspace": (ctypes.c_size_t, [c_i64, c_i64, cp]),
+        "wq_attention_decode": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, cp, c_vp, c_i64, c_i64,
+                                        c_vp, c_f, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                        ctypes.c_size_t, c_vp]),
+        "wq_attention_prompt_workspace": (ctypes.c_size_t, [c_i64, c_i64, c_i64, cp]),
+        "wq_attention_prompt": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i64, cp, c_vp,
+                                        c_i64, c_i64, c_vp, c_f, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                        ctypes.c_size_t, c_vp]),
         "wq_status_string": (ctypes.c_char_p, [c_i32]),
     }
     for name, (res, args) in sig.items():
@@ -731,6 +754,214 @@ def wq_moe(x, router, top_k, gate, up, down, y, workspace, renormalize=True, log
                         ctypes.byref(dd), _ptr(y), _dt(y), _ptr(ids), _ptr(probs),
                         _ptr(workspace), _nbytes(workspace), _stream(stream, x))
     _check(st, what)
+
+
+class KVCache:
+    """A paged cache: k and v [pages][kv_heads][page_size][head_dim] in a 16-bit type or
+    E4M3 (then with fp32 scales [pages][kv_heads][page_size] of each), any view of a
+    tensor with contiguous heads (for example the transpose of [pages][page_size]
+    [kv_heads][head_dim]), the same strides for both.  The tensors are checked and their
+    addresses taken here, once; other tensors are another KVCache."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "shape", "device_index", "_desc",
+                 "_ref")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        what = "KVCache"
+        if k is None or k.dim() != 4 or v is None or v.shape != k.shape or v.dtype != k.dtype:
+            _fail(what, "k and v must be [pages][kv_heads][page_size][head_dim] of one type")
+        dtype, dev, shape, strides = k.dtype, k.get_device(), k.shape, k.stride()
+        pages, kv, page, d = shape
+        e4m3, f32, _, _ = _types()
+        if dtype in e4m3:
+            dt = E4M3
+            _need(what, "k_scales", k_scales, (pages, kv, page), f32, dev)
+            _need(what, "v_scales", v_scales, (pages, kv, page), f32, dev)
+        else:
+            dt = _dt(k)
+            if dt == F32:
+                _fail(what, f"k has dtype {dtype}", _ERR_UNSUP)
+            if k_scales is not None or v_scales is not None:
+                _fail(what, "a 16-bit cache has no scales", _ERR_UNSUP)
+        if strides[3] != 1 and d != 1:
+            _fail(what, "the components of a head are not contiguous")
+        vs = v.stride()
+        if vs != strides and any(a != b and n > 1 for a, b, n in zip(strides, vs, shape)):
+            _fail(what, "k and v have different strides")
+        if v.get_device() != dev:
+            _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.dtype, self.shape, self.device_index = dtype, shape, dev
+        self._desc = _Cache(dt, kv, d, page, pages, strides[0], strides[1], strides[2],
+                            k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales))
+        self._ref = ctypes.byref(self._desc)
+
+    def nbytes(self):
+        return sum(t.nbytes for t in (self.k, self.v, self.k_scales, self.v_scales)
+                   if t is not None)
+
+
+def alloc_kv_cache(pages, kv_heads, page_size, head_dim, dtype, device="cuda"):
+    """An empty cache of float16, bfloat16 or float8_e4m3fn (or uint8: E4M3 codes)."""
+    import torch
+    shape = (pages, kv_heads, page_size, head_dim)
+    k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype not in _types()[0]:
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.empty(shape[:3], dtype=torch.float32, device=device)
+                           for _ in range(2)))
+
+
+_current = None
+
+
+def _run(dev, fn, *args):
+    """fn(*args) with the tensors' device current: that is where a launch goes."""
+    global _current
+    if _current is None:
+        import torch
+        _current = torch._C._cuda_getDevice
+    if _current() == dev:
+        return fn(*args)
+    import torch
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _head_rows(what, name, t, d, dtype, dev):
+    """(rows, heads, stride of the rows) of [rows][heads][d] whose heads are contiguous."""
+    if t is None or t.dim() != 3:
+        _fail(what, f"{name} must be a 3-D [rows][heads][head_dim] tensor")
+    m, h, dd = t.shape
+    if dd != d:
+        _fail(what, f"{name} has heads of {dd}, the cache of {d}")
+    ld, s1, s2 = t.stride()
+    if m == 1:
+        ld = h * d
+    if s2 != 1 or (s1 != d and h > 1) or ld < h * d:
+        _fail(what, f"the rows of {name} are not contiguous")
+    if t.dtype != dtype:
+        _fail(what, f"{name} has dtype {t.dtype}, expected {dtype}", _ERR_UNSUP)
+    if t.get_device() != dev:
+        _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+    return m, h, ld
+
+
+def wq_append_kv(q, k, v, cache, slots, positions=None, cos_sin=None, q_out=None,
+                 interleaved=False, stream=None):
+    """q and q_out [m][heads][head_dim], or None and None; k, v [m][kv_heads][head_dim];
+    cos_sin fp32 [max_pos][rot] with positions int32 [m], or None and None: no rotation."""
+    what = "wq_append_kv"
+    _, kv, _, d = cache.shape
+    dev = cache.device_index
+    _, f32, _, i32 = _types()
+    if k is None:
+        _fail(what, "k is required")
+    dtype, dt = k.dtype, _dt(k)
+    m, hk, ldk = _head_rows(what, "k", k, d, dtype, dev)
+    mv, hv, ldv = _head_rows(what, "v", v, d, dtype, dev)
+    if hk != kv or hv != kv or mv != m:
+        _fail(what, f"k and v must hold equal rows of {kv} heads, as the cache")
+    heads = ldq = ldo = 0
+    if q is not None or q_out is not None:
+        mq, heads, ldq = _head_rows(what, "q", q, d, dtype, dev)
+        mo, ho, ldo = _head_rows(what, "q_out", q_out, d, dtype, dev)
+        if mq != m or mo != m or ho != heads:
+            _fail(what, "q and q_out must have the rows of k and equal heads")
+    _need(what, "slots", slots, (m,), i32, dev)
+    rot = max_pos = 0
+    if cos_sin is not None or positions is not None:
+        if cos_sin is None or cos_sin.dim() != 2:
+            _fail(what, "cos_sin must be a 2-D [max_pos][rot] tensor")
+        max_pos, rot = cos_sin.shape
+        _need(what, "cos_sin", cos_sin, (max_pos, rot), f32, dev)
+        _need(what, "positions", positions, (m,), i32, dev)
+    _device(what, k)
+    st = _run(dev, _load().wq_append_kv, _ptr(q), k.data_ptr(), v.data_ptr(), dt, m, heads,
+              ldq, ldk, ldv, _ptr(positions), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0,
+              _ptr(q_out), ldo, slots.data_ptr(), cache._ref, _stream(stream, k))
+    if st != 0:
+        _check(st, what)
+
+
+def _attention(what, q, batch, cache, pages, lens, y, lse, dev):
+    """Checks what both attention calls take; (m, heads, ldq, max_pages, ldp)."""
+    d = cache.shape[3]
+    if q is None:
+        _fail(what, "q is required")
+    m, heads, ldq = _head_rows(what, "q", q, d, q.dtype, dev)
+    _, f32, _, i32 = _types()
+    n, max_pages, ldp = _rows(what, "pages", pages)
+    if batch is None:
+        batch = m
+    if n != batch:
+        _fail(what, f"pages has {n} rows, expected {batch}")
+    if pages.dtype not in i32:
+        _typed(what, "pages", pages, i32)
+    if pages.get_device() != dev:
+        _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+    _need(what, "lens", lens, (batch,), i32, dev)
+    _like(what, "y", y, (m, heads, d), q.dtype, dev)
+    if lse is not None:
+        _need(what, "lse", lse, (m, heads), f32, dev)
+    return m, heads, ldq, max_pages, ldp
+
+
+def _scratch(what, workspace, dev):
+    if workspace is None:
+        return None, 0
+    _dense(what, "workspace", workspace)
+    if workspace.get_device() != dev:
+        _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def wq_attention_decode_workspace(m, heads, cache):
+    return int(_load().wq_attention_decode_workspace(int(m), int(heads), cache._ref))
+
+
+def wq_attention_decode(q, cache, pages, lens, y, workspace=None, scale=None, window=0, sinks=0,
+                        lse=None, stream=None):
+    """q and y [m][heads][head_dim], one row per sequence; pages int32 [m][max_pages] (rows
+    may be apart), lens int32 [m]; scale None: head_dim ** -0.5; window 0: none."""
+    what = "wq_attention_decode"
+    dev = cache.device_index
+    m, heads, ldq, max_pages, ldp = _attention(what, q, None, cache, pages, lens, y, lse, dev)
+    ws, ws_bytes = _scratch(what, workspace, dev)
+    _device(what, q)
+    st = _run(
+        dev, _load().wq_attention_decode, q.data_ptr(), _dt(q), m, heads, ldq, cache._ref,
+        pages.data_ptr(), max_pages, ldp, lens.data_ptr(),
+        cache.shape[3] ** -0.5 if scale is None else scale, window, sinks, y.data_ptr(),
+        _ptr(lse), ws, ws_bytes, _stream(stream, q))
+    if st != 0:
+        _check(st, what)
+
+
+def wq_attention_prompt_workspace(m, heads, batch, cache):
+    return int(_load().wq_attention_prompt_workspace(int(m), int(heads), int(batch), cache._ref))
+
+
+def wq_attention_prompt(q, starts, cache, pages, lens, y, workspace=None, scale=None, window=0,
+                        sinks=0, lse=None, stream=None):
+    """q and y [m][heads][head_dim]; starts int32 [batch + 1], pages int32 [batch][max_pages],
+    lens int32 [batch]; the rest as wq_attention_decode."""
+    what = "wq_attention_prompt"
+    dev = cache.device_index
+    if starts is None or starts.dim() != 1 or starts.shape[0] < 2:
+        _fail(what, "starts must be a 1-D [batch + 1] tensor")
+    batch = starts.shape[0] - 1
+    m, heads, ldq, max_pages, ldp = _attention(what, q, batch, cache, pages, lens, y, lse, dev)
+    _need(what, "starts", starts, (batch + 1,), _types()[3], dev)
+    ws, ws_bytes = _scratch(what, workspace, dev)
+    _device(what, q)
+    st = _run(
+        dev, _load().wq_attention_prompt, q.data_ptr(), _dt(q), m, heads, ldq,
+        starts.data_ptr(), batch, cache._ref, pages.data_ptr(), max_pages, ldp, lens.data_ptr(),
+        cache.shape[3] ** -0.5 if scale is None else scale, window, sinks, y.data_ptr(),
+        _ptr(lse), ws, ws_bytes, _stream(stream, q))
+    if st != 0:
+        _check(st, what)
 
 
 def wq_dequantize(weight, out, stream=None):

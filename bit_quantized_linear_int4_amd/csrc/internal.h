@@ -206,6 +206,51 @@ struct MoeCall {
 size_t moe_ws_bytes(int64_t t, int64_t e, int64_t top_k, int64_t h, int64_t i);
 hipError_t launch_moe(const MoeCall& c, hipStream_t s);
 
+// paged cache of keys and values, as the kernels take it (checked by the ABI layer)
+struct KvCache {
+  char* k;
+  char* v;
+  float* ks;                 // E4M3: [pages][kv_heads][page_size], else nullptr
+  float* vs;
+  int64_t page_stride, head_stride, token_stride;   // bytes
+  int32_t dt, kv_heads, d, lg_page;                 // log2 of page_size
+  int32_t pages;
+};
+
+struct AppendCall {
+  const uint16_t* q;         // or nullptr
+  const uint16_t* k;
+  const uint16_t* v;
+  int dt;
+  int64_t m, heads, ldq, ldk, ldv, ldo;
+  const int32_t* positions;
+  const float* cos_sin;
+  int64_t max_pos;
+  int rot, interleaved;
+  uint16_t* q_out;
+  const int32_t* slots;
+  KvCache cache;
+};
+hipError_t launch_append_kv(const AppendCall& c, hipStream_t s);
+
+struct AttentionCall {
+  const uint16_t* q;
+  int dt;
+  int64_t m, heads, ldq;
+  const int32_t* starts;     // or nullptr: one row per sequence
+  int64_t batch;
+  KvCache cache;
+  const int32_t* pages;
+  int64_t max_pages, ldp;
+  const int32_t* lens;
+  float scale;
+  int32_t window, sinks;     // window INT32_MAX: none
+  uint16_t* y;
+  float* lse;                // or nullptr
+  float* ws;
+};
+hipError_t launch_attention_rows(const AttentionCall& c, hipStream_t s);
+
 hipError_t launch_dequantize(const wq_weight* w, const float* levels16, void* out, int odt,
                              hipStream_t s);
 

@@ -353,6 +353,94 @@ void* device_scratch() {
   return p;
 }
 
+constexpr int64_t kMaxHeads = 1024;
+
+// m rows of `row` elements, ld apart
+bool rows_ok(int64_t m, int64_t row, int64_t ld) {
+  return sizes_ok(m, row) && ld >= row && ld < kMaxDim && ld % 8 == 0;
+}
+
+wq_status check_cache(const wq_kv_cache* c) {
+  if (c == nullptr || c->k == nullptr || c->v == nullptr) return WQ_ERR_NULL;
+  const bool f8 = c->dt == WQ_E4M3;
+  if (!f8 && !is16(c->dt)) return WQ_ERR_UNSUPPORTED;
+  if (f8 && (c->k_scales == nullptr || c->v_scales == nullptr)) return WQ_ERR_NULL;
+  if (!f8 && (c->k_scales != nullptr || c->v_scales != nullptr)) return WQ_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return WQ_ERR_UNSUPPORTED;
+  if (c->kv_heads < 1 || c->kv_heads > kMaxHeads || c->pages < 1) return WQ_ERR_SHAPE;
+  if (c->page_size < 1 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0)
+    return WQ_ERR_SHAPE;
+  if (c->pages > INT32_MAX / c->page_size) return WQ_ERR_SHAPE;
+  struct {
+    int64_t n, stride;
+  } dim[3] = {{c->pages, c->page_stride}, {c->kv_heads, c->head_stride},
+              {c->page_size, c->token_stride}};
+  const int64_t unit = f8 ? 16 : 8;
+  std::sort(dim, dim + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+  int64_t span = c->head_dim;                    // elements that the dimensions so far cover
+  for (const auto& t : dim) {
+    if (t.n == 1) continue;
+    if (t.stride < span || t.stride % unit != 0) return WQ_ERR_SHAPE;
+    if (t.stride > (kMaxElems - span) / (t.n - 1)) return WQ_ERR_SHAPE;
+    span += t.stride * (t.n - 1);
+  }
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 4) ||
+      !aligned(c->v_scales, 4))
+    return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
+KvCache kernel_cache(const wq_kv_cache* c) {
+  const int64_t b = c->dt == WQ_E4M3 ? 1 : 2;
+  // the stride of a dimension of one place is never used: any value may stand there
+  auto bytes = [b](int64_t n, int64_t stride) { return n == 1 ? 0 : stride * b; };
+  return KvCache{static_cast<char*>(c->k), static_cast<char*>(c->v), c->k_scales, c->v_scales,
+                 bytes(c->pages, c->page_stride), bytes(c->kv_heads, c->head_stride),
+                 bytes(c->page_size, c->token_stride), c->dt, c->kv_heads, c->head_dim,
+                 __builtin_ctz((unsigned)c->page_size), (int32_t)c->pages};
+}
+
+bool attention_sizes_ok(int64_t m, int64_t heads, const wq_kv_cache* cache) {
+  return check_cache(cache) == WQ_OK && heads >= 1 && heads <= kMaxHeads &&
+         heads % cache->kv_heads == 0 && sizes_ok(m, heads * cache->head_dim);
+}
+
+// the checks that both attention calls share; fills everything but starts and ws
+wq_status check_attention(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
+                          int64_t batch, const wq_kv_cache* cache, const int32_t* pages,
+                          int64_t max_pages, int64_t ldp, const int32_t* lens, float scale,
+                          int64_t window, int64_t sinks, void* y, float* lse, AttentionCall* c) {
+  if (q == nullptr || pages == nullptr || lens == nullptr || y == nullptr) return WQ_ERR_NULL;
+  const wq_status st = check_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!is16(dt) || (cache->dt != WQ_E4M3 && cache->dt != dt)) return WQ_ERR_UNSUPPORTED;
+  if (!attention_sizes_ok(m, heads, cache) || !rows_ok(m, heads * cache->head_dim, ldq))
+    return WQ_ERR_SHAPE;
+  if (batch < 1 || batch >= kMaxDim || !sizes_ok(batch, max_pages) || ldp < max_pages ||
+      ldp >= kMaxDim)
+    return WQ_ERR_SHAPE;
+  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return WQ_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(pages, 4) || !aligned(lens, 4) || !aligned(y, 16) ||
+      !aligned(lse, 4))
+    return WQ_ERR_ALIGN;
+  auto i32 = [](int64_t v) { return (int32_t)std::min<int64_t>(v, INT32_MAX); };
+  *c = AttentionCall{static_cast<const uint16_t*>(q), dt, m, heads, ldq, nullptr, batch,
+                     kernel_cache(cache), pages, max_pages, ldp, lens, scale,
+                     window == 0 ? INT32_MAX : i32(window), i32(sinks),
+                     static_cast<uint16_t*>(y), lse, nullptr};
+  return WQ_OK;
+}
+
+wq_status run_attention(AttentionCall* c, void* workspace, size_t ws_bytes, size_t need,
+                        void* stream) {
+  if (need > 0) {
+    if (workspace == nullptr || ws_bytes < need) return WQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
+  }
+  c->ws = static_cast<float*>(workspace);
+  return hip_status(launch_attention_rows(*c, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -521,6 +609,79 @@ wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, cons
                   renormalize ? 1 : 0, static_cast<const uint16_t*>(router), logits, gate, up,
                   down, y, ydt, ids, probs, workspace};
   return hip_status(launch_moe(c, static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, int64_t m,
+                       int64_t heads, int64_t ldq, int64_t ldk, int64_t ldv,
+                       const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                       int64_t rot, int32_t interleaved, void* q_out, int64_t ldo,
+                       const int32_t* slots, const wq_kv_cache* cache, void* stream) {
+  if (k == nullptr || v == nullptr || slots == nullptr || (q == nullptr) != (q_out == nullptr))
+    return WQ_ERR_NULL;
+  const wq_status st = check_cache(cache);
+  if (st != WQ_OK) return st;
+  if (rot != 0 && (positions == nullptr || cos_sin == nullptr)) return WQ_ERR_NULL;
+  if (!is16(dt) || (cache->dt != WQ_E4M3 && cache->dt != dt)) return WQ_ERR_UNSUPPORTED;
+  if (interleaved != 0 && interleaved != 1) return WQ_ERR_UNSUPPORTED;
+  const int64_t d = cache->head_dim;
+  if (rot < 0 || rot > d || rot % 16 != 0) return WQ_ERR_SHAPE;
+  if (rot != 0 && (max_pos < 1 || max_pos > INT32_MAX || max_pos > kMaxElems / rot))
+    return WQ_ERR_SHAPE;
+  if (!rows_ok(m, cache->kv_heads * d, ldk) || !rows_ok(m, cache->kv_heads * d, ldv))
+    return WQ_ERR_SHAPE;
+  if (q != nullptr && (heads < 1 || heads > kMaxHeads || !rows_ok(m, heads * d, ldq) ||
+                       !rows_ok(m, heads * d, ldo)))
+    return WQ_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(positions, 4) || !aligned(cos_sin, 16) || !aligned(slots, 4))
+    return WQ_ERR_ALIGN;
+  const AppendCall c{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                     static_cast<const uint16_t*>(v), dt, m, q == nullptr ? 0 : heads, ldq, ldk,
+                     ldv, ldo, positions, cos_sin, max_pos, (int)rot, interleaved,
+                     static_cast<uint16_t*>(q_out), slots, kernel_cache(cache)};
+  return hip_status(launch_append_kv(c, static_cast<hipStream_t>(stream)));
+}
+
+size_t wq_attention_decode_workspace(int64_t m, int64_t heads, const wq_kv_cache* cache) {
+  if (!attention_sizes_ok(m, heads, cache)) return 0;
+  return 0;
+}
+
+size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,
+                                     const wq_kv_cache* cache) {
+  if (!attention_sizes_ok(m, heads, cache) || batch < 1 || batch >= kMaxDim) return 0;
+  return 0;
+}
+
+wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
+                              const wq_kv_cache* cache, const int32_t* pages, int64_t max_pages,
+                              int64_t ldp, const int32_t* lens, float scale, int64_t window,
+                              int64_t sinks, void* y, float* lse, void* workspace,
+                              size_t ws_bytes, void* stream) {
+  AttentionCall c;
+  const wq_status st = check_attention(q, dt, m, heads, ldq, m, cache, pages, max_pages, ldp, lens,
+                                       scale, window, sinks, y, lse, &c);
+  if (st != WQ_OK) return st;
+  c.starts = nullptr;
+  return run_attention(&c, workspace, ws_bytes, wq_attention_decode_workspace(m, heads, cache),
+                       stream);
+}
+
+wq_status wq_attention_prompt(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
+                              const int32_t* starts, int64_t batch, const wq_kv_cache* cache,
+                              const int32_t* pages, int64_t max_pages, int64_t ldp,
+                              const int32_t* lens, float scale, int64_t window, int64_t sinks,
+                              void* y, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  if (starts == nullptr) return WQ_ERR_NULL;
+  AttentionCall c;
+  const wq_status st = check_attention(q, dt, m, heads, ldq, batch, cache, pages, max_pages, ldp,
+                                       lens, scale, window, sinks, y, lse, &c);
+  if (st != WQ_OK) return st;
+  if (!aligned(starts, 4)) return WQ_ERR_ALIGN;
+  c.starts = starts;
+  return run_attention(&c, workspace, ws_bytes,
+                       wq_attention_prompt_workspace(m, heads, batch, cache), stream);
 }
 
 wq_status wq_dequantize(const wq_weight* w, void* out, int32_t odt, void* stream) {

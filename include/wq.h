@@ -62,7 +62,7 @@ typedef enum {
   WQ_ERR_HIP = 6          /* a kernel launch failed                           */
 } wq_status;
 
-typedef enum { WQ_F16 = 0, WQ_BF16 = 1, WQ_F32 = 2 } wq_dtype;
+typedef enum { WQ_F16 = 0, WQ_BF16 = 1, WQ_F32 = 2, WQ_E4M3 = 3 /* caches only */ } wq_dtype;
 
 typedef enum {
   WQ_FMT_INT4_ASYM = 0,   /* wq_quantize_groupwise(bits=4, symmetric=0)       */
@@ -457,6 +457,117 @@ wq_status wq_moe(const void* x, int32_t xdt, int64_t m, const void* router, cons
                  int64_t experts, int32_t top_k, int32_t renormalize, const wq_weight* gate,
                  const wq_weight* up, const wq_weight* down, void* y, int32_t ydt, int32_t* ids,
                  float* probs, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A paged cache of the keys and values of one layer, written by wq_append_kv and
+ * read by the attention calls below.  It has `pages` pages of page_size tokens;
+ * token t of a page p, head h and component c of k and of v are element
+ *   p * page_stride + h * head_stride + t * token_stride + c
+ * (strides in elements, the same for k and v), so a page may hold its heads or its
+ * tokens outermost.  A slot is page * page_size + place of the token in the page.
+ *  dt          WQ_F16, WQ_BF16, or WQ_E4M3: codes with one fp32 scale per token and
+ *              head, k_scales and v_scales fp32 [pages][kv_heads][page_size]
+ *              (NULL for the 16-bit types)
+ *  head_dim    64 or 128
+ *  page_size   a power of two, at most 65536; pages * page_size below 2^31
+ *  strides     multiples of 16 bytes, such that no two places overlap; k and v span
+ *              at most 2^34 elements each
+ * k and v 16-byte, scales 4-byte aligned.
+ */
+typedef struct {
+  int32_t dt;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t pages;
+  int64_t page_stride, head_stride, token_stride;
+  void* k;
+  void* v;
+  float* k_scales;
+  float* v_scales;
+} wq_kv_cache;
+
+/*
+ * Rotary rotation of queries and keys, and append of keys and values to the cache.
+ *   (c, s) = cos_sin[positions[row]][i], [rot/2 + i];  for every pair i < rot/2 of a
+ *   head, (a, b) = elements (i, i + rot/2), or (2i, 2i + 1) when interleaved != 0:
+ *     a' = a c - b s,  b' = b c + a s         (fp32; the head's other elements stay)
+ *   q_out = round(q'),  k of the slot = k', v of the slot = v: rounded to 16 bits, or
+ *   for WQ_E4M3  scale = max|.| / 448 over the head (1 if 0; at least 2^-126),
+ *   code = E4M3(. / scale) of the unrounded values (as wq_add_rmsnorm's q).
+ * q [m][heads][head_dim], k and v [m][kv_heads][head_dim] in dt in {F16, BF16}, rows
+ * ldq, ldk, ldv elements apart (so they may be parts of one projection's output);
+ * q_out in dt, rows ldo apart, may be q with ldo == ldq (in place), and overlaps no
+ * other input otherwise; q and q_out are both given or both NULL.  cos_sin fp32
+ * [max_pos][rot], positions int32 [m]; both NULL when rot == 0; a position outside
+ * [0, max_pos) is taken as the nearest one inside.  slots int32 [m]: a row whose
+ * slot is negative or past the cache is not stored (its q_out is written); slots
+ * that occur twice in one call hold a mix of their rows.
+ * A 16-bit cache has dt; rot a multiple of 16, at most head_dim; ldq, ldk, ldv, ldo
+ * multiples of 8, at least a row's elements; kv_heads and heads at most 1024; q, k,
+ * v, q_out, cos_sin 16-byte, positions and slots 4-byte aligned.  NaN and infinities
+ * stay in their head, and follow wq_quantize_fp8_rows in an E4M3 cache.
+ */
+wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, int64_t m,
+                       int64_t heads, int64_t ldq, int64_t ldk, int64_t ldv,
+                       const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                       int64_t rot, int32_t interleaved, void* q_out, int64_t ldo,
+                       const int32_t* slots, const wq_kv_cache* cache, void* stream);
+
+/*
+ * Attention of one new token for each of m sequences over the cache.  Query head h
+ * reads kv head h / (heads / kv_heads).  For row i with n = lens[i] tokens, the new
+ * one (at n - 1, already in the cache) among them:
+ *   visible: j < n and (window == 0 or n - 1 - j < window or j < sinks)
+ *   z_j = scale * q . k_j,  y = sum_j exp(z_j) v_j / sum_j exp(z_j),
+ *   lse = log sum_j exp(z_j)                  (sums over the visible j)
+ * A row that sees nothing (n <= 0) gets y = 0 and lse = -inf.  z and all sums are
+ * fp32 and the order of every sum is fixed by the sizes and lens: results are
+ * deterministic.  The weights of v are kept to 16 significant bits.
+ *
+ * q [m][heads][head_dim] in dt in {F16, BF16}, rows ldq elements apart; a 16-bit
+ * cache has dt.  pages int32 [m] rows of max_pages, ldp apart: token j of row i is
+ * in page pages[i][j / page_size] at j % page_size.  Entries behind a row's last
+ * token are not used; an entry outside the cache is taken as the nearest page
+ * inside, lens past max_pages * page_size as that.  Places that no row sees are
+ * not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32 [m][heads] or NULL.
+ * A query, key or scale that is not finite makes what it enters not finite or, where
+ * its z is -inf, leaves it out; a value that is not finite makes the components that
+ * it enters not finite.  No other row is touched by it.
+ * heads a multiple of kv_heads, at most 1024; ldq a multiple of 8; window and sinks
+ * >= 0; scale > 0, finite; q and y 16-byte, pages, lens, lse 4-byte aligned.
+ * workspace: at least wq_attention_decode_workspace(m, heads, cache) bytes, 256-byte
+ * aligned; the query gives 0 for arguments that the call refuses.
+ */
+size_t wq_attention_decode_workspace(int64_t m, int64_t heads, const wq_kv_cache* cache);
+wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
+                              const wq_kv_cache* cache, const int32_t* pages, int64_t max_pages,
+                              int64_t ldp, const int32_t* lens, float scale, int64_t window,
+                              int64_t sinks, void* y, float* lse, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention of several new tokens for each of `batch` sequences: sequence b
+ * has the rows starts[b] .. starts[b+1] - 1 of q, the last of its lens[b] tokens
+ * (all of them in the cache), so row r of it is at lens[b] - starts[b+1] + r.
+ * Formula, arguments and limits as wq_attention_decode, with a row's own position in
+ * the place of n - 1: it sees j at or before its position.  A row at a negative
+ * position sees nothing (y = 0, lse = -inf).  Rows of q before starts[0] or from
+ * starts[batch] on are not read, and y and lse not written there.
+ * starts int32 [batch + 1], ascending, within [0, m]; lens int32 [batch]; pages
+ * int32 [batch] rows of max_pages.  The weights of v are rounded to dt (bf16 for
+ * WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), the sum of weights is not.
+ * workspace: at least wq_attention_prompt_workspace(m, heads, batch, cache) bytes,
+ * 256-byte aligned (may be NULL when that is 0).
+ */
+size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,
+                                     const wq_kv_cache* cache);
+wq_status wq_attention_prompt(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
+                              const int32_t* starts, int64_t batch, const wq_kv_cache* cache,
+                              const int32_t* pages, int64_t max_pages, int64_t ldp,
+                              const int32_t* lens, float scale, int64_t window, int64_t sinks,
+                              void* y, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream);
 
 /*
  * Dequantize a whole weight into 16-bit values (a test and debugging hook;
