@@ -1,0 +1,77 @@
+// Device helpers shared by the attention kernels.
+#pragma once
+
+#include "fp8_util.h"
+
+namespace wq {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+typedef float float16v_t __attribute__((ext_vector_type(16)));
+
+// What a row at `pos` sees of its sequence: the tokens [0, first) and [from, pos],
+// `n` in all; visible token i is token i for i < first, else i - first + from.
+struct Visible {
+  int first, from, n;
+};
+__device__ __forceinline__ Visible visible_of(int pos, int window, int sinks) {
+  Visible v;
+  v.from = pos >= window ? pos - window + 1 : 0;
+  v.first = min(sinks, v.from);
+  v.n = pos < 0 ? 0 : pos + 1 - v.from + v.first;
+  return v;
+}
+
+// tokens of sequence i: lens[i] within what its row of the page table holds
+__device__ __forceinline__ int tokens_of(const AttentionCall& a, int64_t i) {
+  const int64_t room = a.max_pages << a.cache.lg_page;
+  return (int)min((int64_t)max(a.lens[i], 0), room);
+}
+
+__device__ __forceinline__ int page_of(const AttentionCall& a, const int32_t* table, int token) {
+  return min(max(table[token >> a.cache.lg_page], 0), a.cache.pages - 1);
+}
+
+template <int T>
+__device__ __forceinline__ float4_t mfma16(uint4_t a, uint4_t b, float4_t c) {
+  if constexpr (T == WQ_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+
+// four E4M3 codes -> four 16-bit values (exact)
+template <int T>
+__device__ __forceinline__ uint2_t widen4(uint32_t w) {
+  uint2_t r;
+  if constexpr (T == WQ_BF16) {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+  } else {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+  }
+  return r;
+}
+
+// a value of this lane and of the lanes 16, 32 and 48 away
+__device__ __forceinline__ float max_quarters(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_quarters(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The reference of exponents: the running maximum, or 0 where nothing counted yet
+// (all z so far are -inf, and exp2 of them stays 0).
+__device__ __forceinline__ float exp_ref(float m) { return m == -INFINITY ? 0.0f : m; }
+
+}  // namespace wq

@@ -3,12 +3,10 @@
 // One wave per row and query head.  A head of D components is D / 8 lanes of 8;
 // the 512 / D groups of lanes take the visible tokens in turn, each with a running
 // maximum and sums of its own, and are joined at the end.
-#include "fp8_util.h"
+#include "attention.h"
 
 namespace wq {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // 8 components from p: 16 bytes of a 16-bit type, or 8 of E4M3
 template <int CT>
@@ -130,7 +128,7 @@ hipError_t rows_d(const AttentionCall& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attention_rows(const AttentionCall& a, hipStream_t s) {
+hipError_t launch_attention_prompt(const AttentionCall& a, hipStream_t s) {
   return a.dt == WQ_BF16 ? rows_d<WQ_BF16>(a, s) : rows_d<WQ_F16>(a, s);
 }
 

@@ -249,7 +249,10 @@ struct AttentionCall {
   float* lse;                // or nullptr
   float* ws;
 };
-hipError_t launch_attention_rows(const AttentionCall& c, hipStream_t s);
+constexpr int kDecodeMaxWgs = 512;
+size_t decode_ws_bytes(int64_t m, int64_t heads, const KvCache& c);
+hipError_t launch_attention_decode(const AttentionCall& c, hipStream_t s);
+hipError_t launch_attention_prompt(const AttentionCall& c, hipStream_t s);
 
 hipError_t launch_dequantize(const wq_weight* w, const float* levels16, void* out, int odt,
                              hipStream_t s);

@@ -417,7 +417,7 @@ wq_status check_attention(const void* q, int32_t dt, int64_t m, int64_t heads, i
   if (!attention_sizes_ok(m, heads, cache) || !rows_ok(m, heads * cache->head_dim, ldq))
     return WQ_ERR_SHAPE;
   if (batch < 1 || batch >= kMaxDim || !sizes_ok(batch, max_pages) || ldp < max_pages ||
-      ldp >= kMaxDim)
+      ldp >= kMaxDim || max_pages > (int64_t(1) << 30) / cache->page_size)
     return WQ_ERR_SHAPE;
   if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return WQ_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(pages, 4) || !aligned(lens, 4) || !aligned(y, 16) ||
@@ -438,7 +438,9 @@ wq_status run_attention(AttentionCall* c, void* workspace, size_t ws_bytes, size
     if (!aligned(workspace, 256)) return WQ_ERR_ALIGN;
   }
   c->ws = static_cast<float*>(workspace);
-  return hip_status(launch_attention_rows(*c, static_cast<hipStream_t>(stream)));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return hip_status(c->starts == nullptr ? launch_attention_decode(*c, s)
+                                         : launch_attention_prompt(*c, s));
 }
 
 }  // namespace
@@ -644,7 +646,7 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
 
 size_t wq_attention_decode_workspace(int64_t m, int64_t heads, const wq_kv_cache* cache) {
   if (!attention_sizes_ok(m, heads, cache)) return 0;
-  return 0;
+  return decode_ws_bytes(m, heads, kernel_cache(cache));
 }
 
 size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,

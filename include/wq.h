@@ -529,8 +529,8 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
  * cache has dt.  pages int32 [m] rows of max_pages, ldp apart: token j of row i is
  * in page pages[i][j / page_size] at j % page_size.  Entries behind a row's last
  * token are not used; an entry outside the cache is taken as the nearest page
- * inside, lens past max_pages * page_size as that.  Places that no row sees are
- * not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32 [m][heads] or NULL.
+ * inside, lens past max_pages * page_size (at most 2^30) as that.  Places that no row
+ * sees are not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32 [m][heads] or NULL.
  * A query, key or scale that is not finite makes what it enters not finite or, where
  * its z is -inf, leaves it out; a value that is not finite makes the components that
  * it enters not finite.  No other row is touched by it.

@@ -106,6 +106,8 @@ def test_attention_errors(make):
     assert call(ldq=504) == SHAPE and call(ldq=516) == SHAPE and call(ldq=1 << 23) == SHAPE
     assert call(max_pages=0) == SHAPE and call(max_pages=4) == SHAPE
     assert call(max_pages=1 << 23, ldp=1 << 23) == SHAPE and call(ldp=1 << 23) == SHAPE
+    wide = dict(cache=ctypes.byref(cache(page=1024, ps=1024 * 256, hs=1024 * 128)))
+    assert call(**wide, max_pages=(1 << 20) + 1, ldp=(1 << 20) + 1) == SHAPE
     for s in (0.0, -0.1, float("nan"), float("inf")):
         assert call(scale=s) == SHAPE
     assert call(window=-1) == SHAPE and call(sinks=-1) == SHAPE
