@@ -22,10 +22,17 @@ __device__ __forceinline__ Visible visible_of(int pos, int window, int sinks) {
   return v;
 }
 
-// tokens of sequence i: lens[i] within what its row of the page table holds
-__device__ __forceinline__ int tokens_of(const AttentionCall& a, int64_t i) {
+// tokens of a sequence: its entry of lens within what its row of the page table holds
+__device__ __forceinline__ int tokens_of(const AttentionCall& a, int len) {
   const int64_t room = a.max_pages << a.cache.lg_page;
-  return (int)min((int64_t)max(a.lens[i], 0), room);
+  return (int)min((int64_t)max(len, 0), room);
+}
+
+// p[i] with an i that is the same in every lane, as a scalar load: a vector load would
+// wait behind all loads in flight
+__device__ __forceinline__ int scalar_at(const int32_t* p, int i) {
+  using C = const __attribute__((address_space(4))) int32_t*;
+  return ((C)(uintptr_t)p)[__builtin_amdgcn_readfirstlane(i)];
 }
 
 __device__ __forceinline__ int page_of(const AttentionCall& a, const int32_t* table, int token) {
