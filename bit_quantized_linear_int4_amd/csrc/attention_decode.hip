@@ -183,8 +183,10 @@ template <int DT, int CT, int D>
 __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   constexpr bool F8 = CT == WQ_E4M3;
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
-  // weights of f16 are kept 2^15 larger, away from its subnormal range
-  constexpr float kShift = VT == WQ_F16 ? 15.0f : 0.0f;
+  // Exponents are taken from a reference that follows the running maximum only where it
+  // is passed by more than 2^8, so that the sums are rarely rescaled.  Weights of f16 are
+  // kept 2^7 larger: at most 2^15, and away from its subnormal range.
+  constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
   constexpr int KC = Tile<CT, D>::KC, VW = Tile<CT, D>::VW;
   constexpr int NI = D / 16;                             // O^T tiles, components of a lane
   constexpr int OS = D + 4;                              // LDS row of O, in floats
@@ -331,39 +333,50 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) z[4 * s + r] = acc[r] * zscale;
+      for (int r = 0; r < 4; ++r) z[4 * s + r] = acc[r];
     }
+    // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
     float vs[8];
+    if constexpr (F8) {
+      const float ts = lane < 32 ? t.scale * zscale : t.scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int tok = 4 * kq + (i < 4 ? i : 12 + i);
-      if constexpr (F8) {
-        z[i] *= __int_as_float(__builtin_amdgcn_ds_bpermute(tok * 4, __float_as_int(t.scale)));
-        vs[i] = __int_as_float(__builtin_amdgcn_ds_bpermute(tok * 4 + 128,
-                                                            __float_as_int(t.scale)));
+      for (int i = 0; i < 8; ++i) {
+        const int tok = 4 * kq + (i < 4 ? i : 12 + i);
+        z[i] *= __int_as_float(__builtin_amdgcn_ds_bpermute(tok * 4, __float_as_int(ts)));
+        vs[i] = __int_as_float(__builtin_amdgcn_ds_bpermute(tok * 4 + 128, __float_as_int(ts)));
       }
-      z[i] = tok < count ? z[i] : -INFINITY;
+    }
+    const float unit = F8 ? 1.0f : zscale;
+    if (count < 32) {                                    // tokens past the end repeat the last
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool live = 4 * kq + (i < 4 ? i : 12 + i) < count;
+        z[i] = live ? z[i] : -INFINITY;
+        if constexpr (F8) vs[i] = live ? vs[i] : 0.0f;   // it may not be finite
+      }
     }
     float big = z[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) big = fmaxf(big, z[i]);
-    const float mn = fmaxf(m, max_quarters(big)), ref = exp_ref(mn) - kShift;
-    const float fade = __builtin_amdgcn_exp2f(m - (ref + kShift));
-    m = mn;
+    big = max_quarters(big) * unit;
+    if (__any(big > m + kLag)) {
+      const float mn = fmaxf(m, big), fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
+      m = mn;
+      l *= fade;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) o[i] *= fade;
+    }
+    const float ref = exp_ref(m) - kShift;
     float p[8], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(z[i] - ref);
+      p[i] = __builtin_amdgcn_exp2f(F8 ? z[i] - ref : fmaf(z[i], unit, -ref));
       sum += p[i];
     }
-    l = l * fade + sum;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) o[i] *= fade;
+    l += sum;
     if constexpr (F8) {
-      // a token past the end repeats the last one, whose scale may not be finite
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        p[i] = 4 * kq + (i < 4 ? i : 12 + i) < count ? p[i] * vs[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) p[i] *= vs[i];
     }
     // two parts of 8 (bf16) or 11 bits: against one part, whose rounding is as large as
     // that of a 16-bit y, this costs matrix instructions that wait for HBM anyway
@@ -597,7 +610,7 @@ hipError_t decode_go(const AttentionCall& a, hipStream_t s) {
   decode_kernel<DT, CT, D><<<dim3((unsigned)wgs), 256, 0, s>>>(args);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;           // nothing is in parts
-  constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 15.0f : 0.0f;
+  constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
   decode_join_kernel<DT, D>
       <<<dim3((unsigned)a.m, (unsigned)a.heads), 256, 0, s>>>(args, wgs, kShift);
   return hipGetLastError();
