@@ -27,8 +27,18 @@ namespace {
 constexpr int kStep = 128;             // tokens of a workgroup's step: 4 waves of 32
 constexpr int kRows = 16;              // query heads of an item
 
+// What the join is to do for an item: its parts are workgroup `wg`'s second slot, the
+// next ones' second and the last one's first.  Fewer than two parts: nothing.
+struct Joined {
+  int wg, seq, head, rows_parts;       // rows << 16 | parts
+};
+
 struct DecodeArgs {
   AttentionCall a;
+  // behind the parts in the workspace: per item where there are no more items than
+  // workgroups, else per workgroup, for the item that starts in its stretch and goes on
+  Joined* joined;
+  int per_item;
   int group, tiles;                    // query heads per kv head; items of 16 of them
   int lg_unit;                         // log2 of a unit's tokens
   uint32_t page16, token16;            // strides in 16 bytes; a cache spans less than 2^31
@@ -37,8 +47,20 @@ struct DecodeArgs {
 __device__ __forceinline__ Visible decode_visible(const AttentionCall& a, int seq) {
   return visible_of(tokens_of(a, a.lens[seq]) - 1, a.window, a.sinks);
 }
-__device__ __forceinline__ Visible uniform_visible(const AttentionCall& a, int seq) {
-  return visible_of(tokens_of(a, scalar_at(a.lens, seq)) - 1, a.window, a.sinks);
+// the same for a `seq` that is the same in every lane
+template <typename A>
+__device__ __forceinline__ Visible uniform_visible(const A& a, int seq) {
+  const int64_t room = a.max_pages << a.cache.lg_page;
+  const int len = (int)min((int64_t)max(scalar_at(a.lens, seq), 0), room);
+  return visible_of(len - 1, a.window, a.sinks);
+}
+// The kernel's arguments, read where they are used: those of a piece's start and end would
+// otherwise take scalar registers all along, more than there are.
+using DecodeArgsAt = const __attribute__((address_space(4))) DecodeArgs*;
+__device__ __forceinline__ DecodeArgsAt args_here() {
+  auto p = (DecodeArgsAt)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
 }
 __device__ __forceinline__ int units_of(const DecodeArgs& args, const Visible& v) {
   return (v.n + (1 << args.lg_unit) - 1) >> args.lg_unit;
@@ -65,9 +87,10 @@ __device__ __forceinline__ int scan64(int v) {           // inclusive, over the 
 __device__ __forceinline__ Line line_up(const DecodeArgs& args, int* part) {
   const AttentionCall& a = args.a;
   const int m = (int)a.m, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (m == 1) return Line{units_of(args, uniform_visible(a, 0)), 0};
   if (m <= 64) {
     const int own = lane < m ? units_of(args, decode_visible(a, min(lane, m - 1))) : 0;
-    const int sum = m == 1 ? own : scan64(own);
+    const int sum = scan64(own);
     return Line{__builtin_amdgcn_readlane(sum, m - 1), sum - own};
   }
   const int per = (m + 255) / 256, i0 = tid * per, i1 = min(i0 + per, m);
@@ -92,6 +115,10 @@ __device__ __forceinline__ int line_find(const DecodeArgs& args, const Line& lin
                                          const int* part, int want, int& before) {
   const AttentionCall& a = args.a;
   const int m = (int)a.m;
+  if (m == 1) {
+    before = 0;
+    return 0;
+  }
   if (m <= 64) {
     // the last one that starts at or before it: those of no units share their start
     // with the next, and those past the end start at the total
@@ -112,18 +139,6 @@ __device__ __forceinline__ int line_find(const DecodeArgs& args, const Line& lin
     before += n;
     ++seq;
   }
-}
-
-// units before sequence `seq`
-__device__ __forceinline__ int line_before(const DecodeArgs& args, const Line& line,
-                                           const int* part, int seq) {
-  const int m = (int)args.a.m;
-  if (m <= 64) return __builtin_amdgcn_readlane(line.mine, seq);
-  const int per = (m + 255) / 256;
-  int before = part[seq / per];
-  for (int i = seq / per * per; i < seq; ++i)
-    before += units_of(args, decode_visible(args.a, i));
-  return before;
 }
 
 // `units` of the line over `wgs` workgroups (at most as many): the first `more` take
@@ -208,12 +223,16 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   // rows that see nothing are in no unit
   for (int i = blockIdx.x; i < m_rows; i += gridDim.x) {
     if (uniform_visible(a, i).n > 0) continue;
+    if (args.per_item)
+      for (int e = tid; e < per_unit; e += 256)
+        args.joined[i * per_unit + e] = Joined{0, 0, 0, 0};
     for (int64_t e = tid; e < a.heads * (D / 8); e += 256)
       reinterpret_cast<uint4_t*>(a.y)[i * a.heads * (D / 8) + e] = uint4_t{0, 0, 0, 0};
     if (a.lse != nullptr)
       for (int64_t e = tid; e < a.heads; e += 256) a.lse[i * a.heads + e] = -INFINITY;
   }
 
+  if (!args.per_item && tid == 0) args.joined[blockIdx.x] = Joined{0, 0, 0, 0};
   const int wgs = min((int)gridDim.x, all);              // none without a unit
   if ((int)blockIdx.x >= wgs) return;
   const Share share(all, wgs);
@@ -230,23 +249,38 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   Visible vis;
   int at, end;                                           // visible tokens, from the wave's on
   auto take = [&]() {                                    // the piece that starts at u < u_end
-    vis = uniform_visible(a, seq);
-    int units = units_of(args, vis);
+    const DecodeArgsAt k = args_here();
+    const int lg_unit = k->lg_unit, tiles = k->tiles, per_unit = k->a.cache.kv_heads * tiles;
+    const Share share(all, wgs);
+    const int u_end = share.start(blockIdx.x + 1);
+    auto look = [&]() {
+      const int room = (int)(k->a.max_pages << k->a.cache.lg_page);
+      const int len = min(max(scalar_at(k->a.lens, seq), 0), room);
+      vis = visible_of(len - 1, k->a.window, k->a.sinks);
+      return (vis.n + (1 << lg_unit) - 1) >> lg_unit;
+    };
+    int units = look();
     while (u >= item0 + units * per_unit) {
       item0 += units * per_unit;
-      vis = uniform_visible(a, ++seq);
-      units = units_of(args, vis);
+      ++seq;
+      units = look();
     }
     const int sub = (u - item0) / units;                 // kv head and tile of query heads
-    const int kh = sub / args.tiles, ht = sub - kh * args.tiles;
+    const int kh = sub / tiles, ht = sub - kh * tiles;
     const int first = item0 + sub * units;               // the item's first unit
     const int ua = u - first, ub = min(units, u_end - first);
     ahead.seq = seq;
     ahead.rest = kh << 12 | ht << 4 | (ua == 0 ? Owner::kStarts : 0) |
                  (ub == units ? Owner::kEnds : 0);
-    at = ua << args.lg_unit;
-    end = min(ub << args.lg_unit, vis.n);
+    at = ua << lg_unit;
+    end = min(ub << lg_unit, vis.n);
     u = first + ub;
+    if (ua == 0 && (ub < units || k->per_item) && tid == 0) {
+      const int parts = share.owner(first + units - 1) - (int)blockIdx.x + 1;
+      const int rows = min(kRows, k->group - ht * kRows);
+      k->joined[k->per_item ? seq * per_unit + sub : (int)blockIdx.x] =
+          Joined{(int)blockIdx.x, seq, kh * k->group + ht * kRows, rows << 16 | parts};
+    }
   };
   take();
   auto look_up = [&]() {
@@ -297,9 +331,10 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   // Q^T: lane (row nl, piece kq); rows past the group are zeros
   uint4_t q[D / 32];
   auto load_q = [&](const Owner& p) {
-    const int rows = min(kRows, args.group - p.ht() * kRows);
-    const int64_t head = (int64_t)p.kh() * args.group + p.ht() * kRows + min(nl, rows - 1);
-    const uint16_t* qp = a.q + (int64_t)p.seq * a.ldq + head * D;
+    const DecodeArgsAt k = args_here();
+    const int rows = min(kRows, k->group - p.ht() * kRows);
+    const int64_t head = (int64_t)p.kh() * k->group + p.ht() * kRows + min(nl, rows - 1);
+    const uint16_t* qp = k->a.q + (int64_t)p.seq * k->a.ldq + head * D;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       const int d0 = F8 ? 64 * (c / 2) + 16 * kq + 8 * (c % 2) : 32 * c + 8 * kq;
@@ -418,6 +453,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
 
   // joins the four waves' sums of a piece and starts new ones
   auto finish = [&](const Owner& p) {
+    const DecodeArgsAt k = args_here();
     const bool starts = p.rest & Owner::kStarts, ends = p.rest & Owner::kEnds;
     l = sum_quarters(l);
     if (kq == 0) {
@@ -439,8 +475,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
             float4_t{o[i][r] * f, o[i + 1][r] * f, o[i + 2][r] * f, o[i + 3][r] * f};
     }
     __syncthreads();
-    const int rows = min(kRows, args.group - p.ht() * kRows);
-    float* slot = a.ws + (2 * (int64_t)blockIdx.x + (ends ? 0 : 1)) * (kRows * (D + 2));
+    const int rows = min(kRows, k->group - p.ht() * kRows);
+    float* slot = k->a.ws + (2 * (int64_t)blockIdx.x + (ends ? 0 : 1)) * (kRows * (D + 2));
     for (int e = tid; e < rows * (D / 8); e += 256) {
       const int row = e / (D / 8), c = e % (D / 8);
       float big = sm[0][row], sum = 0.0f, v[8];
@@ -460,10 +496,10 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= inv;
         const int64_t out =
-            (int64_t)p.seq * a.heads + (int64_t)p.kh() * args.group + p.ht() * kRows + row;
-        *reinterpret_cast<uint4_t*>(a.y + out * D + c * 8) = pack8<DT>(v);
-        if (a.lse != nullptr && c == 0)
-          a.lse[out] = sum == 0.0f ? -INFINITY
+            (int64_t)p.seq * k->a.heads + (int64_t)p.kh() * k->group + p.ht() * kRows + row;
+        *reinterpret_cast<uint4_t*>(k->a.y + out * D + c * 8) = pack8<DT>(v);
+        if (k->a.lse != nullptr && c == 0)
+          k->a.lse[out] = sum == 0.0f ? -INFINITY
                                    : (big - kShift + __builtin_amdgcn_logf(sum)) * kLn2;
       } else {
 #pragma unroll
@@ -509,78 +545,72 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   }
 }
 
-// One workgroup per row and query head: the parts of its item.  256 / (D / 4) groups of
-// threads take them in turn, each with a running maximum; four parts are loaded together.
+// A workgroup takes one row of an item.  256 / (D / 4) groups of threads take its parts in turn, each with a running reference; four parts are loaded
+// together.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs args, int most, float shift) {
+__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs args, float shift) {
   const AttentionCall& a = args.a;
   constexpr int L = D / 4, G = 256 / L;
   const int tid = threadIdx.x, c = tid % L, g = tid / L;
-  __shared__ int part[260];
   __shared__ __align__(16) float so[G][D];
   __shared__ float sm[G], sl[G];
-  const int seq = blockIdx.x, head = blockIdx.y, kh = head / args.group;
-  const int ht = (head - kh * args.group) / kRows, row = (head - kh * args.group) % kRows;
-  const int units = units_of(args, uniform_visible(a, seq));
-  const Line line = line_up(args, part);
-  if (units == 0) return;
-  const int per_unit = a.cache.kv_heads * args.tiles, all = line.total * per_unit;
-  const Share share(all, min(most, all));
-  const int first = line_before(args, line, part, seq) * per_unit + (kh * args.tiles + ht) * units;
-  const int w0 = share.owner(first), n = share.owner(first + units - 1) - w0 + 1;
-  if (n == 1) return;                                    // one workgroup had it whole
-  float m = -INFINITY, l = 0.0f;
-  float4_t o = {0, 0, 0, 0};
-  for (int i0 = g; i0 < n; i0 += 4 * G) {
-    float pm[4], pl[4];
-    float4_t po[4];
+  const Joined item = args.joined[blockIdx.x];
+  const int n = item.rows_parts & 0xFFFF, row = blockIdx.y;
+  if (n > 1 && row < item.rows_parts >> 16) {
+    float m = -INFINITY, l = 0.0f;
+    float4_t o = {0, 0, 0, 0};
+    for (int i0 = g; i0 < n; i0 += 4 * G) {
+      float pm[4], pl[4];
+      float4_t po[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = min(i0 + j * G, n - 1);
-      const float* slot =
-          a.ws + (2 * (int64_t)(w0 + i) + (i + 1 < n ? 1 : 0)) * (kRows * (D + 2));
-      po[j] = *reinterpret_cast<const float4_t*>(slot + row * D + c * 4);
-      pm[j] = slot[kRows * D + row];
-      pl[j] = slot[kRows * (D + 1) + row];
+      for (int j = 0; j < 4; ++j) {
+        const int i = min(i0 + j * G, n - 1);
+        const float* slot =
+            a.ws + (2 * (int64_t)(item.wg + i) + (i + 1 < n ? 1 : 0)) * (kRows * (D + 2));
+        po[j] = *reinterpret_cast<const float4_t*>(slot + row * D + c * 4);
+        pm[j] = slot[kRows * D + row];
+        pl[j] = slot[kRows * (D + 1) + row];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool live = i0 + j * G < n;
+        const float mn = fmaxf(m, live ? pm[j] : -INFINITY), ref = exp_ref(mn);
+        const float fade = __builtin_amdgcn_exp2f(m - ref);
+        const float f = live ? __builtin_amdgcn_exp2f(pm[j] - ref) : 0.0f;
+        l = l * fade + (live ? pl[j] * f : 0.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = o[e] * fade + (live ? po[j][e] * f : 0.0f);
+        m = mn;
+      }
     }
+    *reinterpret_cast<float4_t*>(&so[g][c * 4]) = o;
+    if (c == 0) {
+      sm[g] = m;
+      sl[g] = l;
+    }
+    __syncthreads();
+    if (tid < D / 8) {
+      float big = sm[0], sum = 0.0f, x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool live = i0 + j * G < n;
-      const float mn = fmaxf(m, live ? pm[j] : -INFINITY), ref = exp_ref(mn);
-      const float fade = __builtin_amdgcn_exp2f(m - ref);
-      const float f = live ? __builtin_amdgcn_exp2f(pm[j] - ref) : 0.0f;
-      l = l * fade + (live ? pl[j] * f : 0.0f);
+      for (int i = 1; i < G; ++i) big = fmaxf(big, sm[i]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * fade + (live ? po[j][e] * f : 0.0f);
-      m = mn;
+      for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float f = __builtin_amdgcn_exp2f(sm[i] - exp_ref(big));
+        sum += sl[i] * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += so[i][tid * 8 + e] * f;
+      }
+      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;
+      const int64_t out = (int64_t)item.seq * a.heads + item.head + row;
+      *reinterpret_cast<uint4_t*>(a.y + out * D + tid * 8) = pack8<DT>(x);
+      if (a.lse != nullptr && tid == 0)
+        a.lse[out] = sum == 0.0f ? -INFINITY : (big - shift + __builtin_amdgcn_logf(sum)) * kLn2;
     }
   }
-  *reinterpret_cast<float4_t*>(&so[g][c * 4]) = o;
-  if (c == 0) {
-    sm[g] = m;
-    sl[g] = l;
-  }
-  __syncthreads();
-  if (tid >= D / 8) return;
-  float big = sm[0], sum = 0.0f, x[8];
-#pragma unroll
-  for (int i = 1; i < G; ++i) big = fmaxf(big, sm[i]);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const float f = __builtin_amdgcn_exp2f(sm[i] - exp_ref(big));
-    sum += sl[i] * f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += so[i][tid * 8 + e] * f;
-  }
-  const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= inv;
-  const int64_t out = (int64_t)seq * a.heads + head;
-  *reinterpret_cast<uint4_t*>(a.y + out * D + tid * 8) = pack8<DT>(x);
-  if (a.lse != nullptr && tid == 0)
-    a.lse[out] = sum == 0.0f ? -INFINITY : (big - shift + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // Workgroups: two per CU (what their registers allow at a time), no more than there
@@ -603,16 +633,18 @@ hipError_t decode_go(const AttentionCall& a, hipStream_t s) {
   int lg_unit = 7;
   while (((most >> lg_unit) + 1) > (int64_t(1) << 30) / items) ++lg_unit;
   const int64_t units = (most + (int64_t(1) << lg_unit) - 1) >> lg_unit;
-  const DecodeArgs args{a, (int)(a.heads / a.cache.kv_heads), (int)tiles, lg_unit,
+  const int wgs = decode_wgs(items, units);
+  Joined* joined = reinterpret_cast<Joined*>(a.ws + (int64_t)wgs * 2 * kRows * (D + 2));
+  const bool per_item = items <= wgs;
+  const DecodeArgs args{a, joined, per_item, (int)(a.heads / a.cache.kv_heads), (int)tiles, lg_unit,
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
-  const int wgs = decode_wgs(items, units);
   decode_kernel<DT, CT, D><<<dim3((unsigned)wgs), 256, 0, s>>>(args);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;           // nothing is in parts
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
-  decode_join_kernel<DT, D>
-      <<<dim3((unsigned)a.m, (unsigned)a.heads), 256, 0, s>>>(args, wgs, kShift);
+  const dim3 grid((unsigned)(per_item ? items : wgs), (unsigned)std::min(kRows, args.group));
+  decode_join_kernel<DT, D><<<grid, 256, 0, s>>>(args, kShift);
   return hipGetLastError();
 }
 template <int DT, int D>
@@ -627,7 +659,9 @@ hipError_t decode_d(const AttentionCall& a, hipStream_t s) {
 }  // namespace
 
 size_t decode_ws_bytes(int64_t m, int64_t heads, const KvCache& c) {
-  return (size_t)decode_wgs(m * c.kv_heads * decode_tiles(heads, c), INT32_MAX) * 2 * kRows * (c.d + 2) * sizeof(float);
+  const int64_t items = m * c.kv_heads * decode_tiles(heads, c);
+  return (size_t)decode_wgs(items, INT32_MAX) *
+         (2 * kRows * (c.d + 2) * sizeof(float) + sizeof(Joined));
 }
 
 hipError_t launch_attention_decode(const AttentionCall& a, hipStream_t s) {
