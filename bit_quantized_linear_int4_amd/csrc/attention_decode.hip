@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   constexpr int KC = Tile<CT, D>::KC, VW = Tile<CT, D>::VW;
   constexpr int NI = D / 16;                             // O^T tiles, components of a lane
   constexpr int OS = D + 4;                              // LDS row of O, in floats
-  constexpr int NT = F8 || D == 64 ? 3 : 2;              // steps whose tiles are in registers
+  constexpr int NT = F8 && D == 128 ? 3 : 2;             // steps whose tiles are in registers
   const AttentionCall& a = args.a;
   const KvCache& cc = a.cache;
   const int tid = threadIdx.x, lane = tid & 63;
