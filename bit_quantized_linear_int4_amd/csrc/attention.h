@@ -81,4 +81,79 @@ __device__ __forceinline__ float sum_quarters(float v) {
 // (all z so far are -inf, and exp2 of them stays 0).
 __device__ __forceinline__ float exp_ref(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// Counts of the sequences 0 .. m-1, each known to `count(i)`, in a line.  Up to 64
+// sequences every wave scans them by itself, one in a lane; more go through LDS
+// (kLineWords), a block of consecutive ones per thread.  The workgroup has NT threads.
+struct Line {
+  int total;                           // of all sequences
+  int mine;                            // before this lane's sequence (up to 64)
+};
+
+__device__ __forceinline__ int scan64(int v) {           // inclusive, over the wave
+  const int lane = (int)__lane_id();
+#pragma unroll
+  for (int w = 1; w < 64; w *= 2) {
+    const int up = __shfl_up(v, w);
+    if (lane >= w) v += up;
+  }
+  return v;
+}
+
+template <int NT, typename F>
+__device__ __forceinline__ Line line_up(int m, int* part, F count) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (m <= 64) {
+    const int own = lane < m ? count(min(lane, m - 1)) : 0;
+    const int sum = scan64(own);
+    return Line{__builtin_amdgcn_readlane(sum, m - 1), sum - own};
+  }
+  const int per = (m + NT - 1) / NT, i0 = tid * per, i1 = min(i0 + per, m);
+  int own = 0;
+  for (int i = i0; i < i1; ++i) own += count(i);
+  const int sum = scan64(own);
+  if (lane == 63) part[NT + wave] = sum;
+  __syncthreads();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    if (w < wave) base += part[NT + w];
+    total += part[NT + w];
+  }
+  part[tid] = base + sum - own;
+  __syncthreads();
+  return Line{total, 0};
+}
+
+// the sequence that holds place `want` (below the total), and the places before it
+template <int NT, typename F>
+__device__ __forceinline__ int line_find(int m, const Line& line, const int* part, int want,
+                                         int& before, F count) {
+  if (m == 1) {
+    before = 0;
+    return 0;
+  }
+  if (m <= 64) {
+    // the last one that starts at or before it: empty ones share their start with the
+    // next, and those past the end start at the total
+    const int lane = (int)__lane_id();
+    const int seq = 63 - __builtin_clzll(__ballot(lane < m && line.mine <= want));
+    before = __builtin_amdgcn_readlane(line.mine, seq);
+    return seq;
+  }
+  int t = 0;                           // the same among the blocks
+#pragma unroll
+  for (int w = NT / 2; w > 0; w /= 2)
+    if (part[t + w] <= want) t += w;
+  int seq = t * ((m + NT - 1) / NT);
+  before = part[t];
+  for (;;) {
+    const int n = count(seq);
+    if (before + n > want || seq + 1 >= m) return seq;
+    before += n;
+    ++seq;
+  }
+}
+template <int NT>
+constexpr int kLineWords = NT + NT / 64;
+
 }  // namespace wq

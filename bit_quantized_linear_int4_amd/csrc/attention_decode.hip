@@ -66,81 +66,6 @@ __device__ __forceinline__ int units_of(const DecodeArgs& args, const Visible& v
   return (v.n + (1 << args.lg_unit) - 1) >> args.lg_unit;
 }
 
-// The units of the sequences, one kv head and tile of each, in a line.  Up to 64
-// sequences every wave scans them by itself, one in a lane; more go through LDS, a
-// block of consecutive ones per thread.
-struct Line {
-  int total;                           // units of all sequences
-  int mine;                            // units before this lane's sequence (up to 64)
-};
-
-__device__ __forceinline__ int scan64(int v) {           // inclusive, over the wave
-  const int lane = (int)__lane_id();
-#pragma unroll
-  for (int w = 1; w < 64; w *= 2) {
-    const int up = __shfl_up(v, w);
-    if (lane >= w) v += up;
-  }
-  return v;
-}
-
-__device__ __forceinline__ Line line_up(const DecodeArgs& args, int* part) {
-  const AttentionCall& a = args.a;
-  const int m = (int)a.m, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (m == 1) return Line{units_of(args, uniform_visible(a, 0)), 0};
-  if (m <= 64) {
-    const int own = lane < m ? units_of(args, decode_visible(a, min(lane, m - 1))) : 0;
-    const int sum = scan64(own);
-    return Line{__builtin_amdgcn_readlane(sum, m - 1), sum - own};
-  }
-  const int per = (m + 255) / 256, i0 = tid * per, i1 = min(i0 + per, m);
-  int own = 0;
-  for (int i = i0; i < i1; ++i) own += units_of(args, decode_visible(a, i));
-  const int sum = scan64(own);
-  if (lane == 63) part[256 + wave] = sum;
-  __syncthreads();
-  int base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) base += part[256 + w];
-    total += part[256 + w];
-  }
-  part[tid] = base + sum - own;
-  __syncthreads();
-  return Line{total, 0};
-}
-
-// the sequence that holds unit `want` (below the total), and the units before it
-__device__ __forceinline__ int line_find(const DecodeArgs& args, const Line& line,
-                                         const int* part, int want, int& before) {
-  const AttentionCall& a = args.a;
-  const int m = (int)a.m;
-  if (m == 1) {
-    before = 0;
-    return 0;
-  }
-  if (m <= 64) {
-    // the last one that starts at or before it: those of no units share their start
-    // with the next, and those past the end start at the total
-    const int lane = (int)__lane_id();
-    const int seq = 63 - __builtin_clzll(__ballot(lane < m && line.mine <= want));
-    before = __builtin_amdgcn_readlane(line.mine, seq);
-    return seq;
-  }
-  int t = 0;                           // the same among the blocks
-#pragma unroll
-  for (int w = 128; w > 0; w /= 2)
-    if (part[t + w] <= want) t += w;
-  int seq = t * ((m + 255) / 256);
-  before = part[t];
-  for (;;) {
-    const int n = units_of(args, decode_visible(a, seq));
-    if (before + n > want || seq + 1 >= m) return seq;
-    before += n;
-    ++seq;
-  }
-}
-
 // `units` of the line over `wgs` workgroups (at most as many): the first `more` take
 // one unit above `each`
 struct Share {
@@ -212,12 +137,14 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, kq = lane >> 4;
 
-  __shared__ int part[260];
+  __shared__ int part[kLineWords<256>];
   __shared__ __align__(16) float so[4 * kRows * OS];
   __shared__ float sm[4][kRows], sl[4][kRows];
 
   const int per_unit = cc.kv_heads * args.tiles, m_rows = (int)a.m;
-  const Line line = line_up(args, part);
+  auto count = [&](int i) { return units_of(args, decode_visible(a, i)); };
+  const Line line = m_rows == 1 ? Line{units_of(args, uniform_visible(a, 0)), 0}
+                                : line_up<256>(m_rows, part, count);
   const int all = line.total * per_unit;
 
   // rows that see nothing are in no unit
@@ -239,7 +166,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   int u = share.start(blockIdx.x);
   const int u_end = share.start(blockIdx.x + 1);
   int item0;                                             // the line's unit where seq starts
-  int seq = line_find(args, line, part, u / per_unit, item0);
+  int seq = line_find<256>(m_rows, line, part, u / per_unit, item0, count);
   seq = __builtin_amdgcn_readfirstlane(seq);
   item0 = __builtin_amdgcn_readfirstlane(item0) * per_unit;
 
@@ -395,7 +322,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
     for (int i = 1; i < 8; ++i) big = fmaxf(big, z[i]);
     big = max_quarters(big) * unit;
     if (__any(big > m + kLag)) {
-      const float mn = fmaxf(m, big), fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
+      // each row by itself, so that it does not depend on the others
+        const float mn = big > m + kLag ? big : m;
+        const float fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
       m = mn;
       l *= fade;
 #pragma unroll

@@ -1,135 +1,588 @@
-// Attention over a paged cache of keys and values (formulas in wq.h).
+// Causal attention of several tokens per sequence over a paged cache (formulas in wq.h).
 //
-// One wave per row and query head.  A head of D components is D / 8 lanes of 8;
-// the 512 / D groups of lanes take the visible tokens in turn, each with a running
-// maximum and sums of its own, and are joined at the end.
+// Bound by the matrix cores for long prompts.  A workgroup takes 32 NW rows of one
+// sequence and kv head, a row being a token and one of the query heads that share the
+// kv head, tokens outermost: all of them read the same keys and values, also where a
+// chunk has few tokens.  Tiles of 64 visible tokens go through LDS, the next one loaded
+// while one is computed; a wave has 32 rows.
+//
+// S^T = K Q^T and O^T = V^T P^T on 32x32x16 matrix instructions: the sums of S^T leave a
+// lane with one row and 16 tokens of each 32, so the softmax needs one exchange between
+// two lanes, and the weights are the operand of P^T as they are, with the tokens of its
+// k in the order in which the sums hold them.  V^T takes its tokens in the same order
+// through the transposing LDS reads.
+//
+// LDS rows are whole heads; their 16-byte pieces are swapped by row (the loads into LDS
+// fetch them in that order), so that no read meets more than its share of a bank.
+#include <algorithm>
+
 #include "attention.h"
 
 namespace wq {
 namespace {
 
-// 8 components from p: 16 bytes of a 16-bit type, or 8 of E4M3
-template <int CT>
-__device__ __forceinline__ void load8(const char* p, float (&v)[8]) {
-  if constexpr (CT == WQ_E4M3) {
-    const uint2_t r = *reinterpret_cast<const uint2_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2v_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)r[i], false);
-      const float2v_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)r[i], true);
-      v[4 * i] = lo[0];
-      v[4 * i + 1] = lo[1];
-      v[4 * i + 2] = hi[0];
-      v[4 * i + 3] = hi[1];
-    }
-  } else {
-    unpack8<CT>(*reinterpret_cast<const uint4_t*>(p), v);
-  }
+constexpr int kTile = 64;              // tokens of a tile
+
+struct PromptArgs {
+  AttentionCall a;
+  int group;                           // query heads per kv head
+  int splits;                          // parts of the visible tokens, each a workgroup's
+  uint32_t page16, token16;            // strides in 16 bytes; a cache spans less than 2^31
+};
+
+// rows of sequence i: where they start in q, and how many
+struct Rows {
+  int start, n;
+};
+__device__ __forceinline__ Rows rows_of(const AttentionCall& a, int i) {
+  const int m = (int)a.m;
+  const int s = min(max(a.starts[i], 0), m), e = min(max(a.starts[i + 1], 0), m);
+  return Rows{s, max(e - s, 0)};
 }
 
-template <int DT, int CT, int D>
-__global__ __launch_bounds__(64) void attention_rows_kernel(AttentionCall a) {
-  constexpr int L = D / 8, G = 64 / L;
+// the same for an `i` that is the same in every lane
+__device__ __forceinline__ Rows uniform_rows(const AttentionCall& a, int i) {
+  const int m = (int)a.m;
+  const int s = min(max(scalar_at(a.starts, i), 0), m);
+  const int e = min(max(scalar_at(a.starts, i + 1), 0), m);
+  return Rows{s, max(e - s, 0)};
+}
+
+template <int T>
+__device__ __forceinline__ float16v_t mfma32(uint4_t a, uint4_t b, float16v_t c) {
+  if constexpr (T == WQ_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+
+// 16-byte piece of a row of LDS that holds piece 0: keys are read a piece of 16 rows at a
+// time, values four pieces of 8 rows
+template <int D>
+__device__ __forceinline__ int key_swap(int row) {
+  return D == 128 ? row & 15 : (row >> 1) & 7;
+}
+template <int D>
+__device__ __forceinline__ int value_swap(int row) {
+  return D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+}
+
+// four tokens of 16 components, transposed: lane i of 16 gets component i of each
+__device__ __forceinline__ uint2_t read_transposed(const char* p) {
+  typedef short short4v_t __attribute__((ext_vector_type(4)));
+  using L = __attribute__((address_space(3))) short4v_t*;
+  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
+}
+
+// exponent bits of a 16-bit type: all set in infinities and NaN
+template <int T>
+constexpr uint32_t kExponent = T == WQ_BF16 ? 0x7F80u : 0x7C00u;
+
+__device__ __forceinline__ float max_halves(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+template <int DT, int CT, int D, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
+  constexpr bool F8 = CT == WQ_E4M3;
+  constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
+  constexpr bool TWO = F8 && DT == WQ_F16;               // weights in two parts of bf16
+  // exponents as in the decode kernel: from a reference that lags the maximum by up to
+  // 2^8; weights of f16 2^7 larger
+  constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
+  constexpr int NT = NW * 64, BM = NW * 32;
+  constexpr int RB = D * 2;                              // bytes of a row in LDS
+  constexpr int KB = kTile * RB;                         // and of a tile
+  constexpr int PC = D / 8;                              // 16-byte pieces of a row
+  constexpr int NL = KB / 1024 / NW;                     // loads of 1 KB per wave and tile
+  constexpr int NC = D / 16, NB = D / 32;                // k-steps of S^T, blocks of O^T
+  const AttentionCall& a = args.a;
   const KvCache& cc = a.cache;
-  const int64_t row = blockIdx.x;
-  const int head = blockIdx.y, lane = threadIdx.x;
-  const int c = lane % L, g = lane / L;
-  const int kh = head / (int)(a.heads / cc.kv_heads);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nl = lane & 31, hi = lane >> 5;
 
-  // the row's sequence, and its position in it
-  int64_t seq = row, after = 0;                        // rows of the sequence after this one
-  if (a.starts != nullptr) {
-    int64_t lo = 0, hi = a.batch;                      // the last start at or before row
-    if (row < a.starts[0] || row >= a.starts[a.batch]) return;
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.starts[mid] <= row) lo = mid; else hi = mid;
-    }
-    seq = lo;
-    after = (int64_t)a.starts[seq + 1] - 1 - row;
-  }
-  const int64_t room = a.max_pages << cc.lg_page;
-  const int64_t len = min((int64_t)max(a.lens[seq], 0), room);
-  const int64_t pos = len - 1 - after;
-  // visible: [0, first) and [from, pos]
-  int64_t from = a.window == INT32_MAX ? 0 : max((int64_t)0, pos + 1 - a.window);
-  const int64_t first = min((int64_t)a.sinks, from);
-  const int64_t seen = pos < 0 ? 0 : first + pos + 1 - from;
+  extern __shared__ __align__(1024) char lds[];          // keys 2 x KB, values 2 x KB
+  __shared__ int part[kLineWords<NT>];
+  __shared__ __align__(16) float scales[F8 ? 2 : 1][F8 ? 2 : 1][F8 ? kTile : 1];
 
-  float q[8];
-  unpack8<DT>(*reinterpret_cast<const uint4_t*>(a.q + row * a.ldq + (int64_t)head * D + c * 8), q);
-  float m = -INFINITY, l = 0.0f, o[8];
+  // this workgroup's kv head, and its tile of rows: later rows of a sequence, which see
+  // more, come first
+  const int batch = (int)a.batch, group = args.group;
+  int work = blockIdx.x;
+  const int kh = work % cc.kv_heads;
+  work /= cc.kv_heads;
+  const int split = work % args.splits;
+  work /= args.splits;
+  auto tiles = [&](int i) { return (rows_of(a, i).n * group + BM - 1) / BM; };
+  const Line line = batch == 1 ? Line{tiles(0), 0} : line_up<NT>(batch, part, tiles);
+  if (work >= __builtin_amdgcn_readfirstlane(line.total)) return;
+  int before;
+  const int seq = __builtin_amdgcn_readfirstlane(
+      line_find<NT>(batch, line, part, work, before, tiles));
+  const Rows rows = uniform_rows(a, seq);
+  const int count = rows.n * group;                      // of this sequence and kv head
+  const int row_tile = (count + BM - 1) / BM - 1 - (work - __builtin_amdgcn_readfirstlane(before));
+  const int len = tokens_of(a, scalar_at(a.lens, seq));
+  const int before_rows = len - rows.n;                  // position of row 0; may be negative
+
+  // this lane's row, and what the wave's and the workgroup's rows see
+  const int r0 = row_tile * BM, rw = r0 + wave * 32, r = rw + nl;
+  const bool live = r < count;
+  const int token = min(r, count - 1) / group, head = kh * group + min(r, count - 1) % group;
+  const int64_t out = (int64_t)(rows.start + token) * a.heads + head;
+  const int pos = before_rows + token;
+  const int wave_lo = before_rows + min(rw, count - 1) / group;
+  const int wave_hi = before_rows + min(rw + 31, count - 1) / group;
+  const int wg_lo = max(before_rows + r0 / group, 0);
+  const int wg_hi = before_rows + min(r0 + BM - 1, count - 1) / group;
+  // the tokens that some row sees: as one row's, from the first row's window on
+  Visible vis;
+  vis.from = wg_lo >= a.window ? wg_lo - a.window + 1 : 0;
+  vis.first = min(a.sinks, vis.from);
+  vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
+  auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
+  const int all_tiles = (vis.n + kTile - 1) / kTile;
+  // (tiles * splits is below 2^24 * 2^6)
+  const int t_begin = all_tiles * split / args.splits;
+  const int t_end = all_tiles * (split + 1) / args.splits;
+
+  float16v_t o[NB];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-  const int32_t* table = a.pages + seq * a.ldp;
-  const float scale = a.scale * kLog2e;
-  for (int64_t i0 = 0; i0 < seen; i0 += G) {
-    const int64_t i = i0 + g;
-    const bool live = i < seen;
-    const int64_t j = !live ? pos : i < first ? i : i - first + from;
-    const int64_t page = min(max(table[j >> cc.lg_page], 0), cc.pages - 1);
-    const int64_t at = j & ((1 << cc.lg_page) - 1);
-    const int64_t off = page * cc.page_stride + kh * cc.head_stride + at * cc.token_stride;
-    const int64_t sat = ((page * cc.kv_heads + kh) << cc.lg_page) + at;
-    constexpr int B = CT == WQ_E4M3 ? 8 : 16;
-    float k[8], v[8], z = 0.0f, vs = 1.0f;
-    load8<CT>(cc.k + off + c * B, k);
-    load8<CT>(cc.v + off + c * B, v);
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z = fmaf(q[e], k[e], z);
+    for (int e = 0; e < 16; ++e) o[b][e] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+
+  if (t_begin < t_end) {
+    // Q^T: lane (row nl, half hi) has 8 components of each k-step
+    uint4_t q[NC];
+    {
+      const uint16_t* qp = a.q + (int64_t)(rows.start + token) * a.ldq + (int64_t)head * D + hi * 8;
 #pragma unroll
-    for (int w = 1; w < L; w *= 2) z += __shfl_xor(z, w);
-    if constexpr (CT == WQ_E4M3) {
-      z *= cc.ks[sat];
-      vs = cc.vs[sat];
+      for (int c = 0; c < NC; ++c) q[c] = *reinterpret_cast<const uint4_t*>(qp + c * 16);
     }
-    z = live ? z * scale : -INFINITY;
-    if (z == -INFINITY) continue;
-    const float mn = fmaxf(m, z);
-    const float r = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(z - mn);
-    l = l * r + p;
+    const float zscale = a.scale * kLog2e;
+    const int32_t* table = a.pages + (int64_t)seq * a.ldp;
+    const char* kbase = cc.k + kh * cc.head_stride;
+    const char* vbase = cc.v + kh * cc.head_stride;
+    char* const kl = lds;
+    char* const vl = lds + 2 * KB;
+
+    // LDS addresses of this lane: keys by piece, values by block of 32 components
+    int ka[NC], va[NB];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * r + p * (v[e] * vs);
-    m = mn;
+    for (int c = 0; c < NC; ++c) ka[c] = nl * RB + (((2 * c + hi) ^ key_swap<D>(nl)) << 4);
+    {
+      const int vr = 4 * hi + ((lane & 15) >> 2);        // row within 8
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int piece = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        va[b] = vr * RB + ((piece ^ value_swap<D>(vr)) << 4) + 8 * (lane & 1);
+      }
+    }
+
+    // the rows of a tile that this lane loads
+    constexpr int LR = F8 ? 1 : NL;
+    auto tile_row = [&](int i) {
+      if constexpr (F8) return tid / (NT / kTile);       // NT / 64 threads per row
+      return (wave * NL + i) * (1024 / RB) + lane / PC;
+    };
+    int page[LR];
+    auto look_up = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < LR; ++i)
+        page[i] = page_of(a, table, token_at(min(t * kTile + tile_row(i), vis.n - 1)));
+    };
+    // E4M3: codes wait in registers until they are widened into LDS
+    constexpr int CB = F8 ? kTile * D / NT : 16;           // codes per thread, of keys and values
+    uint32_t kc[CB / 4], vc[CB / 4];
+    float sc = 0.0f;
+    auto load = [&](int t, int buf) {
+#pragma unroll
+      for (int i = 0; i < LR; ++i) {
+        const int row = tile_row(i);
+        const int tok = token_at(min(t * kTile + row, vis.n - 1));
+        const int place = tok & ((1 << cc.lg_page) - 1);
+        const uint64_t off =
+            (uint64_t)((uint32_t)page[i] * args.page16 + (uint32_t)place * args.token16) << 4;
+        if constexpr (F8) {
+          const int c0 = tid % (NT / kTile) * CB;
+#pragma unroll
+          for (int w = 0; w < CB / 4; w += (CB >= 16 ? 4 : 2)) {
+            if constexpr (CB >= 16) {
+              const uint4_t x = *reinterpret_cast<const uint4_t*>(kbase + off + c0 + 4 * w);
+              const uint4_t y = *reinterpret_cast<const uint4_t*>(vbase + off + c0 + 4 * w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) kc[w + e] = x[e], vc[w + e] = y[e];
+            } else {
+              const uint2_t x = *reinterpret_cast<const uint2_t*>(kbase + off + c0 + 4 * w);
+              const uint2_t y = *reinterpret_cast<const uint2_t*>(vbase + off + c0 + 4 * w);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) kc[w + e] = x[e], vc[w + e] = y[e];
+            }
+          }
+          // the row's first two threads take the scales of its key and value
+          const float* sp = tid % (NT / kTile) == 0 ? cc.ks : cc.vs;
+          sc = sp[(((int64_t)page[i] * cc.kv_heads + kh) << cc.lg_page) + place];
+        } else {
+          const int piece = lane % PC;
+          const char* kp = kbase + off + ((piece ^ key_swap<D>(row)) << 4);
+          const char* vp = vbase + off + ((piece ^ value_swap<D>(row)) << 4);
+          const int to = buf * KB + (wave * NL + i) * 1024;
+          lds_dma16(kp, (lds_void_t*)(kl + to));
+          lds_dma16(vp, (lds_void_t*)(vl + to));
+        }
+      }
+    };
+    auto store = [&](int buf) {                          // E4M3: into LDS
+      if constexpr (F8) {
+        const int row = tile_row(0), p0 = tid % (NT / kTile) * (CB / 8);
+#pragma unroll
+        for (int w = 0; w < CB / 4; w += 2) {
+          const uint2_t k0 = widen4<DT>(kc[w]), k1 = widen4<DT>(kc[w + 1]);
+          const uint2_t v0 = widen4<VT>(vc[w]), v1 = widen4<VT>(vc[w + 1]);
+          const int piece = p0 + w / 2;
+          *reinterpret_cast<uint4_t*>(kl + buf * KB + row * RB + ((piece ^ key_swap<D>(row)) << 4)) =
+              uint4_t{k0[0], k0[1], k1[0], k1[1]};
+          *reinterpret_cast<uint4_t*>(vl + buf * KB + row * RB +
+                                      ((piece ^ value_swap<D>(row)) << 4)) =
+              uint4_t{v0[0], v0[1], v1[0], v1[1]};
+        }
+        const int which = tid % (NT / kTile);
+        if (which < 2) scales[buf][which][row] = sc;
+      }
+    };
+
+    // O^T += V^T P^T of 32 tokens; `safe`: values that are not finite as zeros
+    auto add_values = [&](const char* v, int b, const uint4_t (&p)[2], bool safe) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {
+          const char* at = v + va[e] + (32 * b + 16 * s) * RB;
+          const uint2_t x0 = read_transposed(at), x1 = read_transposed(at + 8 * RB);
+          uint4_t x = {x0[0], x0[1], x1[0], x1[1]};
+          if (safe) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              constexpr uint32_t kE = kExponent<VT>;
+              if ((x[w] & kE) == kE) x[w] &= 0xFFFF0000u;
+              if ((x[w] >> 16 & kE) == kE) x[w] &= 0x0000FFFFu;
+            }
+          }
+          o[e] = mfma32<VT>(x, p[s], o[e]);
+        }
+    };
+
+    auto compute = [&](int t, int buf) {
+      const int i0 = t * kTile, tok0 = token_at(i0), tok1 = token_at(i0 + kTile - 1);
+      // whether the wave's rows see all of the tile, or nothing
+      const bool straight = i0 >= vis.first || i0 + kTile <= vis.first;
+      const bool outside = tok0 > wave_hi || rw >= count ||
+                           (straight && tok0 >= a.sinks && wave_lo - tok1 >= a.window);
+      if (outside) return;
+      const bool whole = straight && i0 + kTile <= vis.n && tok1 <= wave_lo &&
+                         (wave_hi - tok0 < a.window || tok1 < a.sinks);
+      const char* k = kl + buf * KB;
+      const char* v = vl + buf * KB;
+      float16v_t z[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[b][e] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          z[b] = mfma32<DT>(*reinterpret_cast<const uint4_t*>(k + ka[c] + b * 32 * RB), q[c], z[b]);
+      // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
+      const float unit = F8 ? 1.0f : zscale;
+      if constexpr (F8) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4_t ks =
+                *reinterpret_cast<const float4_t*>(&scales[buf][0][32 * b + 8 * j + 4 * hi]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[b][4 * j + e] *= ks[e] * zscale;
+          }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int i = i0 + 32 * b + 8 * (e / 4) + 4 * hi + e % 4, tok = token_at(i);
+            const bool ok = i < vis.n && tok <= pos && (pos - tok < a.window || tok < a.sinks);
+            z[b][e] = ok ? z[b][e] : -INFINITY;
+          }
+      }
+      float big = z[0][0];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) big = fmaxf(big, z[b][e]);
+      big = max_halves(big) * unit;
+      if (__any(big > m + kLag)) {
+        // each row by itself, so that it does not depend on the others
+        const float mn = big > m + kLag ? big : m;
+        const float fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
+        m = mn;
+        l *= fade;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[b][e] *= fade;
+      }
+      const float ref = exp_ref(m) - kShift;
+      float sum = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          z[b][e] = __builtin_amdgcn_exp2f(F8 ? z[b][e] - ref : fmaf(z[b][e], unit, -ref));
+          sum += z[b][e];
+        }
+      l += sum;
+      if constexpr (F8) {
+        // the scales of the values join the weights; a weight of 0 stays 0
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4_t vs =
+                *reinterpret_cast<const float4_t*>(&scales[buf][1][32 * b + 8 * j + 4 * hi]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float w = z[b][4 * j + e];
+              z[b][4 * j + e] = whole || w != 0.0f ? w * vs[e] : 0.0f;
+            }
+          }
+      }
+      // Values that are not finite meet weights of 0 in rows that do not see them: only
+      // where the wave's rows see different tokens, and then they are added by hand.
+      bool bad = false;
+      if (!whole) {
+        typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+        us2_t top = {0, 0};
+#pragma unroll 4
+        for (int i = 0; i < KB / 1024; ++i) {
+          const uint4_t x = *reinterpret_cast<const uint4_t*>(v + i * 1024 + lane * 16);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(us2_t, x[w] & 0x7FFF7FFFu));
+        }
+        bad = __any(top[0] >= kExponent<VT> || top[1] >= kExponent<VT>);
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint4_t p[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) p[s][w] = pack2<VT>(z[b][8 * s + 2 * w], z[b][8 * s + 2 * w + 1]);
+        add_values(v, b, p, bad);
+        if constexpr (TWO) {
+          uint4_t rest[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float h0, h1;
+              unpack2<VT>(p[s][w], h0, h1);
+              rest[s][w] = pack2<VT>(z[b][8 * s + 2 * w] - h0, z[b][8 * s + 2 * w + 1] - h1);
+            }
+          add_values(v, b, rest, bad);
+        }
+      }
+      if (bad) {
+        for (int i = 0; i < kTile; ++i) {
+          const int tok = token_at(i0 + i);
+          const bool ok =
+              i0 + i < vis.n && tok <= pos && (pos - tok < a.window || tok < a.sinks);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int d0 = 32 * b + 8 * j + 4 * hi;
+              const uint2_t x = *reinterpret_cast<const uint2_t*>(
+                  v + i * RB + (((d0 >> 3) ^ value_swap<D>(i)) << 4) + (d0 & 7) * 2);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t h = e % 2 == 0 ? x[e / 2] & 0xFFFFu : x[e / 2] >> 16;
+                float f;
+                if constexpr (VT == WQ_BF16) f = bf16_bits_to_f32((uint16_t)h);
+                else f = f16_bits_to_f32((uint16_t)h);
+                if (ok && (h & kExponent<VT>) == kExponent<VT>) o[b][4 * j + e] += f;
+              }
+            }
+        }
+      }
+    };
+
+    look_up(t_begin);
+    load(t_begin, 0);
+    look_up(t_begin + 1);
+    store(0);
+    for (int t = t_begin; t < t_end; ++t) {
+      const int buf = (t - t_begin) & 1;
+      vm_wait<0>();
+      lgkm_wait0();
+      wg_barrier();                                      // tile t is there, t - 1 done with
+      if (t + 1 < t_end) {
+        load(t + 1, buf ^ 1);
+        look_up(t + 2);
+      }
+      compute(t, buf);
+      if (t + 1 < t_end) store(buf ^ 1);
+    }
   }
+
+  l = sum_halves(l);
+  if (args.splits > 1) {
+    // m, l and the sums of this part
+    if (!live) return;
+    const int64_t total = a.m * a.heads;
+    float* ml = a.ws + (int64_t)args.splits * total * D + (split * total + out) * 2;
+    if (hi == 0) {
+      ml[0] = m;
+      ml[1] = l;
+    }
+    if (m == -INFINITY) return;
+    float* w = a.ws + (split * total + out) * D;
 #pragma unroll
-  for (int w = L; w < 64; w *= 2) {
-    const float mo = __shfl_xor(m, w), lo = __shfl_xor(l, w), mn = fmaxf(m, mo);
-    const float r = m == -INFINITY ? 0.0f : exp2f(m - mn);
-    const float ro = mo == -INFINITY ? 0.0f : exp2f(mo - mn);
-    l = l * r + lo * ro;
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * r + __shfl_xor(o[e], w) * ro;
-    m = mn;
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4_t*>(w + 32 * b + 8 * j + 4 * hi) =
+            float4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
+    return;
   }
-  if (g != 0) return;
-  const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] *= inv;
-  *reinterpret_cast<uint4_t*>(a.y + (row * a.heads + head) * D + c * 8) = pack8<DT>(o);
-  if (a.lse != nullptr && c == 0)
-    a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : m * kLn2 + __logf(l);
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      // this half's 4 components of two groups of 8; after the swap 8 of one group
+      uint32_t w[2][2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[g][e] = pack2<DT>(o[b][4 * (j + g) + 2 * e] * inv, o[b][4 * (j + g) + 2 * e + 1] * inv);
+      auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      if (live)
+        *reinterpret_cast<uint4_t*>(a.y + out * D + 32 * b + 8 * (j + hi)) =
+            uint4_t{s0[0], s1[0], s0[1], s1[1]};
+    }
+  if (a.lse != nullptr && live && hi == 0)
+    a.lse[out] = l == 0.0f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <int DT, int CT, int D>
-hipError_t rows_go(const AttentionCall& a, hipStream_t s) {
-  attention_rows_kernel<DT, CT, D>
-      <<<dim3((unsigned)a.m, (unsigned)a.heads), 64, 0, s>>>(a);
+// joins the parts of a row and head: D / 8 threads
+template <int DT, int D>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float shift) {
+  const AttentionCall& a = args.a;
+  const int64_t total = a.m * a.heads, per = 256 / (D / 8);
+  const int64_t out = (int64_t)blockIdx.x * per + threadIdx.x / (D / 8);
+  const int c = threadIdx.x % (D / 8);
+  if (out >= total) return;
+  const int64_t row = out / a.heads;
+  if (row < a.starts[0] || row >= a.starts[a.batch]) return;
+  const float* ml = a.ws + (int64_t)args.splits * total * D;
+  float m = -INFINITY, l = 0.0f, x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+  for (int s = 0; s < args.splits; ++s) {
+    const int64_t at = s * total + out;
+    const float pm = ml[2 * at], pl = ml[2 * at + 1];
+    if (pm == -INFINITY) continue;                       // no sums were written
+    const float mn = fmaxf(m, pm), fade = __builtin_amdgcn_exp2f(m - mn);
+    const float f = __builtin_amdgcn_exp2f(pm - mn);
+    l = l * fade + pl * f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * fade + a.ws[at * D + c * 8 + e] * f;
+    m = mn;
+  }
+  const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  *reinterpret_cast<uint4_t*>(a.y + out * D + c * 8) = pack8<DT>(x);
+  if (a.lse != nullptr && c == 0)
+    a.lse[out] = l == 0.0f ? -INFINITY : (m - shift + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+struct PromptPlan {
+  int waves, splits;
+  int64_t tiles;                       // of rows, at most
+};
+PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
+  const int64_t group = heads / c.kv_heads;
+  PromptPlan p{8, 1, 0};
+  auto tiles = [&](int waves) {
+    return m * group / (32 * waves) + std::min(batch, m);
+  };
+  p.tiles = tiles(p.waves);
+  return p;
+}
+
+template <int DT, int CT, int D, int NW>
+hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kLds = 4 * kTile * D * 2;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(prompt_kernel<DT, CT, D, NW>), kLds, done);
+  if (e != hipSuccess) return e;
+  const PromptArgs args{a, (int)(a.heads / a.cache.kv_heads), p.splits,
+                        (uint32_t)(a.cache.page_stride >> 4),
+                        (uint32_t)(a.cache.token_stride >> 4)};
+  const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
+  prompt_kernel<DT, CT, D, NW><<<dim3((unsigned)wgs), NW * 64, kLds, s>>>(args);
+  const hipError_t e2 = hipGetLastError();
+  if (e2 != hipSuccess || p.splits == 1) return e2;
+  constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
+  const int64_t per = 256 / (D / 8);
+  prompt_join_kernel<DT, D>
+      <<<dim3((unsigned)((a.m * a.heads + per - 1) / per)), 256, 0, s>>>(args, kShift);
   return hipGetLastError();
 }
+template <int DT, int CT, int D>
+hipError_t prompt_nw(const AttentionCall& a, hipStream_t s) {
+  const PromptPlan p = plan_prompt(a.m, a.heads, a.batch, a.cache);
+  return p.waves == 8 ? prompt_go<DT, CT, D, 8>(a, p, s) : prompt_go<DT, CT, D, 4>(a, p, s);
+}
 template <int DT, int D>
-hipError_t rows_ct(const AttentionCall& a, hipStream_t s) {
-  return a.cache.dt == WQ_E4M3 ? rows_go<DT, WQ_E4M3, D>(a, s) : rows_go<DT, DT, D>(a, s);
+hipError_t prompt_ct(const AttentionCall& a, hipStream_t s) {
+  return a.cache.dt == WQ_E4M3 ? prompt_nw<DT, WQ_E4M3, D>(a, s) : prompt_nw<DT, DT, D>(a, s);
 }
 template <int DT>
-hipError_t rows_d(const AttentionCall& a, hipStream_t s) {
-  return a.cache.d == 128 ? rows_ct<DT, 128>(a, s) : rows_ct<DT, 64>(a, s);
+hipError_t prompt_d(const AttentionCall& a, hipStream_t s) {
+  return a.cache.d == 128 ? prompt_ct<DT, 128>(a, s) : prompt_ct<DT, 64>(a, s);
 }
 
 }  // namespace
 
+size_t prompt_ws_bytes(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
+  const PromptPlan p = plan_prompt(m, heads, batch, c);
+  return p.splits == 1 ? 0 : (size_t)p.splits * m * heads * (c.d + 2) * sizeof(float);
+}
+
+int64_t prompt_wgs(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
+  const PromptPlan p = plan_prompt(m, heads, batch, c);
+  return p.tiles * p.splits * c.kv_heads;
+}
+
 hipError_t launch_attention_prompt(const AttentionCall& a, hipStream_t s) {
-  return a.dt == WQ_BF16 ? rows_d<WQ_BF16>(a, s) : rows_d<WQ_F16>(a, s);
+  return a.dt == WQ_BF16 ? prompt_d<WQ_BF16>(a, s) : prompt_d<WQ_F16>(a, s);
 }
 
 }  // namespace wq

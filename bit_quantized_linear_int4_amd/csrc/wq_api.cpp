@@ -652,7 +652,8 @@ size_t wq_attention_decode_workspace(int64_t m, int64_t heads, const wq_kv_cache
 size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,
                                      const wq_kv_cache* cache) {
   if (!attention_sizes_ok(m, heads, cache) || batch < 1 || batch >= kMaxDim) return 0;
-  return 0;
+  if (prompt_wgs(m, heads, batch, kernel_cache(cache)) > kPromptMaxWgs) return 0;
+  return prompt_ws_bytes(m, heads, batch, kernel_cache(cache));
 }
 
 wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,
@@ -680,6 +681,7 @@ wq_status wq_attention_prompt(const void* q, int32_t dt, int64_t m, int64_t head
   const wq_status st = check_attention(q, dt, m, heads, ldq, batch, cache, pages, max_pages, ldp,
                                        lens, scale, window, sinks, y, lse, &c);
   if (st != WQ_OK) return st;
+  if (prompt_wgs(m, heads, batch, c.cache) > kPromptMaxWgs) return WQ_ERR_SHAPE;
   if (!aligned(starts, 4)) return WQ_ERR_ALIGN;
   c.starts = starts;
   return run_attention(&c, workspace, ws_bytes,

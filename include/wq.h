@@ -555,7 +555,7 @@ wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t head
  * position sees nothing (y = 0, lse = -inf).  Rows of q before starts[0] or from
  * starts[batch] on are not read, and y and lse not written there.
  * starts int32 [batch + 1], ascending, within [0, m]; lens int32 [batch]; pages
- * int32 [batch] rows of max_pages.  The weights of v are rounded to dt (bf16 for
+ * int32 [batch] rows of max_pages; batch * kv_heads below 2^21.  The weights of v are rounded to dt (bf16 for
  * WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), the sum of weights is not.
  * workspace: at least wq_attention_prompt_workspace(m, heads, batch, cache) bytes,
  * 256-byte aligned (may be NULL when that is 0).

@@ -120,6 +120,9 @@ def test_prompt_errors():
     call = prompt()
     assert call(starts=None) == NULL and call(starts=P + 2) == ALIGN
     assert call(batch=0) == SHAPE and call(batch=1 << 23) == SHAPE
+    many = dict(m=1 << 22, batch=1 << 22)
+    assert call(**many) == SHAPE
+    assert wq._load().wq_attention_prompt_workspace(1 << 22, 4, 1 << 22, ctypes.byref(cache())) == 0
 
 
 @needs_lib
