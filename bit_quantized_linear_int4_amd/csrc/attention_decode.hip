@@ -323,8 +323,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
     big = max_quarters(big) * unit;
     if (__any(big > m + kLag)) {
       // each row by itself, so that it does not depend on the others
-        const float mn = big > m + kLag ? big : m;
-        const float fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
+      const float mn = big > m + kLag ? big : m;
+      const float fade = __builtin_amdgcn_exp2f(m - exp_ref(mn));
       m = mn;
       l *= fade;
 #pragma unroll

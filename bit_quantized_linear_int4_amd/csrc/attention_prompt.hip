@@ -1,10 +1,14 @@
 // Causal attention of several tokens per sequence over a paged cache (formulas in wq.h).
 //
-// Bound by the matrix cores for long prompts.  A workgroup takes 32 NW rows of one
-// sequence and kv head, a row being a token and one of the query heads that share the
-// kv head, tokens outermost: all of them read the same keys and values, also where a
-// chunk has few tokens.  Tiles of 64 visible tokens go through LDS, the next one loaded
-// while one is computed; a wave has 32 rows.
+// Bound by the matrix cores for long prompts, by HBM for a few rows behind a long
+// context.  A workgroup takes rows of one sequence and kv head, a row being a token and
+// one of the query heads that share the kv head, tokens outermost: all of them read the
+// same keys and values, also where a chunk has few tokens.  Tiles of 64 visible tokens go
+// through LDS, the next one loaded while one is computed; a wave has 32 rows.  Eight waves
+// are 256 rows (KS = 1), or 128 whose tiles two halves of the waves take in turn (KS = 2)
+// and whose sums they join at the end, without a way through HBM: so the longest row of a
+// shorter prompt takes half as long.  Where that leaves CUs idle, parts of the tokens go
+// to workgroups of their own (`splits`), and a second kernel joins them.
 //
 // S^T = K Q^T and O^T = V^T P^T on 32x32x16 matrix instructions: the sums of S^T leave a
 // lane with one row and 16 tokens of each 32, so the softmax needs one exchange between
@@ -89,15 +93,16 @@ __device__ __forceinline__ float sum_halves(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-template <int DT, int CT, int D, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
+template <int DT, int CT, int D, int KS>
+__global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   constexpr bool F8 = CT == WQ_E4M3;
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
   constexpr bool TWO = F8 && DT == WQ_F16;               // weights in two parts of bf16
   // exponents as in the decode kernel: from a reference that lags the maximum by up to
   // 2^8; weights of f16 2^7 larger
   constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
-  constexpr int NT = NW * 64, BM = NW * 32;
+  constexpr int NT = 512, NW = 8 / KS, BM = NW * 32;     // threads; row waves, rows
+  constexpr int HT = NT / KS;                            // threads that load a tile
   constexpr int RB = D * 2;                              // bytes of a row in LDS
   constexpr int KB = kTile * RB;                         // and of a tile
   constexpr int PC = D / 8;                              // 16-byte pieces of a row
@@ -106,12 +111,14 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
   const AttentionCall& a = args.a;
   const KvCache& cc = a.cache;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int all_wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = KS == 1 ? 0 : all_wave / NW, wave = all_wave - half * NW;
+  const int ht = tid - half * HT;
   const int nl = lane & 31, hi = lane >> 5;
 
-  extern __shared__ __align__(1024) char lds[];          // keys 2 x KB, values 2 x KB
+  extern __shared__ __align__(1024) char lds[];          // per half keys 2 x KB, values 2 x KB
   __shared__ int part[kLineWords<NT>];
-  __shared__ __align__(16) float scales[F8 ? 2 : 1][F8 ? 2 : 1][F8 ? kTile : 1];
+  __shared__ __align__(16) float scales[KS][F8 ? 2 : 1][F8 ? 2 : 1][F8 ? kTile : 1];
 
   // this workgroup's kv head, and its tile of rows: later rows of a sequence, which see
   // more, come first
@@ -149,10 +156,12 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
   vis.first = min(a.sinks, vis.from);
   vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
   auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
+  // parts of at least two steps; those past the last one are empty (tiles are below 2^24,
+  // splits at most 64)
   const int all_tiles = (vis.n + kTile - 1) / kTile;
-  // (tiles * splits is below 2^24 * 2^6)
-  const int t_begin = all_tiles * split / args.splits;
-  const int t_end = all_tiles * (split + 1) / args.splits;
+  const int parts = min(args.splits, max(all_tiles / (2 * KS), 1));
+  const int t_begin = split < parts ? all_tiles * split / parts : 0;
+  const int t_end = split < parts ? all_tiles * (split + 1) / parts : 0;
 
   float16v_t o[NB];
 #pragma unroll
@@ -173,8 +182,8 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
     const int32_t* table = a.pages + (int64_t)seq * a.ldp;
     const char* kbase = cc.k + kh * cc.head_stride;
     const char* vbase = cc.v + kh * cc.head_stride;
-    char* const kl = lds;
-    char* const vl = lds + 2 * KB;
+    char* const kl = lds + half * 4 * KB;
+    char* const vl = kl + 2 * KB;
 
     // LDS addresses of this lane: keys by piece, values by block of 32 components
     int ka[NC], va[NB];
@@ -192,7 +201,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
     // the rows of a tile that this lane loads
     constexpr int LR = F8 ? 1 : NL;
     auto tile_row = [&](int i) {
-      if constexpr (F8) return tid / (NT / kTile);       // NT / 64 threads per row
+      if constexpr (F8) return ht / (HT / kTile);        // HT / 64 threads per row
       return (wave * NL + i) * (1024 / RB) + lane / PC;
     };
     int page[LR];
@@ -202,7 +211,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
         page[i] = page_of(a, table, token_at(min(t * kTile + tile_row(i), vis.n - 1)));
     };
     // E4M3: codes wait in registers until they are widened into LDS
-    constexpr int CB = F8 ? kTile * D / NT : 16;           // codes per thread, of keys and values
+    constexpr int CB = F8 ? kTile * D / HT : 16;           // codes per thread, of keys and values
     uint32_t kc[CB / 4], vc[CB / 4];
     float sc = 0.0f;
     auto load = [&](int t, int buf) {
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
         const uint64_t off =
             (uint64_t)((uint32_t)page[i] * args.page16 + (uint32_t)place * args.token16) << 4;
         if constexpr (F8) {
-          const int c0 = tid % (NT / kTile) * CB;
+          const int c0 = ht % (HT / kTile) * CB;
 #pragma unroll
           for (int w = 0; w < CB / 4; w += (CB >= 16 ? 4 : 2)) {
             if constexpr (CB >= 16) {
@@ -230,7 +239,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
             }
           }
           // the row's first two threads take the scales of its key and value
-          const float* sp = tid % (NT / kTile) == 0 ? cc.ks : cc.vs;
+          const float* sp = ht % (HT / kTile) == 0 ? cc.ks : cc.vs;
           sc = sp[(((int64_t)page[i] * cc.kv_heads + kh) << cc.lg_page) + place];
         } else {
           const int piece = lane % PC;
@@ -244,7 +253,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
     };
     auto store = [&](int buf) {                          // E4M3: into LDS
       if constexpr (F8) {
-        const int row = tile_row(0), p0 = tid % (NT / kTile) * (CB / 8);
+        const int row = tile_row(0), p0 = ht % (HT / kTile) * (CB / 8);
 #pragma unroll
         for (int w = 0; w < CB / 4; w += 2) {
           const uint2_t k0 = widen4<DT>(kc[w]), k1 = widen4<DT>(kc[w + 1]);
@@ -256,8 +265,8 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
                                       ((piece ^ value_swap<D>(row)) << 4)) =
               uint4_t{v0[0], v0[1], v1[0], v1[1]};
         }
-        const int which = tid % (NT / kTile);
-        if (which < 2) scales[buf][which][row] = sc;
+        const int which = ht % (HT / kTile);
+        if (which < 2) scales[half][buf][which][row] = sc;
       }
     };
 
@@ -311,7 +320,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4_t ks =
-                *reinterpret_cast<const float4_t*>(&scales[buf][0][32 * b + 8 * j + 4 * hi]);
+                *reinterpret_cast<const float4_t*>(&scales[half][buf][0][32 * b + 8 * j + 4 * hi]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[b][4 * j + e] *= ks[e] * zscale;
           }
@@ -360,7 +369,7 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4_t vs =
-                *reinterpret_cast<const float4_t*>(&scales[buf][1][32 * b + 8 * j + 4 * hi]);
+                *reinterpret_cast<const float4_t*>(&scales[half][buf][1][32 * b + 8 * j + 4 * hi]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float w = z[b][4 * j + e];
@@ -429,25 +438,50 @@ __global__ __launch_bounds__(NW * 64, 2) void prompt_kernel(PromptArgs args) {
       }
     };
 
-    look_up(t_begin);
-    load(t_begin, 0);
-    look_up(t_begin + 1);
+    // a step is KS tiles, one for each half; past the last one the half has none
+    look_up(t_begin + half);
+    load(t_begin + half, 0);
+    look_up(t_begin + half + KS);
     store(0);
-    for (int t = t_begin; t < t_end; ++t) {
-      const int buf = (t - t_begin) & 1;
+    for (int t0 = t_begin, buf = 0; t0 < t_end; t0 += KS, buf ^= 1) {
+      const int t = t0 + half;
       vm_wait<0>();
       lgkm_wait0();
-      wg_barrier();                                      // tile t is there, t - 1 done with
-      if (t + 1 < t_end) {
-        load(t + 1, buf ^ 1);
-        look_up(t + 2);
+      wg_barrier();                                      // tile t is there, t - KS done with
+      if (t0 + KS < t_end) {
+        load(t + KS, buf ^ 1);
+        look_up(t + 2 * KS);
       }
-      compute(t, buf);
-      if (t + 1 < t_end) store(buf ^ 1);
+      if (t < t_end) compute(t, buf);
+      if (t0 + KS < t_end) store(buf ^ 1);
     }
   }
 
   l = sum_halves(l);
+  if constexpr (KS == 2) {
+    // the second half's sums join the first's, through the tiles' place in LDS: lane's
+    // values next to each other over the lanes
+    __syncthreads();
+    float* x = reinterpret_cast<float*>(lds) + wave * (16 * NB + 2) * 64 + lane;
+    if (half == 1) {
+      x[0] = m;
+      x[64] = l;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[(2 + 16 * b + e) * 64] = o[b][e];
+    }
+    __syncthreads();
+    if (half == 1) return;
+    const float om = x[0], mn = fmaxf(m, om), ref = exp_ref(mn);
+    const float f = __builtin_amdgcn_exp2f(m - ref), g = __builtin_amdgcn_exp2f(om - ref);
+    m = mn;
+    l = l * f + x[64] * g;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[b][e] = o[b][e] * f + x[(2 + 16 * b + e) * 64] * g;
+  }
   if (args.splits > 1) {
     // m, l and the sums of this part
     if (!live) return;
@@ -503,16 +537,33 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
   float m = -INFINITY, l = 0.0f, x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-  for (int s = 0; s < args.splits; ++s) {
-    const int64_t at = s * total + out;
-    const float pm = ml[2 * at], pl = ml[2 * at + 1];
-    if (pm == -INFINITY) continue;                       // no sums were written
-    const float mn = fmaxf(m, pm), fade = __builtin_amdgcn_exp2f(m - mn);
-    const float f = __builtin_amdgcn_exp2f(pm - mn);
-    l = l * fade + pl * f;
+  constexpr int U = 8;                                   // parts whose loads are in flight
+  for (int s0 = 0; s0 < args.splits; s0 += U) {
+    float pm[U], pl[U], px[U][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * fade + a.ws[at * D + c * 8 + e] * f;
-    m = mn;
+    for (int i = 0; i < U; ++i) {
+      const int64_t at = min(s0 + i, args.splits - 1) * total + out;
+      pm[i] = ml[2 * at];
+      pl[i] = ml[2 * at + 1];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4_t v = *reinterpret_cast<const float4_t*>(a.ws + at * D + c * 8 + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) px[i][e + j] = v[j];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      // a part without sums has written none
+      const bool some = s0 + i < args.splits && pm[i] != -INFINITY;
+      const float mn = some ? fmaxf(m, pm[i]) : m;
+      const float fade = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      const float f = some ? __builtin_amdgcn_exp2f(pm[i] - mn) : 0.0f;
+      l = l * fade + (some ? pl[i] * f : 0.0f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * fade + (some ? px[i][e] * f : 0.0f);
+      m = mn;
+    }
   }
   const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll
@@ -523,32 +574,36 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
 }
 
 struct PromptPlan {
-  int waves, splits;
+  int halves, splits;                  // KS, and parts of the tokens
   int64_t tiles;                       // of rows, at most
 };
 PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
-  const int64_t group = heads / c.kv_heads;
-  PromptPlan p{8, 1, 0};
-  auto tiles = [&](int waves) {
-    return m * group / (32 * waves) + std::min(batch, m);
+  const int64_t rows = m * (heads / c.kv_heads);
+  auto tiles = [&](int64_t bm) {
+    return batch == 1 ? (rows + bm - 1) / bm : rows / bm + std::min(batch, m);
   };
-  p.tiles = tiles(p.waves);
+  PromptPlan p{1, 1, tiles(256)};
+  if (p.tiles * c.kv_heads >= 512) return p;
+  p = PromptPlan{2, 1, tiles(128)};
+  const int64_t wgs = p.tiles * c.kv_heads;
+  p.splits = (int)std::min<int64_t>(64, std::max<int64_t>(1, 256 / wgs));
   return p;
 }
 
-template <int DT, int CT, int D, int NW>
+template <int DT, int CT, int D, int KS>
 hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kLds = 4 * kTile * D * 2;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(prompt_kernel<DT, CT, D, NW>), kLds, done);
+  constexpr int kLds = std::max(KS * 4 * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
+  const auto kern = prompt_kernel<DT, CT, D, KS>;
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), kLds, done);
   if (e != hipSuccess) return e;
   const PromptArgs args{a, (int)(a.heads / a.cache.kv_heads), p.splits,
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
   const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
-  prompt_kernel<DT, CT, D, NW><<<dim3((unsigned)wgs), NW * 64, kLds, s>>>(args);
-  const hipError_t e2 = hipGetLastError();
-  if (e2 != hipSuccess || p.splits == 1) return e2;
+  kern<<<dim3((unsigned)wgs), 512, kLds, s>>>(args);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
   const int64_t per = 256 / (D / 8);
   prompt_join_kernel<DT, D>
@@ -556,13 +611,13 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   return hipGetLastError();
 }
 template <int DT, int CT, int D>
-hipError_t prompt_nw(const AttentionCall& a, hipStream_t s) {
+hipError_t prompt_ks(const AttentionCall& a, hipStream_t s) {
   const PromptPlan p = plan_prompt(a.m, a.heads, a.batch, a.cache);
-  return p.waves == 8 ? prompt_go<DT, CT, D, 8>(a, p, s) : prompt_go<DT, CT, D, 4>(a, p, s);
+  return p.halves == 1 ? prompt_go<DT, CT, D, 1>(a, p, s) : prompt_go<DT, CT, D, 2>(a, p, s);
 }
 template <int DT, int D>
 hipError_t prompt_ct(const AttentionCall& a, hipStream_t s) {
-  return a.cache.dt == WQ_E4M3 ? prompt_nw<DT, WQ_E4M3, D>(a, s) : prompt_nw<DT, DT, D>(a, s);
+  return a.cache.dt == WQ_E4M3 ? prompt_ks<DT, WQ_E4M3, D>(a, s) : prompt_ks<DT, DT, D>(a, s);
 }
 template <int DT>
 hipError_t prompt_d(const AttentionCall& a, hipStream_t s) {
