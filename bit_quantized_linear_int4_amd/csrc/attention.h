@@ -39,6 +39,27 @@ __device__ __forceinline__ int page_of(const AttentionCall& a, const int32_t* ta
   return min(max(table[token >> a.cache.lg_page], 0), a.cache.pages - 1);
 }
 
+// The kernel's arguments of type A, read where they are used: those that only a piece's
+// start or end needs would otherwise take scalar registers all along, more than there are.
+template <typename A>
+using ArgsAt = const __attribute__((address_space(4))) A*;
+template <typename A>
+__device__ __forceinline__ ArgsAt<A> args_here() {
+  auto p = (ArgsAt<A>)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// two weights rounded to nearest even into one word (low half first)
+template <int T>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  const float2v_t v = {lo, hi};
+  if constexpr (T == WQ_BF16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2v_t));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
+}
+
 template <int T>
 __device__ __forceinline__ float4_t mfma16(uint4_t a, uint4_t b, float4_t c) {
   if constexpr (T == WQ_BF16)

@@ -54,14 +54,6 @@ __device__ __forceinline__ Visible uniform_visible(const A& a, int seq) {
   const int len = (int)min((int64_t)max(scalar_at(a.lens, seq), 0), room);
   return visible_of(len - 1, a.window, a.sinks);
 }
-// The kernel's arguments, read where they are used: those of a piece's start and end would
-// otherwise take scalar registers all along, more than there are.
-using DecodeArgsAt = const __attribute__((address_space(4))) DecodeArgs*;
-__device__ __forceinline__ DecodeArgsAt args_here() {
-  auto p = (DecodeArgsAt)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return p;
-}
 __device__ __forceinline__ int units_of(const DecodeArgs& args, const Visible& v) {
   return (v.n + (1 << args.lg_unit) - 1) >> args.lg_unit;
 }
@@ -176,7 +168,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   Visible vis;
   int at, end;                                           // visible tokens, from the wave's on
   auto take = [&]() {                                    // the piece that starts at u < u_end
-    const DecodeArgsAt k = args_here();
+    const auto k = args_here<DecodeArgs>();
     const int lg_unit = k->lg_unit, tiles = k->tiles, per_unit = k->a.cache.kv_heads * tiles;
     const Share share(all, wgs);
     const int u_end = share.start(blockIdx.x + 1);
@@ -258,7 +250,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   // Q^T: lane (row nl, piece kq); rows past the group are zeros
   uint4_t q[D / 32];
   auto load_q = [&](const Owner& p) {
-    const DecodeArgsAt k = args_here();
+    const auto k = args_here<DecodeArgs>();
     const int rows = min(kRows, k->group - p.ht() * kRows);
     const int64_t head = (int64_t)p.kh() * k->group + p.ht() * kRows + min(nl, rows - 1);
     const uint16_t* qp = k->a.q + (int64_t)p.seq * k->a.ldq + head * D;
@@ -347,10 +339,10 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
     uint4_t hi, lo;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      hi[w] = pack2<VT>(p[2 * w], p[2 * w + 1]);
+      hi[w] = pack_weights<VT>(p[2 * w], p[2 * w + 1]);
       float h0, h1;
       unpack2<VT>(hi[w], h0, h1);
-      lo[w] = pack2<VT>(p[2 * w] - h0, p[2 * w + 1] - h1);
+      lo[w] = pack_weights<VT>(p[2 * w] - h0, p[2 * w + 1] - h1);
     }
     // 16-bit values of the 8 tokens, D / 16 components each
     uint32_t vv[8][NI / 2];
@@ -382,7 +374,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
 
   // joins the four waves' sums of a piece and starts new ones
   auto finish = [&](const Owner& p) {
-    const DecodeArgsAt k = args_here();
+    const auto k = args_here<DecodeArgs>();
     const bool starts = p.rest & Owner::kStarts, ends = p.rest & Owner::kEnds;
     l = sum_quarters(l);
     if (kq == 0) {

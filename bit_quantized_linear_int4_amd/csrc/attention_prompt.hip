@@ -26,6 +26,7 @@ namespace wq {
 namespace {
 
 constexpr int kTile = 64;              // tokens of a tile
+constexpr int kPartSteps = 4;          // steps of a part at least
 
 struct PromptArgs {
   AttentionCall a;
@@ -73,11 +74,14 @@ __device__ __forceinline__ int value_swap(int row) {
   return D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
 }
 
-// four tokens of 16 components, transposed: lane i of 16 gets component i of each
-__device__ __forceinline__ uint2_t read_transposed(const char* p) {
+// four tokens of 16 components, transposed: lane i of 16 gets component i of each; and the
+// four that are `more` bytes behind them
+__device__ __forceinline__ uint4_t read_transposed(const char* p, int more) {
   typedef short short4v_t __attribute__((ext_vector_type(4)));
   using L = __attribute__((address_space(3))) short4v_t*;
-  return __builtin_bit_cast(uint2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p));
+  const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p);
+  const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(p + more));
+  return __builtin_bit_cast(uint4_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 // exponent bits of a 16-bit type: all set in infinities and NaN
@@ -119,6 +123,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   extern __shared__ __align__(1024) char lds[];          // per half keys 2 x KB, values 2 x KB
   __shared__ int part[kLineWords<NT>];
   __shared__ __align__(16) float scales[KS][F8 ? 2 : 1][F8 ? 2 : 1][F8 ? kTile : 1];
+  __shared__ uint32_t odd[KS][2][2];
 
   // this workgroup's kv head, and its tile of rows: later rows of a sequence, which see
   // more, come first
@@ -144,8 +149,10 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   const int r0 = row_tile * BM, rw = r0 + wave * 32, r = rw + nl;
   const bool live = r < count;
   const int token = min(r, count - 1) / group, head = kh * group + min(r, count - 1) % group;
-  const int64_t out = (int64_t)(rows.start + token) * a.heads + head;
   const int pos = before_rows + token;
+  // it sees the tokens [see, see + width) and those below `sunk`
+  const int see = pos >= a.window ? pos - a.window + 1 : 0;
+  const int width = max(pos + 1 - see, 0), sunk = min(a.sinks, max(pos + 1, 0));
   const int wave_lo = before_rows + min(rw, count - 1) / group;
   const int wave_hi = before_rows + min(rw + 31, count - 1) / group;
   const int wg_lo = max(before_rows + r0 / group, 0);
@@ -156,10 +163,10 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   vis.first = min(a.sinks, vis.from);
   vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
   auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
-  // parts of at least two steps; those past the last one are empty (tiles are below 2^24,
+  // parts of at least kPartSteps steps; those past the last one are empty (tiles are below 2^24,
   // splits at most 64)
   const int all_tiles = (vis.n + kTile - 1) / kTile;
-  const int parts = min(args.splits, max(all_tiles / (2 * KS), 1));
+  const int parts = min(args.splits, max(all_tiles / (kPartSteps * KS), 1));
   const int t_begin = split < parts ? all_tiles * split / parts : 0;
   const int t_end = split < parts ? all_tiles * (split + 1) / parts : 0;
 
@@ -179,9 +186,6 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int c = 0; c < NC; ++c) q[c] = *reinterpret_cast<const uint4_t*>(qp + c * 16);
     }
     const float zscale = a.scale * kLog2e;
-    const int32_t* table = a.pages + (int64_t)seq * a.ldp;
-    const char* kbase = cc.k + kh * cc.head_stride;
-    const char* vbase = cc.v + kh * cc.head_stride;
     char* const kl = lds + half * 4 * KB;
     char* const vl = kl + 2 * KB;
 
@@ -206,22 +210,31 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     };
     int page[LR];
     auto look_up = [&](int t) {
+      const auto k = args_here<PromptArgs>();
+      const int32_t* table = k->a.pages + (int64_t)seq * k->a.ldp;
+      const int lg_page = k->a.cache.lg_page, last = k->a.cache.pages - 1;
 #pragma unroll
-      for (int i = 0; i < LR; ++i)
-        page[i] = page_of(a, table, token_at(min(t * kTile + tile_row(i), vis.n - 1)));
+      for (int i = 0; i < LR; ++i) {
+        const int tok = token_at(min(t * kTile + tile_row(i), vis.n - 1));
+        page[i] = min(max(table[tok >> lg_page], 0), last);
+      }
     };
     // E4M3: codes wait in registers until they are widened into LDS
     constexpr int CB = F8 ? kTile * D / HT : 16;           // codes per thread, of keys and values
     uint32_t kc[CB / 4], vc[CB / 4];
     float sc = 0.0f;
     auto load = [&](int t, int buf) {
+      const auto k = args_here<PromptArgs>();
+      const int lg_page = k->a.cache.lg_page;
+      const char* kbase = k->a.cache.k + kh * k->a.cache.head_stride;
+      const char* vbase = k->a.cache.v + kh * k->a.cache.head_stride;
 #pragma unroll
       for (int i = 0; i < LR; ++i) {
         const int row = tile_row(i);
         const int tok = token_at(min(t * kTile + row, vis.n - 1));
-        const int place = tok & ((1 << cc.lg_page) - 1);
+        const int place = tok & ((1 << lg_page) - 1);
         const uint64_t off =
-            (uint64_t)((uint32_t)page[i] * args.page16 + (uint32_t)place * args.token16) << 4;
+            (uint64_t)((uint32_t)page[i] * k->page16 + (uint32_t)place * k->token16) << 4;
         if constexpr (F8) {
           const int c0 = ht % (HT / kTile) * CB;
 #pragma unroll
@@ -239,8 +252,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             }
           }
           // the row's first two threads take the scales of its key and value
-          const float* sp = ht % (HT / kTile) == 0 ? cc.ks : cc.vs;
-          sc = sp[(((int64_t)page[i] * cc.kv_heads + kh) << cc.lg_page) + place];
+          const float* sp = ht % (HT / kTile) == 0 ? k->a.cache.ks : k->a.cache.vs;
+          sc = sp[(((int64_t)page[i] * k->a.cache.kv_heads + kh) << lg_page) + place];
         } else {
           const int piece = lane % PC;
           const char* kp = kbase + off + ((piece ^ key_swap<D>(row)) << 4);
@@ -270,36 +283,80 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       }
     };
 
-    // O^T += V^T P^T of 32 tokens; `safe`: values that are not finite as zeros
-    auto add_values = [&](const char* v, int b, const uint4_t (&p)[2], bool safe) {
+    // Values that are not finite would make NaN of the weights 0 of rows that do not see
+    // them.  In steps where rows of the workgroup see different tokens, such values
+    // become 0 in LDS and their tokens' bits are set in `odd`; the sums of the rows that do
+    // see them get them by hand.
+    auto differ = [&](int t0) {                            // the same for the workgroup
+      const auto k = args_here<PromptArgs>();
+      const int i0 = t0 * kTile, i1 = i0 + KS * kTile;
+      const bool one = i0 >= vis.first || i1 <= vis.first;
+      return !(one && i1 <= vis.n && token_at(i1 - 1) <= wg_lo &&
+               (wg_hi - token_at(i0) < k->a.window || token_at(i1 - 1) < k->a.sinks));
+    };
+    auto clear_odd = [&](int buf) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < KB / 16 / HT; ++i) {
+        const int at = (i * HT + ht) * 16;
+        uint4_t* p = reinterpret_cast<uint4_t*>(vl + buf * KB + at);
+        uint4_t x = *p;
+        typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+        us2_t top = {0, 0};
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-          const char* at = v + va[e] + (32 * b + 16 * s) * RB;
-          const uint2_t x0 = read_transposed(at), x1 = read_transposed(at + 8 * RB);
-          uint4_t x = {x0[0], x0[1], x1[0], x1[1]};
-          if (safe) {
+        for (int w = 0; w < 4; ++w)
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(us2_t, x[w] & 0x7FFF7FFFu));
+        constexpr uint32_t kE = kExponent<VT>;
+        if (top[0] >= kE || top[1] >= kE) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              constexpr uint32_t kE = kExponent<VT>;
-              if ((x[w] & kE) == kE) x[w] &= 0xFFFF0000u;
-              if ((x[w] >> 16 & kE) == kE) x[w] &= 0x0000FFFFu;
-            }
+          for (int w = 0; w < 4; ++w) {
+            if ((x[w] & kE) == kE) x[w] &= 0xFFFF0000u;
+            if ((x[w] >> 16 & kE) == kE) x[w] &= 0x0000FFFFu;
           }
-          o[e] = mfma32<VT>(x, p[s], o[e]);
+          *p = x;
+          atomicOr(&odd[half][buf][at / RB / 32], 1u << (at / RB % 32));
+        }
+      }
+    };
+    auto add_odd = [&](int t, int i) {                     // token i of the tile
+      const auto k = args_here<PromptArgs>();
+      const int tok = token_at(min(t * kTile + i, vis.n - 1));
+      const bool ok = ((uint32_t)(tok - see) < (uint32_t)width) | (tok < sunk);
+      const int place = tok & ((1 << k->a.cache.lg_page) - 1);
+      const int32_t* row = k->a.pages + (int64_t)seq * k->a.ldp;
+      const int at = min(max(scalar_at(row, tok >> k->a.cache.lg_page), 0), k->a.cache.pages - 1);
+      const char* p = k->a.cache.v + kh * k->a.cache.head_stride + at * k->a.cache.page_stride +
+                      place * k->a.cache.token_stride;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int d0 = 32 * b + 8 * j + 4 * hi;
+          uint2_t x;
+          if constexpr (F8) x = widen4<VT>(*reinterpret_cast<const uint32_t*>(p + d0));
+          else x = *reinterpret_cast<const uint2_t*>(p + 2 * d0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float lo, up;
+            unpack2<VT>(x[e / 2], lo, up);
+            const float f = e % 2 == 0 ? lo : up;
+            if (ok && !(fabsf(f) < INFINITY)) o[b][4 * j + e] += f;
+          }
+          // the compiler would keep the results of all comparisons in scalar registers
+          __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    auto compute = [&](int t, int buf) {
+    auto compute = [&](int t, int buf, bool mixed) {
+      const auto args_at = args_here<PromptArgs>();
+      const int window = args_at->a.window, sinks = args_at->a.sinks;
       const int i0 = t * kTile, tok0 = token_at(i0), tok1 = token_at(i0 + kTile - 1);
       // whether the wave's rows see all of the tile, or nothing
       const bool straight = i0 >= vis.first || i0 + kTile <= vis.first;
       const bool outside = tok0 > wave_hi || rw >= count ||
-                           (straight && tok0 >= a.sinks && wave_lo - tok1 >= a.window);
+                           (straight && tok0 >= sinks && wave_lo - tok1 >= window);
       if (outside) return;
       const bool whole = straight && i0 + kTile <= vis.n && tok1 <= wave_lo &&
-                         (wave_hi - tok0 < a.window || tok1 < a.sinks);
+                         (wave_hi - tok0 < window || tok1 < sinks);
       const char* k = kl + buf * KB;
       const char* v = vl + buf * KB;
       float16v_t z[2];
@@ -326,14 +383,25 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           }
       }
       if (!whole) {
+        if (straight && tok0 >= sinks) {
+          const int x = tok0 + 4 * hi - see;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int i = i0 + 32 * b + 8 * (e / 4) + 4 * hi + e % 4, tok = token_at(i);
-            const bool ok = i < vis.n && tok <= pos && (pos - tok < a.window || tok < a.sinks);
-            z[b][e] = ok ? z[b][e] : -INFINITY;
-          }
+            for (int e = 0; e < 16; ++e) {
+              const bool ok = (uint32_t)(x + 32 * b + 8 * (e / 4) + e % 4) < (uint32_t)width;
+              z[b][e] = ok ? z[b][e] : -INFINITY;
+            }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int tok = token_at(i0 + 32 * b + 8 * (e / 4) + 4 * hi + e % 4);
+              const bool ok = ((uint32_t)(tok - see) < (uint32_t)width) | (tok < sunk);
+              z[b][e] = ok ? z[b][e] : -INFINITY;
+            }
+        }
       }
       float big = z[0][0];
 #pragma unroll
@@ -377,63 +445,35 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             }
           }
       }
-      // Values that are not finite meet weights of 0 in rows that do not see them: only
-      // where the wave's rows see different tokens, and then they are added by hand.
-      bool bad = false;
-      if (!whole) {
-        typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
-        us2_t top = {0, 0};
-#pragma unroll 4
-        for (int i = 0; i < KB / 1024; ++i) {
-          const uint4_t x = *reinterpret_cast<const uint4_t*>(v + i * 1024 + lane * 16);
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(us2_t, x[w] & 0x7FFF7FFFu));
-        }
-        bad = __any(top[0] >= kExponent<VT> || top[1] >= kExponent<VT>);
-      }
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint4_t p[2];
+        for (int s = 0; s < 2; ++s) {
+          // 16 tokens: weights of this lane's 8, in two parts where one would be less
+          // exact than y (the values are codes, but y is f16)
+          uint4_t p, rest;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) p[s][w] = pack2<VT>(z[b][8 * s + 2 * w], z[b][8 * s + 2 * w + 1]);
-        add_values(v, b, p, bad);
-        if constexpr (TWO) {
-          uint4_t rest[2];
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < 4; ++w) {
+            const float w0 = z[b][8 * s + 2 * w], w1 = z[b][8 * s + 2 * w + 1];
+            p[w] = pack_weights<VT>(w0, w1);
+            if constexpr (TWO) {
               float h0, h1;
-              unpack2<VT>(p[s][w], h0, h1);
-              rest[s][w] = pack2<VT>(z[b][8 * s + 2 * w] - h0, z[b][8 * s + 2 * w + 1] - h1);
+              unpack2<VT>(p[w], h0, h1);
+              rest[w] = pack_weights<VT>(w0 - h0, w1 - h1);
             }
-          add_values(v, b, rest, bad);
+          }
+#pragma unroll
+          for (int e = 0; e < NB; ++e) {
+            const uint4_t x = read_transposed(v + va[e] + (32 * b + 16 * s) * RB, 8 * RB);
+            o[e] = mfma32<VT>(x, p, o[e]);
+            if constexpr (TWO) o[e] = mfma32<VT>(x, rest, o[e]);
+          }
         }
-      }
-      if (bad) {
-        for (int i = 0; i < kTile; ++i) {
-          const int tok = token_at(i0 + i);
-          const bool ok =
-              i0 + i < vis.n && tok <= pos && (pos - tok < a.window || tok < a.sinks);
+      if (mixed) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d0 = 32 * b + 8 * j + 4 * hi;
-              const uint2_t x = *reinterpret_cast<const uint2_t*>(
-                  v + i * RB + (((d0 >> 3) ^ value_swap<D>(i)) << 4) + (d0 & 7) * 2);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t h = e % 2 == 0 ? x[e / 2] & 0xFFFFu : x[e / 2] >> 16;
-                float f;
-                if constexpr (VT == WQ_BF16) f = bf16_bits_to_f32((uint16_t)h);
-                else f = f16_bits_to_f32((uint16_t)h);
-                if (ok && (h & kExponent<VT>) == kExponent<VT>) o[b][4 * j + e] += f;
-              }
-            }
+        for (int w = 0; w < 2; ++w) {
+          uint32_t bits = __builtin_amdgcn_readfirstlane(odd[half][buf][w]);
+          for (; bits != 0; bits &= bits - 1) add_odd(t, 32 * w + __builtin_ctz(bits));
         }
       }
     };
@@ -443,6 +483,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     load(t_begin + half, 0);
     look_up(t_begin + half + KS);
     store(0);
+    if (ht < 2) odd[half][0][ht] = 0;
     for (int t0 = t_begin, buf = 0; t0 < t_end; t0 += KS, buf ^= 1) {
       const int t = t0 + half;
       vm_wait<0>();
@@ -452,12 +493,20 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         load(t + KS, buf ^ 1);
         look_up(t + 2 * KS);
       }
-      if (t < t_end) compute(t, buf);
+      const bool mixed = differ(t0);
+      if (ht < 2) odd[half][buf ^ 1][ht] = 0;
+      if (mixed) {
+        clear_odd(buf);
+        lgkm_wait0();
+        wg_barrier();
+      }
+      if (t < t_end) compute(t, buf, mixed);
       if (t0 + KS < t_end) store(buf ^ 1);
     }
   }
 
   l = sum_halves(l);
+  const int64_t out = (int64_t)(rows.start + token) * args_here<PromptArgs>()->a.heads + head;
   if constexpr (KS == 2) {
     // the second half's sums join the first's, through the tiles' place in LDS: lane's
     // values next to each other over the lanes
@@ -482,17 +531,18 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[b][e] = o[b][e] * f + x[(2 + 16 * b + e) * 64] * g;
   }
-  if (args.splits > 1) {
+  const auto k = args_here<PromptArgs>();
+  if (k->splits > 1) {
     // m, l and the sums of this part
     if (!live) return;
-    const int64_t total = a.m * a.heads;
-    float* ml = a.ws + (int64_t)args.splits * total * D + (split * total + out) * 2;
+    const int64_t total = k->a.m * k->a.heads;
+    float* ml = k->a.ws + (int64_t)k->splits * total * D + (split * total + out) * 2;
     if (hi == 0) {
       ml[0] = m;
       ml[1] = l;
     }
     if (m == -INFINITY) return;
-    float* w = a.ws + (split * total + out) * D;
+    float* w = k->a.ws + (split * total + out) * D;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -516,11 +566,11 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
       auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
       if (live)
-        *reinterpret_cast<uint4_t*>(a.y + out * D + 32 * b + 8 * (j + hi)) =
+        *reinterpret_cast<uint4_t*>(k->a.y + out * D + 32 * b + 8 * (j + hi)) =
             uint4_t{s0[0], s1[0], s0[1], s1[1]};
     }
-  if (a.lse != nullptr && live && hi == 0)
-    a.lse[out] = l == 0.0f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
+  if (k->a.lse != nullptr && live && hi == 0)
+    k->a.lse[out] = l == 0.0f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // joins the parts of a row and head: D / 8 threads
@@ -577,7 +627,8 @@ struct PromptPlan {
   int halves, splits;                  // KS, and parts of the tokens
   int64_t tiles;                       // of rows, at most
 };
-PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
+// `most`: tokens that a row can see
+PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c, int64_t most) {
   const int64_t rows = m * (heads / c.kv_heads);
   auto tiles = [&](int64_t bm) {
     return batch == 1 ? (rows + bm - 1) / bm : rows / bm + std::min(batch, m);
@@ -586,7 +637,8 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
   if (p.tiles * c.kv_heads >= 512) return p;
   p = PromptPlan{2, 1, tiles(128)};
   const int64_t wgs = p.tiles * c.kv_heads;
-  p.splits = (int)std::min<int64_t>(64, std::max<int64_t>(1, 256 / wgs));
+  const int64_t steps = (most + 2 * kTile - 1) / (2 * kTile);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, 256 / wgs, steps / kPartSteps}));
   return p;
 }
 
@@ -612,7 +664,8 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
 }
 template <int DT, int CT, int D>
 hipError_t prompt_ks(const AttentionCall& a, hipStream_t s) {
-  const PromptPlan p = plan_prompt(a.m, a.heads, a.batch, a.cache);
+  const PromptPlan p = plan_prompt(
+      a.m, a.heads, a.batch, a.cache, a.max_pages << a.cache.lg_page);
   return p.halves == 1 ? prompt_go<DT, CT, D, 1>(a, p, s) : prompt_go<DT, CT, D, 2>(a, p, s);
 }
 template <int DT, int D>
@@ -627,12 +680,12 @@ hipError_t prompt_d(const AttentionCall& a, hipStream_t s) {
 }  // namespace
 
 size_t prompt_ws_bytes(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
-  const PromptPlan p = plan_prompt(m, heads, batch, c);
+  const PromptPlan p = plan_prompt(m, heads, batch, c, int64_t(1) << 30);
   return p.splits == 1 ? 0 : (size_t)p.splits * m * heads * (c.d + 2) * sizeof(float);
 }
 
 int64_t prompt_wgs(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
-  const PromptPlan p = plan_prompt(m, heads, batch, c);
+  const PromptPlan p = plan_prompt(m, heads, batch, c, int64_t(1) << 30);
   return p.tiles * p.splits * c.kv_heads;
 }
 

@@ -397,6 +397,11 @@ PROMPT = [
     (32, 2, 64, 64, "head", [17], [2000], 0, 0), (64, 8, 128, 16, "head", [3] * 9, [50] * 9, 0, 0),
     (12, 4, 128, 16, "head", [4, 9], [1500, 700], 300, 4),
     (3, 3, 64, 16, "head", [0, 0, 5], [3, 0, 0], 0, 0),
+    # enough sequences and kv heads for workgroups of 256 rows
+    (8, 4, 128, 16, "head", [200, 1, 140] + [2, 1, 3] * 43, [0, 300, 77] + [1, 40, 0] * 43, 0, 0),
+    (12, 4, 64, 32, "token", [190] + [1, 0, 4] * 50, [100] + [30, 5, 0] * 50, 61, 5),
+    (4, 4, 128, 64, "head", [520, 257] + [1] * 130, [0, 64] + [3] * 130, 0, 0),
+    (4, 4, 64, 16, "token", [600] + [2] * 129, [30] + [9] * 129, 200, 70),
 ]
 
 
@@ -486,17 +491,20 @@ def test_places_that_no_row_sees_may_hold_anything(dtype, cdtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[0]).all()
 
 
+@pytest.mark.parametrize("many", [0, 260])
 @pytest.mark.parametrize("what", ["k", "v", "vs"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_not_finite_tokens_reach_the_rows_that_see_them(bad, what):
-    """A token that is not finite among many rows of a prompt, and in a decoded batch."""
+def test_not_finite_tokens_reach_the_rows_that_see_them(bad, what, many):
+    """A token that is not finite among many rows of a prompt, and in a decoded batch;
+    with `many` sequences of one token behind, the workgroups have 256 rows."""
     cdtype = "e4m3" if what == "vs" else "bf16"
     n, at, kv, heads, d = 150, 90, 2, 4, 128
-    table, pages = table_of([n, 20], 16, 10)
+    table, pages = table_of([n, 20] + [1] * many, 16, 10)
     tn = table.cpu().numpy()
     c = Cache(pages, kv, 16, d, cdtype, seed=120)
-    q = rand((n + 20, heads, d), 121, "bf16", 2.0).cuda()
-    starts, lens = i32([0, n, n + 20]), i32([n, 20])
+    q = rand((n + 20 + many, heads, d), 121, "bf16", 2.0).cuda()
+    starts = i32([0, n] + list(range(n + 20, n + 21 + many)))
+    lens = i32([n, 20] + [1] * many)
     for window, sinks in ((0, 0), (25, 2)):
         before, lb = run_prompt(q, starts, c, table, lens, window, sinks)
         t = getattr(c, what)
@@ -504,7 +512,7 @@ def test_not_finite_tokens_reach_the_rows_that_see_them(bad, what):
         keep = t[place].clone()
         t[place] = bad
         y, lse = run_prompt(q, starts, c, table, lens, window, sinks)
-        sees = torch.zeros(n + 20, dtype=torch.bool, device="cuda")
+        sees = torch.zeros(n + 20 + many, dtype=torch.bool, device="cuda")
         sees[at:(at + window if window else n)] = True
         other = ~sees[:, None].expand(-1, heads).clone()
         other[:, :2] = True                                          # the other kv head's
@@ -518,7 +526,7 @@ def test_not_finite_tokens_reach_the_rows_that_see_them(bad, what):
         if what == "v":
             mine = [i for i in range(d) if i != 7]
             assert torch.equal(y[sees][:, 2:, mine], before[sees][:, 2:, mine])
-        yd, _ = run_decode(q[n - 1:n + 1], c, table, lens, window, sinks)
+        yd, _ = run_decode(q[n - 1:n + 1], c, table[:2], lens[:2], window, sinks)
         assert torch.isfinite(yd[1]).all() and torch.isfinite(yd[0, :2]).all()
         assert torch.isfinite(yd[0, 2:]).all().item() == (window > 0) or what == "k"
         t[place] = keep
