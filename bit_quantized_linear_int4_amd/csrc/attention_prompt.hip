@@ -4,7 +4,7 @@
 // context.  A workgroup takes rows of one sequence and kv head, a row being a token and
 // one of the query heads that share the kv head, tokens outermost: all of them read the
 // same keys and values, also where a chunk has few tokens.  Tiles of 64 visible tokens go
-// through LDS, the next one loaded while one is computed; a wave has 32 rows.  Eight waves
+// through LDS, the next two on their way while one is computed; a wave has 32 rows.  Eight waves
 // are 256 rows (KS = 1), or 128 whose tiles two halves of the waves take in turn (KS = 2)
 // and whose sums they join at the end, without a way through HBM: so the longest row of a
 // shorter prompt takes half as long.  Where that leaves CUs idle, parts of the tokens go
@@ -111,6 +111,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   constexpr int KB = kTile * RB;                         // and of a tile
   constexpr int PC = D / 8;                              // 16-byte pieces of a row
   constexpr int NL = KB / 1024 / NW;                     // loads of 1 KB per wave and tile
+  // tiles on their way while one is computed (two halves of D = 128 fill LDS with one)
+  constexpr int AHEAD = KS == 2 && D == 128 ? 1 : 2, BUFS = AHEAD + 1;
   constexpr int NC = D / 16, NB = D / 32;                // k-steps of S^T, blocks of O^T
   const AttentionCall& a = args.a;
   const KvCache& cc = a.cache;
@@ -120,9 +122,9 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   const int ht = tid - half * HT;
   const int nl = lane & 31, hi = lane >> 5;
 
-  extern __shared__ __align__(1024) char lds[];          // per half keys 2 x KB, values 2 x KB
+  extern __shared__ __align__(1024) char lds[];          // per half keys, values BUFS x KB each
   __shared__ int part[kLineWords<NT>];
-  __shared__ __align__(16) float scales[KS][F8 ? 2 : 1][F8 ? 2 : 1][F8 ? kTile : 1];
+  __shared__ __align__(16) float scales[KS][F8 ? BUFS : 1][F8 ? 2 : 1][F8 ? kTile : 1];
   __shared__ uint32_t odd[KS][2][2];
 
   // this workgroup's kv head, and its tile of rows: later rows of a sequence, which see
@@ -186,100 +188,97 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int c = 0; c < NC; ++c) q[c] = *reinterpret_cast<const uint4_t*>(qp + c * 16);
     }
     const float zscale = a.scale * kLog2e;
-    char* const kl = lds + half * 4 * KB;
-    char* const vl = kl + 2 * KB;
+    char* const kl = lds + half * 2 * BUFS * KB;
+    char* const vl = kl + BUFS * KB;
 
-    // LDS addresses of this lane: keys by piece, values by block of 32 components
-    int ka[NC], va[NB];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) ka[c] = nl * RB + (((2 * c + hi) ^ key_swap<D>(nl)) << 4);
-    {
-      const int vr = 4 * hi + ((lane & 15) >> 2);        // row within 8
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int piece = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        va[b] = vr * RB + ((piece ^ value_swap<D>(vr)) << 4) + 8 * (lane & 1);
-      }
-    }
+    // LDS addresses of this lane in a tile: of keys for the first k-step (that of step c is
+    // this one xor 32 c), of values for the first 32 components (block b's: xor 64 b)
+    const int ka = nl * RB + ((hi ^ key_swap<D>(nl)) << 4);
+    const int vr = 4 * hi + ((lane & 15) >> 2);            // row within 8
+    const int va = vr * RB + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swap<D>(vr)) << 4) +
+                   8 * (lane & 1);
 
-    // the rows of a tile that this lane loads
-    constexpr int LR = F8 ? 1 : NL;
-    auto tile_row = [&](int i) {
-      if constexpr (F8) return ht / (HT / kTile);        // HT / 64 threads per row
-      return (wave * NL + i) * (1024 / RB) + lane / PC;
+    // A wave loads RW rows of each of its half's tiles.  Where they are in the cache is
+    // found for GROUP tiles at once, a row in a lane, a group ahead of its use.
+    constexpr int RW = 8 * KS, GROUP = 64 / RW;
+    auto tile_of = [&](int i) { return t_begin + i * KS + half; };
+    auto group_token = [&](int i) {                        // tiles i .. i + GROUP - 1
+      return token_at(min(tile_of(i + lane / RW) * kTile + wave * RW + lane % RW, vis.n - 1));
     };
-    int page[LR];
-    auto look_up = [&](int t) {
+    int page = 0;
+    uint32_t off = 0, off_scale = 0;                       // in 16 bytes; in scales
+    auto look_up = [&](int i) {
       const auto k = args_here<PromptArgs>();
       const int32_t* table = k->a.pages + (int64_t)seq * k->a.ldp;
-      const int lg_page = k->a.cache.lg_page, last = k->a.cache.pages - 1;
-#pragma unroll
-      for (int i = 0; i < LR; ++i) {
-        const int tok = token_at(min(t * kTile + tile_row(i), vis.n - 1));
-        page[i] = min(max(table[tok >> lg_page], 0), last);
-      }
+      page = min(max(table[group_token(i) >> k->a.cache.lg_page], 0), k->a.cache.pages - 1);
     };
-    // E4M3: codes wait in registers until they are widened into LDS
-    constexpr int CB = F8 ? kTile * D / HT : 16;           // codes per thread, of keys and values
+    auto take_group = [&](int i) {                         // its pages are there
+      const auto k = args_here<PromptArgs>();
+      const int lg_page = k->a.cache.lg_page, place = group_token(i) & ((1 << lg_page) - 1);
+      off = (uint32_t)page * k->page16 + (uint32_t)place * k->token16;
+      if constexpr (F8) off_scale = (((uint32_t)page * k->a.cache.kv_heads + kh) << lg_page) + place;
+      look_up(i + GROUP);
+    };
+    // what a lane loads of its rows, 16 bits: one of PC pieces of NL rows, into LDS at once;
+    // E4M3: CB codes of one row, which wait in registers until they are widened into LDS
+    constexpr int CB = F8 ? D * RW / 64 : 16;
     uint32_t kc[CB / 4], vc[CB / 4];
     float sc = 0.0f;
-    auto load = [&](int t, int buf) {
+    auto fetch = [&](const char* p, uint32_t (&c)[CB / 4]) {
+      if constexpr (CB >= 16) {
+#pragma unroll
+        for (int w = 0; w < CB / 4; w += 4) {
+          const uint4_t x = *reinterpret_cast<const uint4_t*>(p + 4 * w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[w + e] = x[e];
+        }
+      } else {
+        const uint2_t x = *reinterpret_cast<const uint2_t*>(p);
+        c[0] = x[0];
+        c[1] = x[1];
+      }
+    };
+    auto load = [&](int i, int buf) {
+      if (i % GROUP == 0) take_group(i);
       const auto k = args_here<PromptArgs>();
-      const int lg_page = k->a.cache.lg_page;
-      const char* kbase = k->a.cache.k + kh * k->a.cache.head_stride;
-      const char* vbase = k->a.cache.v + kh * k->a.cache.head_stride;
+      const int64_t head_at = kh * k->a.cache.head_stride;
+      const char* kbase = k->a.cache.k + head_at;
+      const char* vbase = k->a.cache.v + head_at;
+      const int first = i % GROUP * RW;
+      if constexpr (F8) {
+        const int from = (first + lane / GROUP) * 4;       // GROUP threads per row
+        const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)off) << 4;
+        fetch(kbase + at + lane % GROUP * CB, kc);
+        fetch(vbase + at + lane % GROUP * CB, vc);
+        // the row's first two threads take the scales of its key and value
+        const float* sp = lane % GROUP == 0 ? k->a.cache.ks : k->a.cache.vs;
+        sc = sp[(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)off_scale)];
+      } else {
 #pragma unroll
-      for (int i = 0; i < LR; ++i) {
-        const int row = tile_row(i);
-        const int tok = token_at(min(t * kTile + row, vis.n - 1));
-        const int place = tok & ((1 << lg_page) - 1);
-        const uint64_t off =
-            (uint64_t)((uint32_t)page[i] * k->page16 + (uint32_t)place * k->token16) << 4;
-        if constexpr (F8) {
-          const int c0 = ht % (HT / kTile) * CB;
-#pragma unroll
-          for (int w = 0; w < CB / 4; w += (CB >= 16 ? 4 : 2)) {
-            if constexpr (CB >= 16) {
-              const uint4_t x = *reinterpret_cast<const uint4_t*>(kbase + off + c0 + 4 * w);
-              const uint4_t y = *reinterpret_cast<const uint4_t*>(vbase + off + c0 + 4 * w);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) kc[w + e] = x[e], vc[w + e] = y[e];
-            } else {
-              const uint2_t x = *reinterpret_cast<const uint2_t*>(kbase + off + c0 + 4 * w);
-              const uint2_t y = *reinterpret_cast<const uint2_t*>(vbase + off + c0 + 4 * w);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) kc[w + e] = x[e], vc[w + e] = y[e];
-            }
-          }
-          // the row's first two threads take the scales of its key and value
-          const float* sp = ht % (HT / kTile) == 0 ? k->a.cache.ks : k->a.cache.vs;
-          sc = sp[(((int64_t)page[i] * k->a.cache.kv_heads + kh) << lg_page) + place];
-        } else {
-          const int piece = lane % PC;
-          const char* kp = kbase + off + ((piece ^ key_swap<D>(row)) << 4);
-          const char* vp = vbase + off + ((piece ^ value_swap<D>(row)) << 4);
-          const int to = buf * KB + (wave * NL + i) * 1024;
-          lds_dma16(kp, (lds_void_t*)(kl + to));
-          lds_dma16(vp, (lds_void_t*)(vl + to));
+        for (int j = 0; j < NL; ++j) {
+          const int r = j * (1024 / RB) + lane / PC, row = wave * RW + r;
+          const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(
+                                  (first + r) * 4, (int)off) << 4;
+          const int to = buf * KB + wave * RW * RB + j * 1024;
+          lds_dma16(kbase + at + ((lane % PC ^ key_swap<D>(row)) << 4), (lds_void_t*)(kl + to));
+          lds_dma16(vbase + at + ((lane % PC ^ value_swap<D>(row)) << 4), (lds_void_t*)(vl + to));
         }
       }
     };
-    auto store = [&](int buf) {                          // E4M3: into LDS
+    auto store = [&](int buf) {                            // E4M3: into LDS
       if constexpr (F8) {
-        const int row = tile_row(0), p0 = ht % (HT / kTile) * (CB / 8);
+        const int row = wave * RW + lane / GROUP;
 #pragma unroll
         for (int w = 0; w < CB / 4; w += 2) {
           const uint2_t k0 = widen4<DT>(kc[w]), k1 = widen4<DT>(kc[w + 1]);
           const uint2_t v0 = widen4<VT>(vc[w]), v1 = widen4<VT>(vc[w + 1]);
-          const int piece = p0 + w / 2;
-          *reinterpret_cast<uint4_t*>(kl + buf * KB + row * RB + ((piece ^ key_swap<D>(row)) << 4)) =
+          const int piece = lane % GROUP * (CB / 8) + w / 2, at = buf * KB + row * RB;
+          *reinterpret_cast<uint4_t*>(kl + at + ((piece ^ key_swap<D>(row)) << 4)) =
               uint4_t{k0[0], k0[1], k1[0], k1[1]};
-          *reinterpret_cast<uint4_t*>(vl + buf * KB + row * RB +
-                                      ((piece ^ value_swap<D>(row)) << 4)) =
+          *reinterpret_cast<uint4_t*>(vl + at + ((piece ^ value_swap<D>(row)) << 4)) =
               uint4_t{v0[0], v0[1], v1[0], v1[1]};
         }
-        const int which = ht % (HT / kTile);
-        if (which < 2) scales[half][buf][which][row] = sc;
+        if (lane % GROUP < 2) scales[half][buf][lane % GROUP][row] = sc;
       }
     };
 
@@ -294,7 +293,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       return !(one && i1 <= vis.n && token_at(i1 - 1) <= wg_lo &&
                (wg_hi - token_at(i0) < k->a.window || token_at(i1 - 1) < k->a.sinks));
     };
-    auto clear_odd = [&](int buf) {
+    auto clear_odd = [&](int buf, int step) {
 #pragma unroll
       for (int i = 0; i < KB / 16 / HT; ++i) {
         const int at = (i * HT + ht) * 16;
@@ -313,7 +312,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             if ((x[w] >> 16 & kE) == kE) x[w] &= 0x0000FFFFu;
           }
           *p = x;
-          atomicOr(&odd[half][buf][at / RB / 32], 1u << (at / RB % 32));
+          atomicOr(&odd[half][step & 1][at / RB / 32], 1u << (at / RB % 32));
         }
       }
     };
@@ -346,7 +345,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         }
     };
 
-    auto compute = [&](int t, int buf, bool mixed) {
+    auto compute = [&](int t, int buf, int step, bool mixed) {
       const auto args_at = args_here<PromptArgs>();
       const int window = args_at->a.window, sinks = args_at->a.sinks;
       const int i0 = t * kTile, tok0 = token_at(i0), tok1 = token_at(i0 + kTile - 1);
@@ -357,8 +356,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       if (outside) return;
       const bool whole = straight && i0 + kTile <= vis.n && tok1 <= wave_lo &&
                          (wave_hi - tok0 < window || tok1 < sinks);
-      const char* k = kl + buf * KB;
-      const char* v = vl + buf * KB;
+      const int k = (int)(kl - lds) + buf * KB, v = (int)(vl - lds) + buf * KB;
       float16v_t z[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -368,7 +366,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          z[b] = mfma32<DT>(*reinterpret_cast<const uint4_t*>(k + ka[c] + b * 32 * RB), q[c], z[b]);
+          z[b] = mfma32<DT>(*reinterpret_cast<const uint4_t*>(lds + ((k + ka) ^ (c << 5)) + b * 32 * RB),
+                            q[c], z[b]);
       // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
       const float unit = F8 ? 1.0f : zscale;
       if constexpr (F8) {
@@ -464,7 +463,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           }
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
-            const uint4_t x = read_transposed(v + va[e] + (32 * b + 16 * s) * RB, 8 * RB);
+            const uint4_t x = read_transposed(lds + ((v + va) ^ (e << 6)) + (32 * b + 16 * s) * RB, 8 * RB);
             o[e] = mfma32<VT>(x, p, o[e]);
             if constexpr (TWO) o[e] = mfma32<VT>(x, rest, o[e]);
           }
@@ -472,37 +471,49 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       if (mixed) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          uint32_t bits = __builtin_amdgcn_readfirstlane(odd[half][buf][w]);
+          uint32_t bits = __builtin_amdgcn_readfirstlane(odd[half][step & 1][w]);
           for (; bits != 0; bits &= bits - 1) add_odd(t, 32 * w + __builtin_ctz(bits));
         }
       }
     };
 
-    // a step is KS tiles, one for each half; past the last one the half has none
-    look_up(t_begin + half);
-    load(t_begin + half, 0);
-    look_up(t_begin + half + KS);
-    store(0);
+    // A step is KS tiles, one for each half; past the last one the half has none, and what
+    // is loaded is not used.  16 bits: tile i + AHEAD is loaded in step i, once all waves are
+    // done with tile i - 1, whose place it takes.  E4M3: tile i + 2 is fetched into registers
+    // and tile i + 1 stored.
+    const int steps = (t_end - t_begin + KS - 1) / KS;
+    look_up(0);
+    load(0, 0);
+    if constexpr (F8) {
+      store(0);
+      load(1, 1);
+    } else if constexpr (AHEAD == 2) {
+      load(1, 1);
+    }
     if (ht < 2) odd[half][0][ht] = 0;
-    for (int t0 = t_begin, buf = 0; t0 < t_end; t0 += KS, buf ^= 1) {
-      const int t = t0 + half;
-      vm_wait<0>();
+    for (int step = 0, buf = 0; step < steps; ++step) {
+      const int t = tile_of(step), next = buf + 1 == BUFS ? 0 : buf + 1;
+      // this wave's loads of tile t are done (those of the next may go on); after the
+      // barrier all waves'
+      vm_wait<F8 ? 63 : (AHEAD - 1) * 2 * NL>();
       lgkm_wait0();
-      wg_barrier();                                      // tile t is there, t - KS done with
-      if (t0 + KS < t_end) {
-        load(t + KS, buf ^ 1);
-        look_up(t + 2 * KS);
-      }
-      const bool mixed = differ(t0);
-      if (ht < 2) odd[half][buf ^ 1][ht] = 0;
+      wg_barrier();
+      if constexpr (!F8) load(step + AHEAD, buf == 0 ? BUFS - 1 : buf - 1);
+      const bool mixed = differ(t - half);
+      if (ht < 2) odd[half][(step + 1) & 1][ht] = 0;
       if (mixed) {
-        clear_odd(buf);
+        clear_odd(buf, step);
         lgkm_wait0();
         wg_barrier();
       }
-      if (t < t_end) compute(t, buf, mixed);
-      if (t0 + KS < t_end) store(buf ^ 1);
+      if (t < t_end) compute(t, buf, step, mixed);
+      if constexpr (F8) {
+        store(next);
+        load(step + 2, 0);
+      }
+      buf = next;
     }
+    vm_wait<0>();                                          // nothing is on its way into LDS
   }
 
   l = sum_halves(l);
@@ -645,7 +656,9 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
 template <int DT, int CT, int D, int KS>
 hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kLds = std::max(KS * 4 * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
+  // tiles as in the kernel, and the place where two halves join
+  constexpr int kBufs = KS == 2 && D == 128 ? 2 : 3;
+  constexpr int kLds = std::max(KS * 2 * kBufs * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
   const auto kern = prompt_kernel<DT, CT, D, KS>;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), kLds, done);
   if (e != hipSuccess) return e;
