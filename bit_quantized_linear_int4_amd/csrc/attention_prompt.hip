@@ -188,6 +188,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int c = 0; c < NC; ++c) q[c] = *reinterpret_cast<const uint4_t*>(qp + c * 16);
     }
     const float zscale = a.scale * kLog2e;
+    const int window = a.window, sinks = a.sinks;
     char* const kl = lds + half * 2 * BUFS * KB;
     char* const vl = kl + BUFS * KB;
 
@@ -238,12 +239,11 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         c[1] = x[1];
       }
     };
+    const char* const kbase = cc.k + kh * cc.head_stride;
+    const char* const vbase = cc.v + kh * cc.head_stride;
+    const float* const sbase = lane % GROUP == 0 ? cc.ks : cc.vs;
     auto load = [&](int i, int buf) {
       if (i % GROUP == 0) take_group(i);
-      const auto k = args_here<PromptArgs>();
-      const int64_t head_at = kh * k->a.cache.head_stride;
-      const char* kbase = k->a.cache.k + head_at;
-      const char* vbase = k->a.cache.v + head_at;
       const int first = i % GROUP * RW;
       if constexpr (F8) {
         const int from = (first + lane / GROUP) * 4;       // GROUP threads per row
@@ -251,8 +251,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         fetch(kbase + at + lane % GROUP * CB, kc);
         fetch(vbase + at + lane % GROUP * CB, vc);
         // the row's first two threads take the scales of its key and value
-        const float* sp = lane % GROUP == 0 ? k->a.cache.ks : k->a.cache.vs;
-        sc = sp[(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)off_scale)];
+        sc = sbase[(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)off_scale)];
       } else {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -287,11 +286,10 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     // become 0 in LDS and their tokens' bits are set in `odd`; the sums of the rows that do
     // see them get them by hand.
     auto differ = [&](int t0) {                            // the same for the workgroup
-      const auto k = args_here<PromptArgs>();
       const int i0 = t0 * kTile, i1 = i0 + KS * kTile;
       const bool one = i0 >= vis.first || i1 <= vis.first;
       return !(one && i1 <= vis.n && token_at(i1 - 1) <= wg_lo &&
-               (wg_hi - token_at(i0) < k->a.window || token_at(i1 - 1) < k->a.sinks));
+               (wg_hi - token_at(i0) < window || token_at(i1 - 1) < sinks));
     };
     auto clear_odd = [&](int buf, int step) {
 #pragma unroll
@@ -346,8 +344,6 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     };
 
     auto compute = [&](int t, int buf, int step, bool mixed) {
-      const auto args_at = args_here<PromptArgs>();
-      const int window = args_at->a.window, sinks = args_at->a.sinks;
       const int i0 = t * kTile, tok0 = token_at(i0), tok1 = token_at(i0 + kTile - 1);
       // whether the wave's rows see all of the tile, or nothing
       const bool straight = i0 >= vis.first || i0 + kTile <= vis.first;
@@ -368,6 +364,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         for (int b = 0; b < 2; ++b)
           z[b] = mfma32<DT>(*reinterpret_cast<const uint4_t*>(lds + ((k + ka) ^ (c << 5)) + b * 32 * RB),
                             q[c], z[b]);
+      // a wave of this SIMD that is past its scores goes before one that multiplies
+      __builtin_amdgcn_s_setprio(1);
       // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
       const float unit = F8 ? 1.0f : zscale;
       if constexpr (F8) {
@@ -468,6 +466,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             if constexpr (TWO) o[e] = mfma32<VT>(x, rest, o[e]);
           }
         }
+      __builtin_amdgcn_s_setprio(0);
       if (mixed) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
