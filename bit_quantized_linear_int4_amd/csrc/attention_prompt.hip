@@ -76,12 +76,22 @@ __device__ __forceinline__ int value_swap(int row) {
 
 // four tokens of 16 components, transposed: lane i of 16 gets component i of each; and the
 // four that are `more` bytes behind them
-__device__ __forceinline__ uint4_t read_transposed(const char* p, int more) {
+__device__ __forceinline__ uint4_t read_transposed(uint32_t at, uint32_t more) {
   typedef short short4v_t __attribute__((ext_vector_type(4)));
   using L = __attribute__((address_space(3))) short4v_t*;
-  const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)p);
-  const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(p + more));
+  const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
+  const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + more));
   return __builtin_bit_cast(uint4_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// LDS by address: plain pointers into it take a check and an addition at each use
+template <typename T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+  return *(const __attribute__((address_space(3))) T*)at;
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(uint32_t at, T v) {
+  *(__attribute__((address_space(3))) T*)at = v;
 }
 
 // exponent bits of a 16-bit type: all set in infinities and NaN
@@ -188,9 +198,22 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int c = 0; c < NC; ++c) q[c] = *reinterpret_cast<const uint4_t*>(qp + c * 16);
     }
     const float zscale = a.scale * kLog2e;
-    const int window = a.window, sinks = a.sinks;
-    char* const kl = lds + half * 2 * BUFS * KB;
-    char* const vl = kl + BUFS * KB;
+    const uint32_t kl = (uint32_t)(uintptr_t)(lds_void_t*)lds + half * 2 * BUFS * KB;
+    const uint32_t vl = kl + BUFS * KB;
+
+    // Tiles by what the wave's rows see of them: all of [whole0, whole1) and of those below
+    // `sink_tiles`, nothing of [out0, out1) and from past1 on, and of the others each row
+    // its own; from out0 on a tile is one stretch of tokens without a sink.  All rows of
+    // the workgroup see all of [same0, same1).
+    const int shift = vis.from - vis.first;                // token of visible i >= first
+    const int sink_tiles = vis.first / kTile, one0 = (vis.first + kTile - 1) / kTile;
+    const int whole0 = max(one0, ((wave_hi - a.window - shift) >> 6) + 1);
+    const int whole1 = ((wave_lo - (kTile - 1) - shift) >> 6) + 1;
+    const int out0 = max(one0, (a.sinks - shift + kTile - 1) >> 6);
+    const int out1 = ((wave_lo - a.window - (kTile - 1) - shift) >> 6) + 1;
+    const int past1 = rw < count ? ((wave_hi - shift) >> 6) + 1 : 0;
+    const int same0 = max(one0, ((wg_hi - a.window - shift) >> 6) + 1);
+    const int same1 = ((wg_lo - (kTile - 1) - shift) >> 6) + 2 - KS;
 
     // LDS addresses of this lane in a tile: of keys for the first k-step (that of step c is
     // this one xor 32 c), of values for the first 32 components (block b's: xor 64 b)
@@ -259,8 +282,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(
                                   (first + r) * 4, (int)off) << 4;
           const int to = buf * KB + wave * RW * RB + j * 1024;
-          lds_dma16(kbase + at + ((lane % PC ^ key_swap<D>(row)) << 4), (lds_void_t*)(kl + to));
-          lds_dma16(vbase + at + ((lane % PC ^ value_swap<D>(row)) << 4), (lds_void_t*)(vl + to));
+          lds_dma16(kbase + at + ((lane % PC ^ key_swap<D>(row)) << 4), (lds_void_t*)(uintptr_t)(kl + to));
+          lds_dma16(vbase + at + ((lane % PC ^ value_swap<D>(row)) << 4), (lds_void_t*)(uintptr_t)(vl + to));
         }
       }
     };
@@ -272,10 +295,9 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           const uint2_t k0 = widen4<DT>(kc[w]), k1 = widen4<DT>(kc[w + 1]);
           const uint2_t v0 = widen4<VT>(vc[w]), v1 = widen4<VT>(vc[w + 1]);
           const int piece = lane % GROUP * (CB / 8) + w / 2, at = buf * KB + row * RB;
-          *reinterpret_cast<uint4_t*>(kl + at + ((piece ^ key_swap<D>(row)) << 4)) =
-              uint4_t{k0[0], k0[1], k1[0], k1[1]};
-          *reinterpret_cast<uint4_t*>(vl + at + ((piece ^ value_swap<D>(row)) << 4)) =
-              uint4_t{v0[0], v0[1], v1[0], v1[1]};
+          lds_put(kl + at + ((piece ^ key_swap<D>(row)) << 4), uint4_t{k0[0], k0[1], k1[0], k1[1]});
+          lds_put(vl + at + ((piece ^ value_swap<D>(row)) << 4),
+                  uint4_t{v0[0], v0[1], v1[0], v1[1]});
         }
         if (lane % GROUP < 2) scales[half][buf][lane % GROUP][row] = sc;
       }
@@ -285,18 +307,12 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     // them.  In steps where rows of the workgroup see different tokens, such values
     // become 0 in LDS and their tokens' bits are set in `odd`; the sums of the rows that do
     // see them get them by hand.
-    auto differ = [&](int t0) {                            // the same for the workgroup
-      const int i0 = t0 * kTile, i1 = i0 + KS * kTile;
-      const bool one = i0 >= vis.first || i1 <= vis.first;
-      return !(one && i1 <= vis.n && token_at(i1 - 1) <= wg_lo &&
-               (wg_hi - token_at(i0) < window || token_at(i1 - 1) < sinks));
-    };
     auto clear_odd = [&](int buf, int step) {
 #pragma unroll
       for (int i = 0; i < KB / 16 / HT; ++i) {
         const int at = (i * HT + ht) * 16;
-        uint4_t* p = reinterpret_cast<uint4_t*>(vl + buf * KB + at);
-        uint4_t x = *p;
+        const uint32_t p = vl + buf * KB + at;
+        uint4_t x = lds_at<uint4_t>(p);
         typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
         us2_t top = {0, 0};
 #pragma unroll
@@ -309,7 +325,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             if ((x[w] & kE) == kE) x[w] &= 0xFFFF0000u;
             if ((x[w] >> 16 & kE) == kE) x[w] &= 0x0000FFFFu;
           }
-          *p = x;
+          lds_put(p, x);
           atomicOr(&odd[half][step & 1][at / RB / 32], 1u << (at / RB % 32));
         }
       }
@@ -344,26 +360,27 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     };
 
     auto compute = [&](int t, int buf, int step, bool mixed) {
-      const int i0 = t * kTile, tok0 = token_at(i0), tok1 = token_at(i0 + kTile - 1);
-      // whether the wave's rows see all of the tile, or nothing
-      const bool straight = i0 >= vis.first || i0 + kTile <= vis.first;
-      const bool outside = tok0 > wave_hi || rw >= count ||
-                           (straight && tok0 >= sinks && wave_lo - tok1 >= window);
-      if (outside) return;
-      const bool whole = straight && i0 + kTile <= vis.n && tok1 <= wave_lo &&
-                         (wave_hi - tok0 < window || tok1 < sinks);
-      const int k = (int)(kl - lds) + buf * KB, v = (int)(vl - lds) + buf * KB;
+      if (t >= past1 || (t >= out0 && t < out1)) return;
+      const bool whole = (t >= whole0 && t < whole1) || t < sink_tiles;
       float16v_t z[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) z[b][e] = 0.0f;
+      const uint32_t k = kl + buf * KB + ka, v = vl + buf * KB + va;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          z[b] = mfma32<DT>(*reinterpret_cast<const uint4_t*>(lds + ((k + ka) ^ (c << 5)) + b * 32 * RB),
-                            q[c], z[b]);
+          z[b] = mfma32<DT>(lds_at<uint4_t>((k ^ (c << 5)) + b * 32 * RB), q[c], z[b]);
+      // three k-steps of operands ahead of the products
+      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+      for (int c = 0; c < NC - 3; ++c) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
       // a wave of this SIMD that is past its scores goes before one that multiplies
       __builtin_amdgcn_s_setprio(1);
       // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
@@ -380,8 +397,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           }
       }
       if (!whole) {
-        if (straight && tok0 >= sinks) {
-          const int x = tok0 + 4 * hi - see;
+        if (t >= out0) {
+          const int x = t * kTile + shift + 4 * hi - see;
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -394,7 +411,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int tok = token_at(i0 + 32 * b + 8 * (e / 4) + 4 * hi + e % 4);
+              const int tok = token_at(t * kTile + 32 * b + 8 * (e / 4) + 4 * hi + e % 4);
               const bool ok = ((uint32_t)(tok - see) < (uint32_t)width) | (tok < sunk);
               z[b][e] = ok ? z[b][e] : -INFINITY;
             }
@@ -461,7 +478,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           }
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
-            const uint4_t x = read_transposed(lds + ((v + va) ^ (e << 6)) + (32 * b + 16 * s) * RB, 8 * RB);
+            const uint4_t x = read_transposed((v ^ (e << 6)) + (32 * b + 16 * s) * RB, 8 * RB);
             o[e] = mfma32<VT>(x, p, o[e]);
             if constexpr (TWO) o[e] = mfma32<VT>(x, rest, o[e]);
           }
@@ -498,7 +515,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       lgkm_wait0();
       wg_barrier();
       if constexpr (!F8) load(step + AHEAD, buf == 0 ? BUFS - 1 : buf - 1);
-      const bool mixed = differ(t - half);
+      const int t0 = t - half;
+      const bool mixed = !((t0 >= same0 && t0 < same1) || t0 + KS <= sink_tiles);
       if (ht < 2) odd[half][(step + 1) & 1][ht] = 0;
       if (mixed) {
         clear_odd(buf, step);

@@ -233,6 +233,7 @@ struct AppendCall {
 };
 hipError_t launch_append_kv(const AppendCall& c, hipStream_t s);
 
+constexpr int32_t kNoWindow = 1 << 30;         // sequences have at most as many tokens
 struct AttentionCall {
   const uint16_t* q;
   int dt;
@@ -244,7 +245,7 @@ struct AttentionCall {
   int64_t max_pages, ldp;
   const int32_t* lens;
   float scale;
-  int32_t window, sinks;     // window INT32_MAX: none
+  int32_t window, sinks;     // kNoWindow and above (past every position): none
   uint16_t* y;
   float* lse;                // or nullptr
   float* ws;

@@ -417,16 +417,16 @@ wq_status check_attention(const void* q, int32_t dt, int64_t m, int64_t heads, i
   if (!attention_sizes_ok(m, heads, cache) || !rows_ok(m, heads * cache->head_dim, ldq))
     return WQ_ERR_SHAPE;
   if (batch < 1 || batch >= kMaxDim || !sizes_ok(batch, max_pages) || ldp < max_pages ||
-      ldp >= kMaxDim || max_pages > (int64_t(1) << 30) / cache->page_size)
+      ldp >= kMaxDim || max_pages > kNoWindow / cache->page_size)
     return WQ_ERR_SHAPE;
   if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return WQ_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(pages, 4) || !aligned(lens, 4) || !aligned(y, 16) ||
       !aligned(lse, 4))
     return WQ_ERR_ALIGN;
-  auto i32 = [](int64_t v) { return (int32_t)std::min<int64_t>(v, INT32_MAX); };
+  auto i32 = [](int64_t v) { return (int32_t)std::min<int64_t>(v, kNoWindow); };
   *c = AttentionCall{static_cast<const uint16_t*>(q), dt, m, heads, ldq, nullptr, batch,
                      kernel_cache(cache), pages, max_pages, ldp, lens, scale,
-                     window == 0 ? INT32_MAX : i32(window), i32(sinks),
+                     window == 0 ? kNoWindow : i32(window), i32(sinks),
                      static_cast<uint16_t*>(y), lse, nullptr};
   return WQ_OK;
 }
