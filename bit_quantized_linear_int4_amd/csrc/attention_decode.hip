@@ -550,8 +550,11 @@ hipError_t decode_go(const AttentionCall& a, hipStream_t s) {
   // what a row can see at most
   int64_t most = std::min<int64_t>(a.max_pages << a.cache.lg_page, int64_t(1) << 30);
   most = std::min<int64_t>(most, (int64_t)a.window + a.sinks);
-  // a unit is one step, more where the line could pass 32 bits
-  int lg_unit = 7;
+  // A unit is one step.  It is four where no item has more, so that none is split and the
+  // join not launched (bf16, 8 kv heads of 128: 1 sequence of 250 tokens 6.3 us and 7.9
+  // split, of 500 8.2 and 8.2, 64 of 500 27.6 and 29.6; and the call one launch, 3.6 us of
+  // the host's time, shorter), and more where the line could pass 32 bits.
+  int lg_unit = most <= (kStep << 2) ? 9 : 7;
   while (((most >> lg_unit) + 1) > (int64_t(1) << 30) / items) ++lg_unit;
   const int64_t units = (most + (int64_t(1) << lg_unit) - 1) >> lg_unit;
   const int wgs = decode_wgs(items, units);

@@ -299,7 +299,8 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
           lds_put(vl + at + ((piece ^ value_swap<D>(row)) << 4),
                   uint4_t{v0[0], v0[1], v1[0], v1[1]});
         }
-        if (lane % GROUP < 2) scales[half][buf][lane % GROUP][row] = sc;
+        // those of keys with the scale of z in them
+        if (lane % GROUP < 2) scales[half][buf][lane % GROUP][row] = lane % GROUP == 0 ? sc * zscale : sc;
       }
     };
 
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
             const float4_t ks =
                 *reinterpret_cast<const float4_t*>(&scales[half][buf][0][32 * b + 8 * j + 4 * hi]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[b][4 * j + e] *= ks[e] * zscale;
+            for (int e = 0; e < 4; ++e) z[b][4 * j + e] *= ks[e];
           }
       }
       if (!whole) {
@@ -445,19 +446,23 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
         }
       l += sum;
       if constexpr (F8) {
-        // the scales of the values join the weights; a weight of 0 stays 0
+        // the scales of the values join the weights; where rows see different tokens, a
+        // weight of 0 stays 0
+        auto scale = [&](auto f) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4_t vs =
-                *reinterpret_cast<const float4_t*>(&scales[half][buf][1][32 * b + 8 * j + 4 * hi]);
+            for (int j = 0; j < 4; ++j) {
+              const float4_t vs =
+                  *reinterpret_cast<const float4_t*>(&scales[half][buf][1][32 * b + 8 * j + 4 * hi]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float w = z[b][4 * j + e];
-              z[b][4 * j + e] = whole || w != 0.0f ? w * vs[e] : 0.0f;
+              for (int e = 0; e < 4; ++e) z[b][4 * j + e] = f(z[b][4 * j + e], vs[e]);
             }
-          }
+        };
+        if (whole)
+          scale([](float w, float s) { return w * s; });
+        else
+          scale([](float w, float s) { return w != 0.0f ? w * s : 0.0f; });
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b)

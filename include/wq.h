@@ -532,8 +532,9 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
  * inside, lens past max_pages * page_size (at most 2^30) as that.  Places that no row
  * sees are not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32 [m][heads] or NULL.
  * A query, key or scale that is not finite makes what it enters not finite or, where
- * its z is -inf, leaves it out; a value that is not finite makes the components that
- * it enters not finite.  No other row is touched by it.
+ * its z is -inf, leaves it out; a value (or its scale) that is not finite makes the
+ * components that it enters not finite, unless its weight underflows to 0.  No other
+ * row is touched by it.
  * heads a multiple of kv_heads, at most 1024; ldq a multiple of 8; window and sinks
  * >= 0; scale > 0, finite; q and y 16-byte, pages, lens, lse 4-byte aligned.
  * workspace: at least wq_attention_decode_workspace(m, heads, cache) bytes, 256-byte
