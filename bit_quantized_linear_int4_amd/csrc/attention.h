@@ -9,6 +9,20 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 typedef float float16v_t __attribute__((ext_vector_type(16)));
 
+// Division of numbers below 2^31 by one that the host knows: n / d is
+// (n + n * mul / 2^32) >> shift with 2^shift >= d the smallest such power.
+struct Divisor {
+  uint32_t d, mul, shift;
+  static Divisor of(uint32_t d) {
+    uint32_t s = 0;
+    while ((1u << s) < d) ++s;
+    return Divisor{d, (uint32_t)((((uint64_t)1 << 32) * ((1u << s) - d)) / d + 1), s};
+  }
+  __device__ __forceinline__ int quotient(int n) const {
+    return (int)(((uint32_t)n + __umulhi((uint32_t)n, mul)) >> shift);
+  }
+};
+
 // What a row at `pos` sees of its sequence: the tokens [0, first) and [from, pos],
 // `n` in all; visible token i is token i for i < first, else i - first + from.
 struct Visible {

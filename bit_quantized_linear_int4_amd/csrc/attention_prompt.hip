@@ -30,8 +30,9 @@ constexpr int kPartSteps = 4;          // steps of a part at least
 
 struct PromptArgs {
   AttentionCall a;
-  int group;                           // query heads per kv head
-  int splits;                          // parts of the visible tokens, each a workgroup's
+  Divisor group;                       // query heads per kv head
+  Divisor kv_heads;
+  Divisor splits;                      // parts of the visible tokens, each a workgroup's
   uint32_t page16, token16;            // strides in 16 bytes; a cache spans less than 2^31
 };
 
@@ -139,36 +140,37 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
 
   // this workgroup's kv head, and its tile of rows: later rows of a sequence, which see
   // more, come first
-  const int batch = (int)a.batch, group = args.group;
-  int work = blockIdx.x;
-  const int kh = work % cc.kv_heads;
-  work /= cc.kv_heads;
-  const int split = work % args.splits;
-  work /= args.splits;
+  const int batch = (int)a.batch, group = (int)args.group.d;
+  const int of_head = args.kv_heads.quotient(blockIdx.x), kh = blockIdx.x - of_head * cc.kv_heads;
+  const int work = args.splits.quotient(of_head), split = of_head - work * (int)args.splits.d;
   auto tiles = [&](int i) { return (rows_of(a, i).n * group + BM - 1) / BM; };
-  const Line line = batch == 1 ? Line{tiles(0), 0} : line_up<NT>(batch, part, tiles);
-  if (work >= __builtin_amdgcn_readfirstlane(line.total)) return;
-  int before;
-  const int seq = __builtin_amdgcn_readfirstlane(
-      line_find<NT>(batch, line, part, work, before, tiles));
+  int seq = 0, before = 0;
+  if (batch > 1) {
+    const Line line = line_up<NT>(batch, part, tiles);
+    if (work >= __builtin_amdgcn_readfirstlane(line.total)) return;
+    seq = __builtin_amdgcn_readfirstlane(line_find<NT>(batch, line, part, work, before, tiles));
+    before = __builtin_amdgcn_readfirstlane(before);
+  }
   const Rows rows = uniform_rows(a, seq);
   const int count = rows.n * group;                      // of this sequence and kv head
-  const int row_tile = (count + BM - 1) / BM - 1 - (work - __builtin_amdgcn_readfirstlane(before));
+  const int row_tile = (count + BM - 1) / BM - 1 - (work - before);
+  if (row_tile < 0) return;
   const int len = tokens_of(a, scalar_at(a.lens, seq));
   const int before_rows = len - rows.n;                  // position of row 0; may be negative
 
   // this lane's row, and what the wave's and the workgroup's rows see
   const int r0 = row_tile * BM, rw = r0 + wave * 32, r = rw + nl;
   const bool live = r < count;
-  const int token = min(r, count - 1) / group, head = kh * group + min(r, count - 1) % group;
+  const int token = args.group.quotient(min(r, count - 1));
+  const int head = kh * group + min(r, count - 1) - token * group;
   const int pos = before_rows + token;
   // it sees the tokens [see, see + width) and those below `sunk`
   const int see = pos >= a.window ? pos - a.window + 1 : 0;
   const int width = max(pos + 1 - see, 0), sunk = min(a.sinks, max(pos + 1, 0));
-  const int wave_lo = before_rows + min(rw, count - 1) / group;
-  const int wave_hi = before_rows + min(rw + 31, count - 1) / group;
-  const int wg_lo = max(before_rows + r0 / group, 0);
-  const int wg_hi = before_rows + min(r0 + BM - 1, count - 1) / group;
+  const int wave_lo = before_rows + args.group.quotient(min(rw, count - 1));
+  const int wave_hi = before_rows + args.group.quotient(min(rw + 31, count - 1));
+  const int wg_lo = max(before_rows + args.group.quotient(r0), 0);
+  const int wg_hi = before_rows + args.group.quotient(min(r0 + BM - 1, count - 1));
   // the tokens that some row sees: as one row's, from the first row's window on
   Visible vis;
   vis.from = wg_lo >= a.window ? wg_lo - a.window + 1 : 0;
@@ -178,7 +180,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   // parts of at least kPartSteps steps; those past the last one are empty (tiles are below 2^24,
   // splits at most 64)
   const int all_tiles = (vis.n + kTile - 1) / kTile;
-  const int parts = min(args.splits, max(all_tiles / (kPartSteps * KS), 1));
+  const int parts = min((int)args.splits.d, max(all_tiles / (kPartSteps * KS), 1));
   const int t_begin = split < parts ? all_tiles * split / parts : 0;
   const int t_end = split < parts ? all_tiles * (split + 1) / parts : 0;
 
@@ -565,11 +567,11 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
       for (int e = 0; e < 16; ++e) o[b][e] = o[b][e] * f + x[(2 + 16 * b + e) * 64] * g;
   }
   const auto k = args_here<PromptArgs>();
-  if (k->splits > 1) {
+  if (k->splits.d > 1) {
     // m, l and the sums of this part
     if (!live) return;
     const int64_t total = k->a.m * k->a.heads;
-    float* ml = k->a.ws + (int64_t)k->splits * total * D + (split * total + out) * 2;
+    float* ml = k->a.ws + (int64_t)k->splits.d * total * D + (split * total + out) * 2;
     if (hi == 0) {
       ml[0] = m;
       ml[1] = l;
@@ -610,22 +612,23 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
 template <int DT, int D>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float shift) {
   const AttentionCall& a = args.a;
+  const int splits = (int)args.splits.d;
   const int64_t total = a.m * a.heads, per = 256 / (D / 8);
   const int64_t out = (int64_t)blockIdx.x * per + threadIdx.x / (D / 8);
   const int c = threadIdx.x % (D / 8);
   if (out >= total) return;
   const int64_t row = out / a.heads;
   if (row < a.starts[0] || row >= a.starts[a.batch]) return;
-  const float* ml = a.ws + (int64_t)args.splits * total * D;
+  const float* ml = a.ws + (int64_t)splits * total * D;
   float m = -INFINITY, l = 0.0f, x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.0f;
   constexpr int U = 8;                                   // parts whose loads are in flight
-  for (int s0 = 0; s0 < args.splits; s0 += U) {
+  for (int s0 = 0; s0 < splits; s0 += U) {
     float pm[U], pl[U], px[U][8];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t at = min(s0 + i, args.splits - 1) * total + out;
+      const int64_t at = min(s0 + i, splits - 1) * total + out;
       pm[i] = ml[2 * at];
       pl[i] = ml[2 * at + 1];
 #pragma unroll
@@ -638,7 +641,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       // a part without sums has written none
-      const bool some = s0 + i < args.splits && pm[i] != -INFINITY;
+      const bool some = s0 + i < splits && pm[i] != -INFINITY;
       const float mn = some ? fmaxf(m, pm[i]) : m;
       const float fade = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
       const float f = some ? __builtin_amdgcn_exp2f(pm[i] - mn) : 0.0f;
@@ -684,7 +687,8 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   const auto kern = prompt_kernel<DT, CT, D, KS>;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), kLds, done);
   if (e != hipSuccess) return e;
-  const PromptArgs args{a, (int)(a.heads / a.cache.kv_heads), p.splits,
+  const PromptArgs args{a, Divisor::of((uint32_t)(a.heads / a.cache.kv_heads)),
+                        Divisor::of((uint32_t)a.cache.kv_heads), Divisor::of((uint32_t)p.splits),
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
   const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
