@@ -608,53 +608,72 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
     k->a.lse[out] = l == 0.0f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// joins the parts of a row and head: D / 8 threads
-template <int DT, int D>
+// Joins the parts of a row and head: G groups of D / 4 threads take them in turn, four
+// loaded together.
+template <int DT, int D, int G>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float shift) {
+  constexpr int L = D / 4, U = 4;
+  constexpr int kPer = 256 / (L * G);                    // rows and heads of a workgroup
   const AttentionCall& a = args.a;
   const int splits = (int)args.splits.d;
-  const int64_t total = a.m * a.heads, per = 256 / (D / 8);
-  const int64_t out = (int64_t)blockIdx.x * per + threadIdx.x / (D / 8);
-  const int c = threadIdx.x % (D / 8);
-  if (out >= total) return;
-  const int64_t row = out / a.heads;
-  if (row < a.starts[0] || row >= a.starts[a.batch]) return;
+  const int who = threadIdx.x / (L * G), g = threadIdx.x / L % G, c = threadIdx.x % L;
+  const int64_t total = a.m * a.heads;
+  const int64_t out = min((int64_t)blockIdx.x * kPer + who, total - 1), row = out / a.heads;
+  const bool live = (int64_t)blockIdx.x * kPer + who < total && row >= a.starts[0] &&
+                    row < a.starts[a.batch];
   const float* ml = a.ws + (int64_t)splits * total * D;
-  float m = -INFINITY, l = 0.0f, x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-  constexpr int U = 8;                                   // parts whose loads are in flight
-  for (int s0 = 0; s0 < splits; s0 += U) {
-    float pm[U], pl[U], px[U][8];
+  float m = -INFINITY, l = 0.0f;
+  float4_t x = {0, 0, 0, 0};
+  for (int s0 = g; s0 < splits; s0 += U * G) {
+    float pm[U], pl[U];
+    float4_t px[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t at = min(s0 + i, splits - 1) * total + out;
+      const int64_t at = min(s0 + i * G, splits - 1) * total + out;
       pm[i] = ml[2 * at];
       pl[i] = ml[2 * at + 1];
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4_t v = *reinterpret_cast<const float4_t*>(a.ws + at * D + c * 8 + e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) px[i][e + j] = v[j];
-      }
+      px[i] = *reinterpret_cast<const float4_t*>(a.ws + at * D + c * 4);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       // a part without sums has written none
-      const bool some = s0 + i < splits && pm[i] != -INFINITY;
+      const bool some = s0 + i * G < splits && pm[i] != -INFINITY;
       const float mn = some ? fmaxf(m, pm[i]) : m;
       const float fade = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
       const float f = some ? __builtin_amdgcn_exp2f(pm[i] - mn) : 0.0f;
       l = l * fade + (some ? pl[i] * f : 0.0f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * fade + (some ? px[i][e] * f : 0.0f);
+      for (int e = 0; e < 4; ++e) x[e] = x[e] * fade + (some ? px[i][e] * f : 0.0f);
       m = mn;
     }
   }
-  const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+  if constexpr (G > 1) {
+    __shared__ __align__(16) float sx[kPer][G][D];
+    __shared__ float sm[kPer][G], sl[kPer][G];
+    *reinterpret_cast<float4_t*>(&sx[who][g][c * 4]) = x;
+    if (c == 0) {
+      sm[who][g] = m;
+      sl[who][g] = l;
+    }
+    __syncthreads();
+    if (g != 0) return;
+    float big = m;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= inv;
-  *reinterpret_cast<uint4_t*>(a.y + out * D + c * 8) = pack8<DT>(x);
+    for (int i = 1; i < G; ++i) big = fmaxf(big, sm[who][i]);
+    x = float4_t{0, 0, 0, 0};
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const float f = __builtin_amdgcn_exp2f(sm[who][i] - exp_ref(big));
+      l += sl[who][i] * f;
+      x += f * *reinterpret_cast<const float4_t*>(&sx[who][i][c * 4]);
+    }
+    m = big;
+  }
+  if (!live) return;
+  const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+  *reinterpret_cast<uint2_t*>(a.y + out * D + c * 4) =
+      uint2_t{pack2<DT>(x[0] * inv, x[1] * inv), pack2<DT>(x[2] * inv, x[3] * inv)};
   if (a.lse != nullptr && c == 0)
     a.lse[out] = l == 0.0f ? -INFINITY : (m - shift + __builtin_amdgcn_logf(l)) * kLn2;
 }
@@ -696,9 +715,15 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
-  const int64_t per = 256 / (D / 8);
-  prompt_join_kernel<DT, D>
-      <<<dim3((unsigned)((a.m * a.heads + per - 1) / per)), 256, 0, s>>>(args, kShift);
+  // many parts: a workgroup's threads share them
+  const int64_t total = a.m * a.heads;
+  if (p.splits >= 8) {
+    const int64_t per = 32 / (D / 4);
+    prompt_join_kernel<DT, D, 8><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
+  } else {
+    const int64_t per = 256 / (D / 4);
+    prompt_join_kernel<DT, D, 1><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
+  }
   return hipGetLastError();
 }
 template <int DT, int CT, int D>
