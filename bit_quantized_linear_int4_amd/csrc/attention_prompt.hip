@@ -33,6 +33,9 @@ struct PromptArgs {
   Divisor group;                       // query heads per kv head
   Divisor kv_heads;
   Divisor splits;                      // parts of the visible tokens, each a workgroup's
+  int longest_first;                   // the order of the workgroups; up to 64 sequences
+  int tokens;                          // of a workgroup's rows, at least 1
+  Divisor by_tokens;
   uint32_t page16, token16;            // strides in 16 bytes; a cache spans less than 2^31
 };
 
@@ -52,6 +55,22 @@ __device__ __forceinline__ Rows uniform_rows(const AttentionCall& a, int i) {
   const int s = min(max(scalar_at(a.starts, i), 0), m);
   const int e = min(max(scalar_at(a.starts, i + 1), 0), m);
   return Rows{s, max(e - s, 0)};
+}
+
+// sum and largest over the wave, in every lane
+__device__ __forceinline__ int sum_wave(int v) {
+  uint32_t s = (uint32_t)v;
+  s += dpp<0xB1>(s);
+  s += dpp<0x4E>(s);
+  s += dpp<0x141>(s);
+  s += dpp<0x140>(s);
+  return (__builtin_amdgcn_readlane((int)s, 0) + __builtin_amdgcn_readlane((int)s, 16)) +
+         (__builtin_amdgcn_readlane((int)s, 32) + __builtin_amdgcn_readlane((int)s, 48));
+}
+__device__ __forceinline__ int max_wave(int v) {         // of values from 0 on
+  const int s = (int)max16((uint32_t)v);
+  return max(max(__builtin_amdgcn_readlane(s, 0), __builtin_amdgcn_readlane(s, 16)),
+             max(__builtin_amdgcn_readlane(s, 32), __builtin_amdgcn_readlane(s, 48)));
 }
 
 template <int T>
@@ -144,16 +163,49 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   const int of_head = args.kv_heads.quotient(blockIdx.x), kh = blockIdx.x - of_head * cc.kv_heads;
   const int work = args.splits.quotient(of_head), split = of_head - work * (int)args.splits.d;
   auto tiles = [&](int i) { return (rows_of(a, i).n * group + BM - 1) / BM; };
-  int seq = 0, before = 0;
-  if (batch > 1) {
+  int seq = 0, nth = work;                               // of the sequence's tiles, last first
+  if (KS == 1 && batch > 1 && args.longest_first) {
+    // All sequences' tiles by decreasing tokens: those of a lane's sequence have `size`,
+    // and BM / group less each.  The least x that at most `work` tiles pass, and of the
+    // tiles of just x tokens the one in its turn.
+    const int mine = min(lane, batch - 1), step = args.tokens;
+    const int have = lane < batch ? tiles(mine) : 0;
+    const int size = tokens_of(a, a.lens[mine]);
+    auto longer = [&](int x) {
+      return min(args.by_tokens.quotient(max(size - x + step - 1, 0)), have);
+    };
+    int lo = -1, hi = 0;                                   // keys below 0 count as 0: rows
+    hi = max_wave(have > 0 ? size : 0);                    // before their sequence
+    if (work >= sum_wave(have)) return;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sum_wave(longer(mid)) <= work) hi = mid; else lo = mid;
+    }
+    // (for x = -1 all that are there)
+    const int above = longer(hi), with = lo < 0 ? have : longer(lo);
+    int turn = work - sum_wave(above);
+    uint64_t lanes = __ballot(with > above);
+    if (hi == 0) {
+      // several tiles of a sequence may be left, all of few tokens or none: in its order
+      const int left = with - above, behind = scan64(left) - left;
+      lanes = __ballot(lane < batch && behind <= turn && turn < behind + left);
+      seq = __builtin_ctzll(lanes);
+      nth = __builtin_amdgcn_readlane(above, seq) + turn - __builtin_amdgcn_readlane(behind, seq);
+    } else {
+      for (; turn > 0; --turn) lanes &= lanes - 1;
+      seq = __builtin_ctzll(lanes);
+      nth = __builtin_amdgcn_readlane(above, seq);
+    }
+  } else if (batch > 1) {
     const Line line = line_up<NT>(batch, part, tiles);
     if (work >= __builtin_amdgcn_readfirstlane(line.total)) return;
+    int before;
     seq = __builtin_amdgcn_readfirstlane(line_find<NT>(batch, line, part, work, before, tiles));
-    before = __builtin_amdgcn_readfirstlane(before);
+    nth = work - __builtin_amdgcn_readfirstlane(before);
   }
   const Rows rows = uniform_rows(a, seq);
   const int count = rows.n * group;                      // of this sequence and kv head
-  const int row_tile = (count + BM - 1) / BM - 1 - (work - before);
+  const int row_tile = (count + BM - 1) / BM - 1 - nth;
   if (row_tile < 0) return;
   const int len = tokens_of(a, scalar_at(a.lens, seq));
   const int before_rows = len - rows.n;                  // position of row 0; may be negative
@@ -691,7 +743,8 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
   PromptPlan p{1, 1, tiles(256)};
   if (p.tiles * c.kv_heads >= 512) return p;
   p = PromptPlan{2, 1, tiles(128)};
-  const int64_t wgs = p.tiles * c.kv_heads;
+  // parts that fill the GPU once, by the tiles that there are in earnest
+  const int64_t wgs = std::max((rows + 127) / 128, std::min(batch, m)) * c.kv_heads;
   const int64_t steps = (most + 2 * kTile - 1) / (2 * kTile);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, 256 / wgs, steps / kPartSteps}));
   return p;
@@ -706,11 +759,19 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   const auto kern = prompt_kernel<DT, CT, D, KS>;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), kLds, done);
   if (e != hipSuccess) return e;
-  const PromptArgs args{a, Divisor::of((uint32_t)(a.heads / a.cache.kv_heads)),
-                        Divisor::of((uint32_t)a.cache.kv_heads), Divisor::of((uint32_t)p.splits),
+  const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
+  const uint32_t group = (uint32_t)(a.heads / a.cache.kv_heads);
+  const uint32_t tokens = std::max<uint32_t>(256 / KS / group, 1);
+  // Past one round of workgroups the order matters: 11 prompts of 5730 tokens, 4 heads, 519
+  // us in the sequences' order and 447 by length; 11 of 2000, 32 heads, 435 and 440, what
+  // finding it costs.  Rounds of shorter workgroups gain nothing (16 sequences of 4 rows 59
+  // and 62).
+  const bool longest_first = KS == 1 && a.batch > 1 && a.batch <= 64;
+  const PromptArgs args{a, Divisor::of(group), Divisor::of((uint32_t)a.cache.kv_heads),
+                        Divisor::of((uint32_t)p.splits), longest_first, (int)tokens,
+                        Divisor::of(tokens),
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
-  const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
   kern<<<dim3((unsigned)wgs), 512, kLds, s>>>(args);
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

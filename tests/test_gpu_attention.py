@@ -402,6 +402,11 @@ PROMPT = [
     (12, 4, 64, 32, "token", [190] + [1, 0, 4] * 50, [100] + [30, 5, 0] * 50, 61, 5),
     (4, 4, 128, 64, "head", [520, 257] + [1] * 130, [0, 64] + [3] * 130, 0, 0),
     (4, 4, 64, 16, "token", [600] + [2] * 129, [30] + [9] * 129, 200, 70),
+    # more workgroups than run at once, up to 64 sequences: the longest come first
+    (32, 32, 64, 16, "head", [40, 1, 0, 300, 77, 130, 5, 64, 3],
+     [0, 200, 5, 10, 0, 30, 400, 0, 90], 0, 0),
+    (64, 16, 128, 32, "head", [70, 2, 70, 33], [5, 100, 5, 0], 20, 2),
+    (56, 8, 64, 16, "head", [9, 1, 30] * 14, [0, 33, 4] * 14, 0, 0),
 ]
 
 
@@ -447,6 +452,17 @@ def test_prompt_leaves_other_rows():
     check(y, lse, q, c.values(), rows, 128 ** -0.5, 0, 0, ULP["bf16"], "bf16", table.cpu().numpy())
     y, lse = run_prompt(q, i32(starts), c, table, i32([0, -5]))
     assert not y[3:38].any() and torch.all(lse[3:38] == -float("inf"))
+
+
+def test_rows_before_their_sequences():
+    """More rows than tokens in several sequences, with many workgroups."""
+    case = (40, 40, 64, 16, "head", [150, 3, 140, 40, 9, 300, 1], [0] * 7, 0, 0)
+    q, starts, c, table, _, _ = prompt_case(case, "bf16", "bf16")
+    lens = [20, 0, 140, 1, -2, 33, 1]
+    y, lse = run_prompt(q, i32(starts), c, table, i32(lens))
+    rows = [(starts[s] + i, s, lens[s] - n + i if lens[s] > 0 else -1, max(lens[s], 0))
+            for s, n in enumerate(case[5]) for i in range(n)]
+    check(y, lse, q, c.values(), rows, 0.125, 0, 0, ULP["bf16"], "bf16", table.cpu().numpy())
 
 
 def test_tables_and_lens_past_their_ends():
