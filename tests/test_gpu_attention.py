@@ -402,11 +402,12 @@ PROMPT = [
     (12, 4, 64, 32, "token", [190] + [1, 0, 4] * 50, [100] + [30, 5, 0] * 50, 61, 5),
     (4, 4, 128, 64, "head", [520, 257] + [1] * 130, [0, 64] + [3] * 130, 0, 0),
     (4, 4, 64, 16, "token", [600] + [2] * 129, [30] + [9] * 129, 200, 70),
-    # more workgroups than run at once, up to 64 sequences: the longest come first
-    (32, 32, 64, 16, "head", [40, 1, 0, 300, 77, 130, 5, 64, 3],
+    # the same for up to 64 sequences: the longest come first
+    (64, 64, 64, 16, "head", [40, 1, 0, 300, 77, 130, 5, 64, 3],
      [0, 200, 5, 10, 0, 30, 400, 0, 90], 0, 0),
-    (64, 16, 128, 32, "head", [70, 2, 70, 33], [5, 100, 5, 0], 20, 2),
-    (56, 8, 64, 16, "head", [9, 1, 30] * 14, [0, 33, 4] * 14, 0, 0),
+    (128, 64, 64, 32, "head", [70, 2, 70, 33, 1, 0, 90, 12, 4], [5, 100, 5, 0, 30, 2, 5, 5, 5],
+     20, 2),
+    (56, 8, 128, 16, "head", [9, 1, 30] * 16, [0, 33, 4] * 16, 0, 0),
 ]
 
 
@@ -456,7 +457,7 @@ def test_prompt_leaves_other_rows():
 
 def test_rows_before_their_sequences():
     """More rows than tokens in several sequences, with many workgroups."""
-    case = (40, 40, 64, 16, "head", [150, 3, 140, 40, 9, 300, 1], [0] * 7, 0, 0)
+    case = (64, 64, 64, 16, "head", [150, 3, 140, 40, 9, 300, 1], [0] * 7, 0, 0)
     q, starts, c, table, _, _ = prompt_case(case, "bf16", "bf16")
     lens = [20, 0, 140, 1, -2, 33, 1]
     y, lse = run_prompt(q, i32(starts), c, table, i32(lens))
