@@ -130,17 +130,25 @@ __global__ __launch_bounds__(256) void append_kv_kernel(AppendCall a) {
   }
 }
 
-template <int DT, int D, bool F8>
+template <int DT, int D, bool F8, int U>
 hipError_t append_u(const AppendCall& a, hipStream_t s) {
-  constexpr int HP = 256 / (D / 8), U = 2;
+  constexpr int HP = 256 / (D / 8);
   const int64_t units = a.heads + 2 * a.cache.kv_heads;
   const dim3 grid((unsigned)a.m, (unsigned)((units + U * HP - 1) / (U * HP)));
   append_kv_kernel<DT, D, F8, U><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
+// Few rows: more workgroups, each with fewer loads before its first store; many rows: the
+// row's cos and sin serve more heads (32 query and 8 kv heads of 128, bf16 | E4M3: 1 row
+// 2.5 | 2.6 us with one head a thread and 3.1 | 3.2 with four, 128 rows 3.0 and 3.5, 512
+// 4.4 and 4.4, 8192 43.4 | 43.1 and 41.2 | 39.2).
+template <int DT, int D, bool F8>
+hipError_t append_rows(const AppendCall& a, hipStream_t s) {
+  return a.m < 512 ? append_u<DT, D, F8, 1>(a, s) : append_u<DT, D, F8, 4>(a, s);
+}
 template <int DT, int D>
 hipError_t append_f8(const AppendCall& a, hipStream_t s) {
-  return a.cache.dt == WQ_E4M3 ? append_u<DT, D, true>(a, s) : append_u<DT, D, false>(a, s);
+  return a.cache.dt == WQ_E4M3 ? append_rows<DT, D, true>(a, s) : append_rows<DT, D, false>(a, s);
 }
 template <int DT>
 hipError_t append_d(const AppendCall& a, hipStream_t s) {
