@@ -466,8 +466,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   }
 }
 
-// A workgroup takes one row of an item.  256 / (D / 4) groups of threads take its parts in turn, each with a running reference; four parts are loaded
-// together.
+// A workgroup takes one row of an item.  256 / (D / 4) groups of threads take its parts in
+// turn, each with a running reference; four parts are loaded together.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs args, float shift) {
   const AttentionCall& a = args.a;

@@ -26,7 +26,9 @@ namespace wq {
 namespace {
 
 constexpr int kTile = 64;              // tokens of a tile
-constexpr int kPartSteps = 4;          // steps of a part at least
+// Steps of a part at least: with 1, 2 and 4 of them 2 tokens behind 8000 take 15, 17 and 19
+// us, 2 x 300 behind 1000 (8 heads of 64) 23, 17 and 18.
+constexpr int kPartSteps = 2;
 
 struct PromptArgs {
   AttentionCall a;
@@ -740,8 +742,13 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
   auto tiles = [&](int64_t bm) {
     return batch == 1 ? (rows + bm - 1) / bm : rows / bm + std::min(batch, m);
   };
+  // More than a round of workgroups of 256 rows: those, which read each tile for twice the
+  // rows (32 heads on 8 of 128, KS = 1 | 2: 2600 tokens 79 | 89 us, 8 x 300 25 | 37, 8 x 200
+  // behind 3000 108 | 126).  One round or less: 128, of which the short ones of a causal
+  // prompt run beside the long ones (2048 tokens 65 | 60, 1024 behind 8000 221 | 160; only
+  // just one round behind a long context loses, 2048 behind 8000 302 | 328).
   PromptPlan p{1, 1, tiles(256)};
-  if (p.tiles * c.kv_heads >= 512) return p;
+  if (p.tiles * c.kv_heads > 256) return p;
   p = PromptPlan{2, 1, tiles(128)};
   // parts that fill the GPU once, by the tiles that there are in earnest
   const int64_t wgs = std::max((rows + 127) / 128, std::min(batch, m)) * c.kv_heads;
@@ -776,9 +783,11 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
-  // many parts: a workgroup's threads share them
+  // Many parts of few rows: groups of a workgroup's threads share them, where a group for
+  // each row would leave CUs idle (7 tokens behind 30000 33 us, 37 with one group a row; 128
+  // behind 4000 31 and 28).
   const int64_t total = a.m * a.heads;
-  if (p.splits >= 8) {
+  if (p.splits > 4 && total * (D / 4) < 256 * 256) {
     const int64_t per = 32 / (D / 4);
     prompt_join_kernel<DT, D, 8><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
   } else {

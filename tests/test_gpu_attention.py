@@ -171,6 +171,9 @@ APPEND = [
     (3, 7, 1, 128, 96, False, 1, "head"), (5, 64, 8, 64, 32, False, 32, "head"),
     (33, 5, 5, 128, 16, True, 16, "token"), (70, 28, 4, 64, 48, True, 128, "head"),
     (130, 3, 3, 128, 0, False, 8, "token"), (9, 40, 40, 128, 112, True, 16, "head"),
+    # more heads per thread
+    (512, 5, 1, 64, 64, False, 64, "head"), (600, 30, 9, 128, 64, True, 16, "token"),
+    (700, 1, 16, 64, 32, False, 16, "head"),
 ]
 
 
@@ -397,6 +400,8 @@ PROMPT = [
     (32, 2, 64, 64, "head", [17], [2000], 0, 0), (64, 8, 128, 16, "head", [3] * 9, [50] * 9, 0, 0),
     (12, 4, 128, 16, "head", [4, 9], [1500, 700], 300, 4),
     (3, 3, 64, 16, "head", [0, 0, 5], [3, 0, 0], 0, 0),
+    # many parts of many rows
+    (32, 8, 128, 64, "head", [100], [1500], 0, 0),
     # enough sequences and kv heads for workgroups of 256 rows
     (8, 4, 128, 16, "head", [200, 1, 140] + [2, 1, 3] * 43, [0, 300, 77] + [1, 40, 0] * 43, 0, 0),
     (12, 4, 64, 32, "token", [190] + [1, 0, 4] * 50, [100] + [30, 5, 0] * 50, 61, 5),
