@@ -26,15 +26,21 @@ namespace wq {
 namespace {
 
 constexpr int kTile = 64;              // tokens of a tile
-// Steps of a part at least: with 1, 2 and 4 of them 2 tokens behind 8000 take 15, 17 and 19
-// us, 2 x 300 behind 1000 (8 heads of 64) 23, 17 and 18.
-constexpr int kPartSteps = 2;
+// Parts of `steps` steps of KS tiles, at most `splits`: as many as make the time of a part
+// and of the parts' way through HBM least (about 2 us a step, and for 1e6 components of all
+// rows; there are `million` times as many).  7 tokens behind 240, 370, 500 and 1000, 32 heads
+// of 128: 10.5, 10.6, 10.5 and 11.4 us with parts of one step, 10.0, 11.8, 13.8 and 16.1 with
+// at least three; 300 behind 1000, 8 heads of 64, twice: 23 with parts of one step, 17 so.
+__host__ __device__ __forceinline__ int parts_of(int steps, int splits, float million) {
+  return min(min(splits, steps), (int)sqrtf((float)steps / million));
+}
 
 struct PromptArgs {
   AttentionCall a;
   Divisor group;                       // query heads per kv head
   Divisor kv_heads;
   Divisor splits;                      // parts of the visible tokens, each a workgroup's
+  float million;                       // components of all rows
   int longest_first;                   // the order of the workgroups; up to 64 sequences
   int tokens;                          // of a workgroup's rows, at least 1
   Divisor by_tokens;
@@ -231,10 +237,9 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
   vis.first = min(a.sinks, vis.from);
   vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
   auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
-  // parts of at least kPartSteps steps; those past the last one are empty (tiles are below 2^24,
-  // splits at most 64)
+  // parts past the last one are empty (tiles are below 2^24, splits at most 64)
   const int all_tiles = (vis.n + kTile - 1) / kTile;
-  const int parts = min((int)args.splits.d, max(all_tiles / (kPartSteps * KS), 1));
+  const int parts = max(parts_of((all_tiles + KS - 1) / KS, (int)args.splits.d, args.million), 1);
   const int t_begin = split < parts ? all_tiles * split / parts : 0;
   const int t_end = split < parts ? all_tiles * (split + 1) / parts : 0;
 
@@ -732,6 +737,10 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
     a.lse[out] = l == 0.0f ? -INFINITY : (m - shift + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+float millions(int64_t m, int64_t heads, const KvCache& c) {
+  return (float)(m * heads * c.d) * 1e-6f;
+}
+
 struct PromptPlan {
   int halves, splits;                  // KS, and parts of the tokens
   int64_t tiles;                       // of rows, at most
@@ -753,7 +762,11 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
   // parts that fill the GPU once, by the tiles that there are in earnest
   const int64_t wgs = std::max((rows + 127) / 128, std::min(batch, m)) * c.kv_heads;
   const int64_t steps = (most + 2 * kTile - 1) / (2 * kTile);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, 256 / wgs, steps / kPartSteps}));
+  const float million = millions(m, heads, c);
+  const int n = parts_of((int)steps, (int)std::min<int64_t>(64, 256 / wgs), million);
+  // where they save more than the join costs (100 behind 500, 32 heads of 128, 19.1 us in two
+  // parts and 18.0 in one; 512 behind 2000 42 and 50)
+  if (n > 1 && steps - (steps + n - 1) / n > 1.5f + 1.5f * million * n) p.splits = n;
   return p;
 }
 
@@ -775,7 +788,8 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   // and 62).
   const bool longest_first = KS == 1 && a.batch > 1 && a.batch <= 64;
   const PromptArgs args{a, Divisor::of(group), Divisor::of((uint32_t)a.cache.kv_heads),
-                        Divisor::of((uint32_t)p.splits), longest_first, (int)tokens,
+                        Divisor::of((uint32_t)p.splits),
+                        millions(a.m, a.heads, a.cache), longest_first, (int)tokens,
                         Divisor::of(tokens),
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
@@ -783,11 +797,11 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
-  // Many parts of few rows: groups of a workgroup's threads share them, where a group for
-  // each row would leave CUs idle (7 tokens behind 30000 33 us, 37 with one group a row; 128
-  // behind 4000 31 and 28).
+  // Many parts of few rows: eight groups of a workgroup's threads share them, where one
+  // group for each row would leave most CUs idle (2 tokens behind 8000 15 us, 19 with one
+  // group a row; 33 behind 700, 56 heads, 19.8 and 18.7).
   const int64_t total = a.m * a.heads;
-  if (p.splits > 4 && total * (D / 4) < 256 * 256) {
+  if (p.splits > 4 && total * (D / 4) < 256 * 64) {
     const int64_t per = 32 / (D / 4);
     prompt_join_kernel<DT, D, 8><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
   } else {
