@@ -4,11 +4,12 @@
 // context.  A workgroup takes rows of one sequence and kv head, a row being a token and
 // one of the query heads that share the kv head, tokens outermost: all of them read the
 // same keys and values, also where a chunk has few tokens.  Tiles of 64 visible tokens go
-// through LDS, the next two on their way while one is computed; a wave has 32 rows.  Eight waves
-// are 256 rows (KS = 1), or 128 whose tiles two halves of the waves take in turn (KS = 2)
-// and whose sums they join at the end, without a way through HBM: so the longest row of a
-// shorter prompt takes half as long.  Where that leaves CUs idle, parts of the tokens go
-// to workgroups of their own (`splits`), and a second kernel joins them.
+// through LDS, the next two on their way while one is computed; a wave has 32 rows.  With
+// KS = 1 a workgroup is 256 rows, 128 for heads of 64, of which three fit into a CU.  With
+// KS = 2 it is 128 rows, whose tiles two halves of its waves take in turn and whose sums
+// they join at the end, without a way through HBM: so the longest row of a shorter prompt
+// takes half as long.  Where that leaves CUs idle, parts of the tokens go to workgroups of
+// their own (`splits`), and a second kernel joins them.
 //
 // S^T = K Q^T and O^T = V^T P^T on 32x32x16 matrix instructions: the sums of S^T leave a
 // lane with one row and 16 tokens of each 32, so the softmax needs one exchange between
@@ -135,16 +136,28 @@ __device__ __forceinline__ float sum_halves(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// Row waves of a workgroup, 32 rows each.  For heads of 64 workgroups of four leave each
+// other the matrix cores at their starts and ends (10001 tokens, window 1024, 16 heads: 78
+// us, 101 with eight waves; 7 x 900 behind 500 28 and 38; 8192 tokens 342 and 343); heads of
+// 128 have registers for eight waves a CU, which load a tile once (8192 tokens 516 us, 547
+// with two workgroups of four).
+template <int D, int KS>
+constexpr int kRowWaves = D == 128 && KS == 1 ? 8 : 4;
+// waves of a SIMD that registers are left for
 template <int DT, int CT, int D, int KS>
-__global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
+constexpr int kWaves = D == 64 && KS == 1 && !(DT == WQ_F16 && CT == WQ_E4M3) ? 3 : 2;
+
+template <int DT, int CT, int D, int KS>
+__global__ __launch_bounds__(64 * KS * (kRowWaves<D, KS>), (kWaves<DT, CT, D, KS>))
+void prompt_kernel(PromptArgs args) {
   constexpr bool F8 = CT == WQ_E4M3;
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
   constexpr bool TWO = F8 && DT == WQ_F16;               // weights in two parts of bf16
   // exponents as in the decode kernel: from a reference that lags the maximum by up to
   // 2^8; weights of f16 2^7 larger
   constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
-  constexpr int NT = 512, NW = 8 / KS, BM = NW * 32;     // threads; row waves, rows
-  constexpr int HT = NT / KS;                            // threads that load a tile
+  constexpr int NW = kRowWaves<D, KS>, BM = NW * 32;     // row waves, rows
+  constexpr int HT = 64 * NW, NT = HT * KS;              // threads that load a tile; all
   constexpr int RB = D * 2;                              // bytes of a row in LDS
   constexpr int KB = kTile * RB;                         // and of a tile
   constexpr int PC = D / 8;                              // 16-byte pieces of a row
@@ -285,7 +298,7 @@ __global__ __launch_bounds__(512, 2) void prompt_kernel(PromptArgs args) {
 
     // A wave loads RW rows of each of its half's tiles.  Where they are in the cache is
     // found for GROUP tiles at once, a row in a lane, a group ahead of its use.
-    constexpr int RW = 8 * KS, GROUP = 64 / RW;
+    constexpr int RW = 64 / NW, GROUP = 64 / RW;
     auto tile_of = [&](int i) { return t_begin + i * KS + half; };
     auto group_token = [&](int i) {                        // tiles i .. i + GROUP - 1
       return token_at(min(tile_of(i + lane / RW) * kTile + wave * RW + lane % RW, vis.n - 1));
@@ -751,13 +764,15 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
   auto tiles = [&](int64_t bm) {
     return batch == 1 ? (rows + bm - 1) / bm : rows / bm + std::min(batch, m);
   };
-  // More than a round of workgroups of 256 rows: those, which read each tile for twice the
-  // rows (32 heads on 8 of 128, KS = 1 | 2: 2600 tokens 79 | 89 us, 8 x 300 25 | 37, 8 x 200
-  // behind 3000 108 | 126).  One round or less: 128, of which the short ones of a causal
-  // prompt run beside the long ones (2048 tokens 65 | 60, 1024 behind 8000 221 | 160; only
-  // just one round behind a long context loses, 2048 behind 8000 302 | 328).
-  PromptPlan p{1, 1, tiles(256)};
-  if (p.tiles * c.kv_heads > 256) return p;
+  // More than a round of workgroups of all eight waves: KS = 1, which reads each tile for
+  // twice the rows (32 heads on 8 of 128, KS = 1 | 2: 2600 tokens 79 | 89 us, 8 x 300 25 | 37,
+  // 8 x 200 behind 3000 108 | 126).  One round or less: 128 rows, of which the short ones of
+  // a causal prompt run beside the long ones (2048 tokens 65 | 60, 1024 behind 8000 221 |
+  // 160; only just one round behind a long context loses, 2048 behind 8000 302 | 328).
+  // Heads of 64, workgroups of four waves: from one and a half a CU on (1500 tokens 29 | 23,
+  // 30 x 4 behind 2000 38 | 30, 4000 tokens, window 1024, 16 heads, E4M3 47 | 55).
+  PromptPlan p{1, 1, tiles(c.d == 128 ? 256 : 128)};
+  if (p.tiles * c.kv_heads > (c.d == 128 ? 256 : 384)) return p;
   p = PromptPlan{2, 1, tiles(128)};
   // parts that fill the GPU once, by the tiles that there are in earnest
   const int64_t wgs = std::max((rows + 127) / 128, std::min(batch, m)) * c.kv_heads;
@@ -773,6 +788,7 @@ PromptPlan plan_prompt(int64_t m, int64_t heads, int64_t batch, const KvCache& c
 template <int DT, int CT, int D, int KS>
 hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
+  constexpr int kRows = 32 * kRowWaves<D, KS>;
   // tiles as in the kernel, and the place where two halves join
   constexpr int kBufs = KS == 2 && D == 128 ? 2 : 3;
   constexpr int kLds = std::max(KS * 2 * kBufs * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
@@ -781,7 +797,7 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   if (e != hipSuccess) return e;
   const int64_t wgs = p.tiles * p.splits * a.cache.kv_heads;
   const uint32_t group = (uint32_t)(a.heads / a.cache.kv_heads);
-  const uint32_t tokens = std::max<uint32_t>(256 / KS / group, 1);
+  const uint32_t tokens = std::max<uint32_t>(kRows / group, 1);
   // Past one round of workgroups the order matters: 11 prompts of 5730 tokens, 4 heads, 519
   // us in the sequences' order and 447 by length; 11 of 2000, 32 heads, 435 and 440, what
   // finding it costs.  Rounds of shorter workgroups gain nothing (16 sequences of 4 rows 59
@@ -793,7 +809,7 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
                         Divisor::of(tokens),
                         (uint32_t)(a.cache.page_stride >> 4),
                         (uint32_t)(a.cache.token_stride >> 4)};
-  kern<<<dim3((unsigned)wgs), 512, kLds, s>>>(args);
+  kern<<<dim3((unsigned)wgs), kRows / 32 * 64 * KS, kLds, s>>>(args);
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
