@@ -16,7 +16,14 @@
 // the operand P^T wants, so the weights never move between lanes.  Keys are loaded with
 // a row's pieces in adjacent lanes and reordered by lane permutes; a lane's values are
 // the same D / 16 components of its 8 tokens, transposed in registers.  The loads of
-// the next step are in flight while one is computed, its page numbers one step more.
+// the next step are in flight while one is computed, its page numbers one step more; a
+// third step in registers gains nothing (64 x 4096 tokens, E4M3 109 us and 109).
+//
+// Measured with 8 kv heads of 128, two launches where items are split: 1 token 5.3 us, 1000
+// 8.2, 131072 in E4M3 for 64 query heads 58 (4.8 TB/s, the join 5 of it); 64 x 4096 bf16
+// 185 (5.8 TB/s), E4M3 109 (5.0); 24 of 1 to 8000 tokens, 32 kv heads 88 (4.6).  Heads of
+// 64 in E4M3: 64 x 4096 62 (4.7); 129 windows of 1024 for 4 kv heads 25, of which HBM asks
+// for 11: ten steps a workgroup, whose start, joins and page numbers are chains of latency.
 #include <algorithm>
 
 #include "attention.h"
@@ -116,13 +123,14 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   constexpr bool F8 = CT == WQ_E4M3;
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
   // Exponents are taken from a reference that follows the running maximum only where it
-  // is passed by more than 2^8, so that the sums are rarely rescaled.  Weights of f16 are
-  // kept 2^7 larger: at most 2^15, and away from its subnormal range.
+  // is passed by more than 2^8, so that the sums are rarely rescaled (which the prompt
+  // kernel needs; HBM hides it here).  Weights of f16 are kept 2^7 larger: at most 2^15,
+  // and away from its subnormal range.
   constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
   constexpr int KC = Tile<CT, D>::KC, VW = Tile<CT, D>::VW;
   constexpr int NI = D / 16;                             // O^T tiles, components of a lane
   constexpr int OS = D + 4;                              // LDS row of O, in floats
-  constexpr int NT = F8 && D == 128 ? 3 : 2;             // steps whose tiles are in registers
+  constexpr int NT = 2;                                  // steps whose tiles are in registers
   const AttentionCall& a = args.a;
   const KvCache& cc = a.cache;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -334,8 +342,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] *= vs[i];
     }
-    // two parts of 8 (bf16) or 11 bits: against one part, whose rounding is as large as
-    // that of a 16-bit y, this costs matrix instructions that wait for HBM anyway
+    // two parts of 8 (bf16) or 11 bits: one part's rounding would be as large as that of a
+    // 16-bit y, and saves little (64 x 4096 tokens 186.1 us with two, 185.5 with one; 500
+    // tokens 8.2 and 7.9)
     uint4_t hi, lo;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -534,8 +543,9 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs args, float
   }
 }
 
-// Workgroups: two per CU (what their registers allow at a time), no more than there
-// can be units.
+// Workgroups: two per CU (what their registers allow at a time; for heads of 64 three fit,
+// E4M3 129 windows of 1024 23.5 us against 26.5, but 64 x 4096 tokens 65 against 60), no
+// more than there can be units.
 int decode_wgs(int64_t items, int64_t units) {
   if (units >= kDecodeMaxWgs || items >= kDecodeMaxWgs) return kDecodeMaxWgs;
   return (int)std::max<int64_t>(1, std::min<int64_t>(kDecodeMaxWgs, items * units));

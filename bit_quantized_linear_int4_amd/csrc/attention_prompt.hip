@@ -19,6 +19,14 @@
 //
 // LDS rows are whole heads; their 16-byte pieces are swapped by row (the loads into LDS
 // fetch them in that order), so that no read meets more than its share of a bank.
+//
+// Measured, 32 heads on 8: 8192 tokens, heads of 128 520 us (1050 TFLOP/s at 2.0 GHz; the
+// matrix cores are busy for half of the cycles and the vector units, a third of whose time
+// is the exponentials, for the other: two waves of a SIMD are mostly in the same phase), from
+// an E4M3 cache 610, heads of 64 332 (half the products for the same weights); 64 tokens
+// 9.3; 7 behind 30000 33 (3.7 TB/s).  A wave with 64 rows, 512 registers and the scores of
+// the next 32 tokens between the weights of the last ones reads LDS half as often, but has
+// nobody beside it at barriers and loads: 585.  The same with 32 rows 572.
 #include <algorithm>
 
 #include "attention.h"
@@ -154,7 +162,7 @@ void prompt_kernel(PromptArgs args) {
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
   constexpr bool TWO = F8 && DT == WQ_F16;               // weights in two parts of bf16
   // exponents as in the decode kernel: from a reference that lags the maximum by up to
-  // 2^8; weights of f16 2^7 larger
+  // 2^8 (8192 tokens 521 us, 544 without the lag); weights of f16 2^7 larger
   constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
   constexpr int NW = kRowWaves<D, KS>, BM = NW * 32;     // row waves, rows
   constexpr int HT = 64 * NW, NT = HT * KS;              // threads that load a tile; all
@@ -162,7 +170,9 @@ void prompt_kernel(PromptArgs args) {
   constexpr int KB = kTile * RB;                         // and of a tile
   constexpr int PC = D / 8;                              // 16-byte pieces of a row
   constexpr int NL = KB / 1024 / NW;                     // loads of 1 KB per wave and tile
-  // tiles on their way while one is computed (two halves of D = 128 fill LDS with one)
+  // tiles on their way while one is computed (two halves of D = 128 fill LDS with one; 8192
+  // tokens 551 us with two tiles and the places of eight tiles' rows found at once, 641 with
+  // one and a tile's)
   constexpr int AHEAD = KS == 2 && D == 128 ? 1 : 2, BUFS = AHEAD + 1;
   constexpr int NC = D / 16, NB = D / 32;                // k-steps of S^T, blocks of O^T
   const AttentionCall& a = args.a;
@@ -293,8 +303,8 @@ void prompt_kernel(PromptArgs args) {
     // this one xor 32 c), of values for the first 32 components (block b's: xor 64 b)
     const int ka = nl * RB + ((hi ^ key_swap<D>(nl)) << 4);
     const int vr = 4 * hi + ((lane & 15) >> 2);            // row within 8
-    const int va = vr * RB + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swap<D>(vr)) << 4) +
-                   8 * (lane & 1);
+    const int vp = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int va = vr * RB + ((vp ^ value_swap<D>(vr)) << 4) + 8 * (lane & 1);
 
     // A wave loads RW rows of each of its half's tiles.  Where they are in the cache is
     // found for GROUP tiles at once, a row in a lane, a group ahead of its use.
@@ -314,7 +324,8 @@ void prompt_kernel(PromptArgs args) {
       const auto k = args_here<PromptArgs>();
       const int lg_page = k->a.cache.lg_page, place = group_token(i) & ((1 << lg_page) - 1);
       off = (uint32_t)page * k->page16 + (uint32_t)place * k->token16;
-      if constexpr (F8) off_scale = (((uint32_t)page * k->a.cache.kv_heads + kh) << lg_page) + place;
+      if constexpr (F8)
+        off_scale = (((uint32_t)page * k->a.cache.kv_heads + kh) << lg_page) + place;
       look_up(i + GROUP);
     };
     // what a lane loads of its rows, 16 bits: one of PC pieces of NL rows, into LDS at once;
@@ -356,8 +367,10 @@ void prompt_kernel(PromptArgs args) {
           const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(
                                   (first + r) * 4, (int)off) << 4;
           const int to = buf * KB + wave * RW * RB + j * 1024;
-          lds_dma16(kbase + at + ((lane % PC ^ key_swap<D>(row)) << 4), (lds_void_t*)(uintptr_t)(kl + to));
-          lds_dma16(vbase + at + ((lane % PC ^ value_swap<D>(row)) << 4), (lds_void_t*)(uintptr_t)(vl + to));
+          lds_dma16(kbase + at + ((lane % PC ^ key_swap<D>(row)) << 4),
+                    (lds_void_t*)(uintptr_t)(kl + to));
+          lds_dma16(vbase + at + ((lane % PC ^ value_swap<D>(row)) << 4),
+                    (lds_void_t*)(uintptr_t)(vl + to));
         }
       }
     };
@@ -374,7 +387,8 @@ void prompt_kernel(PromptArgs args) {
                   uint4_t{v0[0], v0[1], v1[0], v1[1]});
         }
         // those of keys with the scale of z in them
-        if (lane % GROUP < 2) scales[half][buf][lane % GROUP][row] = lane % GROUP == 0 ? sc * zscale : sc;
+        if (lane % GROUP < 2)
+          scales[half][buf][lane % GROUP][row] = lane % GROUP == 0 ? sc * zscale : sc;
       }
     };
 
@@ -448,7 +462,8 @@ void prompt_kernel(PromptArgs args) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           z[b] = mfma32<DT>(lds_at<uint4_t>((k ^ (c << 5)) + b * 32 * RB), q[c], z[b]);
-      // three k-steps of operands ahead of the products
+      // three k-steps of operands ahead of the products (8192 tokens 521 us, 527 in the
+      // compiler's order)
       __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
       for (int c = 0; c < NC - 3; ++c) {
@@ -456,7 +471,8 @@ void prompt_kernel(PromptArgs args) {
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
-      // a wave of this SIMD that is past its scores goes before one that multiplies
+      // a wave of this SIMD that is past its scores goes before one that multiplies (8192
+      // tokens 520 us, 527 without)
       __builtin_amdgcn_s_setprio(1);
       // scores in units of ln 2: 16 bits z * zscale; E4M3 z, with the scale of the key
       const float unit = F8 ? 1.0f : zscale;
@@ -527,8 +543,8 @@ void prompt_kernel(PromptArgs args) {
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float4_t vs =
-                  *reinterpret_cast<const float4_t*>(&scales[half][buf][1][32 * b + 8 * j + 4 * hi]);
+              const float4_t vs = *reinterpret_cast<const float4_t*>(
+                  &scales[half][buf][1][32 * b + 8 * j + 4 * hi]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) z[b][4 * j + e] = f(z[b][4 * j + e], vs[e]);
             }
@@ -791,7 +807,8 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   constexpr int kRows = 32 * kRowWaves<D, KS>;
   // tiles as in the kernel, and the place where two halves join
   constexpr int kBufs = KS == 2 && D == 128 ? 2 : 3;
-  constexpr int kLds = std::max(KS * 2 * kBufs * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
+  constexpr int kLds =
+      std::max(KS * 2 * kBufs * kTile * D * 2, KS == 2 ? 4 * (D / 2 + 2) * 256 : 0);
   const auto kern = prompt_kernel<DT, CT, D, KS>;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), kLds, done);
   if (e != hipSuccess) return e;
@@ -819,10 +836,12 @@ hipError_t prompt_go(const AttentionCall& a, const PromptPlan& p, hipStream_t s)
   const int64_t total = a.m * a.heads;
   if (p.splits > 4 && total * (D / 4) < 256 * 64) {
     const int64_t per = 32 / (D / 4);
-    prompt_join_kernel<DT, D, 8><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
+    const dim3 grid((unsigned)((total + per - 1) / per));
+    prompt_join_kernel<DT, D, 8><<<grid, 256, 0, s>>>(args, kShift);
   } else {
     const int64_t per = 256 / (D / 4);
-    prompt_join_kernel<DT, D, 1><<<dim3((unsigned)((total + per - 1) / per)), 256, 0, s>>>(args, kShift);
+    const dim3 grid((unsigned)((total + per - 1) / per));
+    prompt_join_kernel<DT, D, 1><<<grid, 256, 0, s>>>(args, kShift);
   }
   return hipGetLastError();
 }
@@ -843,9 +862,12 @@ hipError_t prompt_d(const AttentionCall& a, hipStream_t s) {
 
 }  // namespace
 
-size_t prompt_ws_bytes(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {
-  const PromptPlan p = plan_prompt(m, heads, batch, c, int64_t(1) << 30);
-  return p.splits == 1 ? 0 : (size_t)p.splits * m * heads * (c.d + 2) * sizeof(float);
+// What a call of m or fewer rows can need: its parts are at most 64, and with wgs workgroups
+// of 128 rows or less, at least m * heads / 128 of them, at most 256 / wgs.
+size_t prompt_ws_bytes(int64_t m, int64_t heads, const KvCache& c) {
+  const int64_t parts = std::min(64, 256 / c.kv_heads);
+  if (parts < 2) return 0;
+  return (size_t)std::min<int64_t>(parts * m * heads, 256 * 128) * (c.d + 2) * sizeof(float);
 }
 
 int64_t prompt_wgs(int64_t m, int64_t heads, int64_t batch, const KvCache& c) {

@@ -253,7 +253,7 @@ struct AttentionCall {
 constexpr int kDecodeMaxWgs = 512;
 size_t decode_ws_bytes(int64_t m, int64_t heads, const KvCache& c);
 hipError_t launch_attention_decode(const AttentionCall& c, hipStream_t s);
-size_t prompt_ws_bytes(int64_t m, int64_t heads, int64_t batch, const KvCache& c);
+size_t prompt_ws_bytes(int64_t m, int64_t heads, const KvCache& c);
 constexpr int64_t kPromptMaxWgs = int64_t(1) << 22;   // of at most 512 work-items
 int64_t prompt_wgs(int64_t m, int64_t heads, int64_t batch, const KvCache& c);
 hipError_t launch_attention_prompt(const AttentionCall& c, hipStream_t s);

@@ -1,11 +1,12 @@
 // Rotary rotation of queries and keys, and append of keys and values to a paged
 // cache in 16 bits or E4M3 (formulas in wq.h).
 //
-// Bound by HBM for many rows and by latency (slot or position, table, store) for
-// few.  A head is D / 8 lanes of 8 elements; a thread takes the same elements of U
-// heads of one row, so the row's cos and sin are loaded once and all its loads are
-// in flight together.  The other element of a pair (i, i + rot / 2) is in another
-// lane of the same head and comes from it by a lane permute, so q_out may be q.
+// Bound by HBM for many rows (8191 rows, 32 query and 32 kv heads of 128, bf16: 79 us,
+// 5.1 TB/s) and by latency (slot or position, table, store) for few (1 row 2.5 us, where a
+// launch takes 2; 50 rows into E4M3 3.1).  A head is D / 8 lanes of 8 elements; a thread
+// takes the same elements of U heads of one row, so the row's cos and sin are loaded once
+// and all its loads are in flight together.  The other element of a pair (i, i + rot / 2)
+// is in another lane of the same head and comes from it by a lane permute, so q_out may be q.
 #include "fp8_util.h"
 
 namespace wq {

@@ -653,7 +653,7 @@ size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,
                                      const wq_kv_cache* cache) {
   if (!attention_sizes_ok(m, heads, cache) || batch < 1 || batch >= kMaxDim) return 0;
   if (prompt_wgs(m, heads, batch, kernel_cache(cache)) > kPromptMaxWgs) return 0;
-  return prompt_ws_bytes(m, heads, batch, kernel_cache(cache));
+  return prompt_ws_bytes(m, heads, kernel_cache(cache));
 }
 
 wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t heads, int64_t ldq,

@@ -58,8 +58,8 @@ class AttentionBlock:
     """w_qkv [(heads + 2 kv_heads) * head_dim][hidden], w_o [hidden][heads * head_dim] in
     16 bits; at most `tokens` rows a call."""
 
-    def __init__(self, gain, w_qkv, w_o, heads, cache, table, tokens, batch=None, window=0,
-                 sinks=0, eps=1e-6):
+    def __init__(self, gain, w_qkv, w_o, heads, cache, table, tokens, window=0, sinks=0,
+                 eps=1e-6):
         _, self.kv, _, d = cache.shape
         dt, dev = w_qkv.dtype, w_qkv.device
         hidden = w_o.shape[0]
@@ -75,7 +75,7 @@ class AttentionBlock:
         need = max(wq.wq_linear_fp8_workspace(tokens, self.w_qkv),
                    wq.wq_linear_fp8_workspace(tokens, self.w_o),
                    wq.wq_attention_decode_workspace(tokens, heads, cache),
-                   wq.wq_attention_prompt_workspace(tokens, heads, batch or 1, cache))
+                   wq.wq_attention_prompt_workspace(tokens, heads, 1, cache))
         self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
 
     def _project(self, x, residual, positions, slots):
@@ -153,8 +153,8 @@ def main():
     dt = torch.bfloat16 if a.cache == "bf16" else torch.float8_e4m3fn
     cache = wq.alloc_kv_cache(seqs.count, kv, a.page_size, d, dt)
     weights = (gain, w_qkv, w_o, a.heads, cache, table)
-    block = AttentionBlock(*weights, b * a.prompt, b, a.window, a.sinks)
-    step = AttentionBlock(*weights, b, None, a.window, a.sinks)
+    block = AttentionBlock(*weights, b * a.prompt, a.window, a.sinks)
+    step = AttentionBlock(*weights, b, a.window, a.sinks)
 
     # prompts of all sequences in one call
     x, r = rand(b * a.prompt, hidden), torch.zeros((b * a.prompt, hidden), dtype=torch.bfloat16,

@@ -530,11 +530,13 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
  * in page pages[i][j / page_size] at j % page_size.  Entries behind a row's last
  * token are not used; an entry outside the cache is taken as the nearest page
  * inside, lens past max_pages * page_size (at most 2^30) as that.  Places that no row
- * sees are not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32 [m][heads] or NULL.
+ * sees are not used, whatever they hold.  y dt [m][heads][head_dim]; lse fp32
+ * [m][heads] or NULL; neither overlaps an input, the other or the workspace.
  * A query, key or scale that is not finite makes what it enters not finite or, where
  * its z is -inf, leaves it out; a value (or its scale) that is not finite makes the
  * components that it enters not finite, unless its weight underflows to 0.  No other
- * row is touched by it.
+ * row is touched by it.  Values past 2^118 over the number of tokens may overflow the
+ * fp32 sums, whose weights go up to 2^8.
  * heads a multiple of kv_heads, at most 1024; ldq a multiple of 8; window and sinks
  * >= 0; scale > 0, finite; q and y 16-byte, pages, lens, lse 4-byte aligned.
  * workspace: at least wq_attention_decode_workspace(m, heads, cache) bytes, 256-byte
@@ -556,10 +558,13 @@ wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t head
  * position sees nothing (y = 0, lse = -inf).  Rows of q before starts[0] or from
  * starts[batch] on are not read, and y and lse not written there.
  * starts int32 [batch + 1], ascending, within [0, m]; lens int32 [batch]; pages
- * int32 [batch] rows of max_pages; batch * kv_heads below 2^21.  The weights of v are rounded to dt (bf16 for
- * WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), the sum of weights is not.
+ * int32 [batch] rows of max_pages; batch * kv_heads below 2^21.  The weights of v are
+ * rounded to dt (bf16 for WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), the sum of
+ * weights is not.
  * workspace: at least wq_attention_prompt_workspace(m, heads, batch, cache) bytes,
- * 256-byte aligned (may be NULL when that is 0).
+ * 256-byte aligned (may be NULL when that is 0).  The query grows with m to at most 17
+ * MB and does not depend on batch: what suffices for m rows does for fewer, in any
+ * number of sequences.
  */
 size_t wq_attention_prompt_workspace(int64_t m, int64_t heads, int64_t batch,
                                      const wq_kv_cache* cache);

@@ -144,6 +144,19 @@ def test_workspaces(d, kv, heads, m):
     assert lib.wq_attention_prompt_workspace(m, heads, 0, c) == 0
 
 
+@needs_lib
+@pytest.mark.parametrize("d,kv,heads", [(128, 8, 32), (64, 1, 71), (128, 32, 32), (64, 200, 200)])
+def test_workspaces_suffice_for_fewer_rows(d, kv, heads):
+    lib = wq._load()
+    c = ctypes.byref(cache(d=d, kv=kv, ts=d, hs=16 * d, ps=16 * kv * d))
+    for need in (lambda m, b: lib.wq_attention_decode_workspace(m, heads, c),
+                 lambda m, b: lib.wq_attention_prompt_workspace(m, heads, b, c)):
+        last = 0
+        for m in list(range(1, 130)) + [300, 1000, 4096, 20000]:
+            assert need(m, 1) == need(m, 3) == need(m, 1000) >= last
+            last = need(m, 1)
+
+
 # ------------------------------------------------------------ binding, CPU tensors
 def refused_type(fn, *a, **kw):
     with pytest.raises(wq.WqError) as e:

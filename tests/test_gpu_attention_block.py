@@ -40,9 +40,9 @@ class Setup:
                         rand((hidden, heads * d), 3, dtype, 0.06).cuda())
         self.heads = heads
 
-    def block(self, rows, batch=None):
+    def block(self, rows):
         return self.ab.AttentionBlock(self.gain, *self.weights, self.heads, self.cache, self.table,
-                                      rows, batch, self.window, self.sinks)
+                                      rows, self.window, self.sinks)
 
     def values(self):
         out = []
@@ -91,7 +91,7 @@ def test_prompts_chunks_and_tokens(heads, kv, d, window, sinks, dtype, cdtype):
         pos, slots, starts = s.seqs.add(n)
         m = int(n.sum())
         x, r = rand((m, 256), 11, dtype).cuda(), rand((m, 256), 12, dtype).cuda()
-        before, b = r.clone(), s.block(m, 3)
+        before, b = r.clone(), s.block(m)
         y = b.prompt(x, r, pos, slots, starts, s.seqs.pages, s.seqs.lens)
         torch.cuda.synchronize()
         rows, at = [], 0
@@ -126,7 +126,7 @@ def test_layer_replays():
         n = torch.tensor([33, 5, 70]).cuda()
         pos, slots, starts = s.seqs.add(n)
         x = rand((108, hidden), 50, "bf16").cuda()
-        s.block(108, b).prompt(x, torch.zeros_like(x), pos, slots, starts, s.seqs.pages,
+        s.block(108).prompt(x, torch.zeros_like(x), pos, slots, starts, s.seqs.pages,
                                s.seqs.lens)
         return s, s.block(b), m
 
