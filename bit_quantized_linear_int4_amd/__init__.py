@@ -13,6 +13,7 @@ bfloat16 -> WQ_BF16, float32 -> WQ_F32.  Outputs are caller-allocated (the
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "WqError", "QuantizedWeight", "F16", "BF16", "F32",
@@ -71,6 +72,10 @@ class _Cache(ctypes.Structure):
     ]
 
 
+# the descriptor's bytes, which cost a third of the structure's time
+_pack_cache = struct.Struct("4i4q4P").pack
+
+
 def library_path():
     return _LIB_PATH
 
@@ -84,7 +89,8 @@ def _load():
                           "or python -m bit_quantized_linear_int4_amd._build")
     lib = ctypes.CDLL(_LIB_PATH)
     c_i32, c_i64, c_vp, c_f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
-    wp, cp = ctypes.POINTER(_Weight), ctypes.POINTER(_Cache)
+    wp = ctypes.POINTER(_Weight)
+    cp = c_vp                            # a _Cache by reference, or its bytes
     sig = {
         "wq_quantize_groupwise": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i32, c_i32, c_i32,
                                           c_vp, c_vp, c_vp, c_vp]),
@@ -763,8 +769,7 @@ class KVCache:
     [kv_heads][head_dim]), the same strides for both.  The tensors are checked and their
     addresses taken here, once; other tensors are another KVCache."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "shape", "device_index", "_desc",
-                 "_ref")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "shape", "device_index", "_ref")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         what = "KVCache"
@@ -792,9 +797,17 @@ class KVCache:
             _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.dtype, self.shape, self.device_index = dtype, shape, dev
-        self._desc = _Cache(dt, kv, d, page, pages, strides[0], strides[1], strides[2],
-                            k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales))
-        self._ref = ctypes.byref(self._desc)
+        try:
+            self._ref = _pack_cache(
+                dt, kv, d, page, pages, strides[0], strides[1], strides[2], k.data_ptr(),
+                v.data_ptr(), 0 if k_scales is None else k_scales.data_ptr(),
+                0 if v_scales is None else v_scales.data_ptr())
+        except struct.error:
+            _fail(what, f"sizes {tuple(shape)} are too large")
+
+    @property
+    def _desc(self):
+        return _Cache.from_buffer_copy(self._ref)
 
     def nbytes(self):
         return sum(t.nbytes for t in (self.k, self.v, self.k_scales, self.v_scales)
@@ -830,19 +843,21 @@ def _run(dev, fn, *args):
 
 def _head_rows(what, name, t, d, dtype, dev):
     """(rows, heads, stride of the rows) of [rows][heads][d] whose heads are contiguous."""
-    if t is None or t.dim() != 3:
+    try:
+        m, h, dd = t.shape
+        ld, s1, s2 = t.stride()
+    except (AttributeError, ValueError):
         _fail(what, f"{name} must be a 3-D [rows][heads][head_dim] tensor")
-    m, h, dd = t.shape
-    if dd != d:
-        _fail(what, f"{name} has heads of {dd}, the cache of {d}")
-    ld, s1, s2 = t.stride()
     if m == 1:
         ld = h * d
-    if s2 != 1 or (s1 != d and h > 1) or ld < h * d:
-        _fail(what, f"the rows of {name} are not contiguous")
-    if t.dtype != dtype:
-        _fail(what, f"{name} has dtype {t.dtype}, expected {dtype}", _ERR_UNSUP)
-    if t.get_device() != dev:
+    if (dd != d or s2 != 1 or s1 != d and h > 1 or ld < h * d or t.dtype != dtype
+            or t.get_device() != dev):
+        if dd != d:
+            _fail(what, f"{name} has heads of {dd}, the cache of {d}")
+        if s2 != 1 or s1 != d and h > 1 or ld < h * d:
+            _fail(what, f"the rows of {name} are not contiguous")
+        if t.dtype != dtype:
+            _fail(what, f"{name} has dtype {t.dtype}, expected {dtype}", _ERR_UNSUP)
         _fail(what, "tensors must be GPU tensors, all on one device", _ERR_UNSUP)
     return m, h, ld
 
