@@ -35,6 +35,7 @@ namespace wq {
 namespace {
 
 constexpr int kTile = 64;              // tokens of a tile
+constexpr float kDone = -1.0f;         // in the place of a sum of weights: y is written
 // Parts of `steps` steps of KS tiles, at most `splits`: as many as make the time of a part
 // and of the parts' way through HBM least (about 2 us a step, and for 1e6 components of all
 // rows; there are `million` times as many).  7 tokens behind 240, 370, 500 and 1000, 32 heads
@@ -260,9 +261,12 @@ void prompt_kernel(PromptArgs args) {
   vis.first = min(a.sinks, vis.from);
   vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
   auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
-  // parts past the last one are empty (tiles are below 2^24, splits at most 64)
+  // Parts past the last one are empty (tiles are below 2^24, splits at most 64).  A single
+  // part writes y itself, and kDone for the join: the host plans for what the page table
+  // has room for (512 tokens in a table for 131072: 22 us, 24 through the workspace).
   const int all_tiles = (vis.n + kTile - 1) / kTile;
   const int parts = max(parts_of((all_tiles + KS - 1) / KS, (int)args.splits.d, args.million), 1);
+  if (parts == 1 && split > 0) return;
   const int t_begin = split < parts ? all_tiles * split / parts : 0;
   const int t_end = split < parts ? all_tiles * (split + 1) / parts : 0;
 
@@ -657,22 +661,23 @@ void prompt_kernel(PromptArgs args) {
   const auto k = args_here<PromptArgs>();
   if (k->splits.d > 1) {
     // m, l and the sums of this part
-    if (!live) return;
     const int64_t total = k->a.m * k->a.heads;
     float* ml = k->a.ws + (int64_t)k->splits.d * total * D + (split * total + out) * 2;
-    if (hi == 0) {
+    if (live && hi == 0) {
       ml[0] = m;
-      ml[1] = l;
+      ml[1] = parts == 1 ? kDone : l;
     }
-    if (m == -INFINITY) return;
-    float* w = k->a.ws + (split * total + out) * D;
+    if (parts > 1) {
+      if (!live || m == -INFINITY) return;
+      float* w = k->a.ws + (split * total + out) * D;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4_t*>(w + 32 * b + 8 * j + 4 * hi) =
-            float4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
-    return;
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4_t*>(w + 32 * b + 8 * j + 4 * hi) =
+              float4_t{o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]};
+      return;
+    }
   }
   const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll
@@ -710,6 +715,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
   const bool live = (int64_t)blockIdx.x * kPer + who < total && row >= a.starts[0] &&
                     row < a.starts[a.batch];
   const float* ml = a.ws + (int64_t)splits * total * D;
+  const bool done = ml[2 * out + 1] == kDone;
   float m = -INFINITY, l = 0.0f;
   float4_t x = {0, 0, 0, 0};
   for (int s0 = g; s0 < splits; s0 += U * G) {
@@ -758,7 +764,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
     }
     m = big;
   }
-  if (!live) return;
+  if (!live || done) return;
   const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
   *reinterpret_cast<uint2_t*>(a.y + out * D + c * 4) =
       uint2_t{pack2<DT>(x[0] * inv, x[1] * inv), pack2<DT>(x[2] * inv, x[3] * inv)};
