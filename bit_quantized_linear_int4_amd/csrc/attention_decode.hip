@@ -22,7 +22,7 @@
 // Measured with 8 kv heads of 128, two launches where items are split: 1 token 5.3 us, 1000
 // 8.2, 131072 in E4M3 for 64 query heads 58 (4.8 TB/s, the join 5 of it); 64 x 4096 bf16
 // 185 (5.8 TB/s), E4M3 109 (5.0); 24 of 1 to 8000 tokens, 32 kv heads 88 (4.6).  Heads of
-// 64 in E4M3: 64 x 4096 62 (4.7); 129 windows of 1024 for 4 kv heads 25, of which HBM asks
+// 64 in E4M3: 64 x 4096 61 (4.7); 129 windows of 1024 for 4 kv heads 23.5, of which HBM asks
 // for 11: ten steps a workgroup, whose start, joins and page numbers are chains of latency.
 #include <algorithm>
 
@@ -475,72 +475,72 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   }
 }
 
-// A workgroup takes one row of an item.  256 / (D / 4) groups of threads take its parts in
-// turn, each with a running reference; four parts are loaded together.
-template <int DT, int D>
+// A workgroup takes rows of an item.  Its groups of D / 4 threads take parts in turn, each
+// with a running reference, four parts loaded together: BY_ROW a group a row and all its
+// parts, else all groups the parts of one row, which they then join.
+template <int DT, int D, bool BY_ROW>
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs args, float shift) {
   const AttentionCall& a = args.a;
-  constexpr int L = D / 4, G = 256 / L;
+  constexpr int L = D / 4, G = 256 / L, STEP = BY_ROW ? 1 : G;
   const int tid = threadIdx.x, c = tid % L, g = tid / L;
-  __shared__ __align__(16) float so[G][D];
-  __shared__ float sm[G], sl[G];
   const Joined item = args.joined[blockIdx.x];
-  const int n = item.rows_parts & 0xFFFF, row = blockIdx.y;
-  if (n > 1 && row < item.rows_parts >> 16) {
-    float m = -INFINITY, l = 0.0f;
-    float4_t o = {0, 0, 0, 0};
-    for (int i0 = g; i0 < n; i0 += 4 * G) {
-      float pm[4], pl[4];
-      float4_t po[4];
+  const int n = item.rows_parts & 0xFFFF, rows = item.rows_parts >> 16;
+  const int row = BY_ROW ? (int)blockIdx.y * G + g : blockIdx.y;
+  if (n < 2 || row >= rows) return;
+  float m = -INFINITY, l = 0.0f;
+  float4_t o = {0, 0, 0, 0};
+  for (int i0 = BY_ROW ? 0 : g; i0 < n; i0 += 4 * STEP) {
+    float pm[4], pl[4];
+    float4_t po[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = min(i0 + j * G, n - 1);
-        const float* slot =
-            a.ws + (2 * (int64_t)(item.wg + i) + (i + 1 < n ? 1 : 0)) * (kRows * (D + 2));
-        po[j] = *reinterpret_cast<const float4_t*>(slot + row * D + c * 4);
-        pm[j] = slot[kRows * D + row];
-        pl[j] = slot[kRows * (D + 1) + row];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool live = i0 + j * G < n;
-        const float mn = fmaxf(m, live ? pm[j] : -INFINITY), ref = exp_ref(mn);
-        const float fade = __builtin_amdgcn_exp2f(m - ref);
-        const float f = live ? __builtin_amdgcn_exp2f(pm[j] - ref) : 0.0f;
-        l = l * fade + (live ? pl[j] * f : 0.0f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * fade + (live ? po[j][e] * f : 0.0f);
-        m = mn;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(i0 + j * STEP, n - 1);
+      const float* slot =
+          a.ws + (2 * (int64_t)(item.wg + i) + (i + 1 < n ? 1 : 0)) * (kRows * (D + 2));
+      po[j] = *reinterpret_cast<const float4_t*>(slot + row * D + c * 4);
+      pm[j] = slot[kRows * D + row];
+      pl[j] = slot[kRows * (D + 1) + row];
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool live = i0 + j * STEP < n;
+      const float mn = fmaxf(m, live ? pm[j] : -INFINITY), ref = exp_ref(mn);
+      const float fade = __builtin_amdgcn_exp2f(m - ref);
+      const float f = live ? __builtin_amdgcn_exp2f(pm[j] - ref) : 0.0f;
+      l = l * fade + (live ? pl[j] * f : 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = o[e] * fade + (live ? po[j][e] * f : 0.0f);
+      m = mn;
+    }
+  }
+  if constexpr (!BY_ROW) {
+    __shared__ __align__(16) float so[G][D];
+    __shared__ float sm[G], sl[G];
     *reinterpret_cast<float4_t*>(&so[g][c * 4]) = o;
     if (c == 0) {
       sm[g] = m;
       sl[g] = l;
     }
     __syncthreads();
-    if (tid < D / 8) {
-      float big = sm[0], sum = 0.0f, x[8];
+    if (g != 0) return;
+    m = sm[0];
 #pragma unroll
-      for (int i = 1; i < G; ++i) big = fmaxf(big, sm[i]);
+    for (int i = 1; i < G; ++i) m = fmaxf(m, sm[i]);
+    l = 0.0f;
+    o = float4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const float f = __builtin_amdgcn_exp2f(sm[i] - exp_ref(big));
-        sum += sl[i] * f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += so[i][tid * 8 + e] * f;
-      }
-      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv;
-      const int64_t out = (int64_t)item.seq * a.heads + item.head + row;
-      *reinterpret_cast<uint4_t*>(a.y + out * D + tid * 8) = pack8<DT>(x);
-      if (a.lse != nullptr && tid == 0)
-        a.lse[out] = sum == 0.0f ? -INFINITY : (big - shift + __builtin_amdgcn_logf(sum)) * kLn2;
+    for (int i = 0; i < G; ++i) {
+      const float f = __builtin_amdgcn_exp2f(sm[i] - exp_ref(m));
+      l += sl[i] * f;
+      o += f * *reinterpret_cast<const float4_t*>(&so[i][c * 4]);
     }
   }
+  const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+  const int64_t out = (int64_t)item.seq * a.heads + item.head + row;
+  *reinterpret_cast<uint2_t*>(a.y + out * D + c * 4) =
+      uint2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+  if (a.lse != nullptr && c == 0)
+    a.lse[out] = l == 0.0f ? -INFINITY : (m - shift + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Workgroups: two per CU (what their registers allow at a time; for heads of 64 three fit,
@@ -577,8 +577,19 @@ hipError_t decode_go(const AttentionCall& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;           // nothing is in parts
   constexpr float kShift = CT != WQ_E4M3 && DT == WQ_F16 ? 7.0f : 0.0f;
-  const dim3 grid((unsigned)(per_item ? items : wgs), (unsigned)std::min(kRows, args.group));
-  decode_join_kernel<DT, D><<<grid, 256, 0, s>>>(args, kShift);
+  const int64_t records = per_item ? items : wgs;
+  const int rows = std::min(kRows, args.group);
+  // Many items have few parts each (129 windows of 1024, heads of 64 24.1 us by row and 25.6
+  // else; 16 x 2048 17.5 and 18.9), few have many (1 x 8000 17.9 and 10.2).  One long
+  // sequence among many has at most wgs / kv_heads: all its heads are as long.
+  if (4 * items >= wgs && a.cache.kv_heads >= 4) {
+    const int groups = 256 / (D / 4);
+    const dim3 grid((unsigned)records, (unsigned)((rows + groups - 1) / groups));
+    decode_join_kernel<DT, D, true><<<grid, 256, 0, s>>>(args, kShift);
+  } else {
+    decode_join_kernel<DT, D, false>
+        <<<dim3((unsigned)records, (unsigned)rows), 256, 0, s>>>(args, kShift);
+  }
   return hipGetLastError();
 }
 template <int DT, int D>

@@ -9,7 +9,7 @@ from test_build_resources import kernel_metadata, pytestmark  # noqa: F401
 FAMILIES = {
     "append_kv_kernel": 2 * 2 * 2 * 2,      # types, head sizes, caches, heads per thread
     "decode_kernel": 2 * 2 * 2,
-    "decode_join_kernel": 2 * 2,
+    "decode_join_kernel": 2 * 2 * 2,        # a group of threads a row, or all of them
     "prompt_kernel": 2 * 2 * 2 * 2,         # one or two halves of waves
     "prompt_join_kernel": 2 * 2 * 2,
 }

@@ -47,6 +47,22 @@ def test_decode_of_many_sequences(m, heads, kv, d, page, cdtype, window, sinks):
           sinks, DECODE_R, "bf16", table[i:i + 1].cpu().numpy())
 
 
+@pytest.mark.parametrize("heads,kv,d,cdtype", [(8, 4, 128, "bf16"), (66, 4, 64, "e4m3"),
+                                               (8, 1, 128, "bf16"), (20, 20, 64, "bf16")])
+def test_one_long_sequence_among_many(heads, kv, d, cdtype):
+    """Its items have many parts, those of the others one or two."""
+    say(f"one long {heads} {kv} {d} {cdtype}")
+    heads = heads // kv * kv
+    lens = [5, 200, 9000, 0, 130] + [int(n) for n in np.random.default_rng(2).integers(1, 60, 60)]
+    table, pages = table_of(lens, 16, 14)
+    c = Cache(pages, kv, 16, d, cdtype, seed=91)
+    q = rand((len(lens), heads, d), 92, "bf16", 2.0).cuda()
+    y, lse = run_decode(q, c, table, i32(lens))
+    check(y, lse, q, c.values(), rows_of(lens)[:8], d ** -0.5, 0, 0, DECODE_R, "bf16",
+          table.cpu().numpy())
+    assert not torch.isnan(y).any()
+
+
 @pytest.mark.parametrize("heads,kv,d", [(1024, 1, 64), (1024, 1024, 64), (1000, 8, 128),
                                         (272, 1, 128)])
 def test_many_heads(heads, kv, d):
