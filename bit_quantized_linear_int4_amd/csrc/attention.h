@@ -179,8 +179,10 @@ __device__ __forceinline__ int line_find(int m, const Line& line, const int* par
 #pragma unroll
   for (int w = NT / 2; w > 0; w /= 2)
     if (part[t + w] <= want) t += w;
-  int seq = t * ((m + NT - 1) / NT);
+  const int per = (m + NT - 1) / NT;
+  int seq = t * per;
   before = part[t];
+  if (per == 1) return seq;            // without its count, one load less in the chain
   for (;;) {
     const int n = count(seq);
     if (before + n > want || seq + 1 >= m) return seq;
