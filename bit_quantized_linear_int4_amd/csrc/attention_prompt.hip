@@ -562,8 +562,11 @@ void prompt_kernel(PromptArgs args) {
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          // 16 tokens: weights of this lane's 8, in two parts where one would be less
-          // exact than y (the values are codes, but y is f16)
+          // 16 tokens: weights of this lane's 8, rounded to the products' type: half a step
+          // each, by chance up or down over the tokens, so y is 2.2e-3 of a row's norm off
+          // in bf16 where its own rounding is 1.6e-3, and two parts would cost half of the
+          // products again (8192 tokens 706 us, 526 with one).  Two parts where bf16 weights
+          // meet an f16 y (codes and their scales: 792 us, 618 with one and 8 times the error)
           uint4_t p, rest;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
