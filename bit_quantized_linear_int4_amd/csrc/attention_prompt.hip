@@ -566,7 +566,7 @@ void prompt_kernel(PromptArgs args) {
           // each, by chance up or down over the tokens, so y is 2.2e-3 of a row's norm off
           // in bf16 where its own rounding is 1.6e-3, and two parts would cost half of the
           // products again (8192 tokens 706 us, 526 with one).  Two parts where bf16 weights
-          // meet an f16 y (codes and their scales: 792 us, 618 with one and 8 times the error)
+          // meet an f16 y (codes and their scales: 792 us, 618 with one, but bf16's error)
           uint4_t p, rest;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
