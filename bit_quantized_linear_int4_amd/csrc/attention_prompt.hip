@@ -322,14 +322,15 @@ void prompt_kernel(PromptArgs args) {
     auto look_up = [&](int i) {
       const auto k = args_here<PromptArgs>();
       const int32_t* table = k->a.pages + (int64_t)seq * k->a.ldp;
-      page = min(max(table[group_token(i) >> k->a.cache.lg_page], 0), k->a.cache.pages - 1);
+      page = table[group_token(i) >> k->a.cache.lg_page];
     };
     auto take_group = [&](int i) {                         // its pages are there
       const auto k = args_here<PromptArgs>();
       const int lg_page = k->a.cache.lg_page, place = group_token(i) & ((1 << lg_page) - 1);
-      off = (uint32_t)page * k->page16 + (uint32_t)place * k->token16;
+      const uint32_t inside = (uint32_t)min(max(page, 0), k->a.cache.pages - 1);
+      off = inside * k->page16 + (uint32_t)place * k->token16;
       if constexpr (F8)
-        off_scale = (((uint32_t)page * k->a.cache.kv_heads + kh) << lg_page) + place;
+        off_scale = ((inside * k->a.cache.kv_heads + kh) << lg_page) + place;
       look_up(i + GROUP);
     };
     // what a lane loads of its rows, 16 bits: one of PC pieces of NL rows, into LDS at once;
