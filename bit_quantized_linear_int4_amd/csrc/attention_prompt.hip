@@ -35,7 +35,10 @@ namespace wq {
 namespace {
 
 constexpr int kTile = 64;              // tokens of a tile
-constexpr float kDone = -1.0f;         // in the place of a sum of weights: y is written
+// In the place of a part's sum of weights: the workspace has no sums of it, as y is written
+// (in the first part) or the part has no tiles.  What a part with tiles holds never decides
+// whether it counts: NaN scores leave the maximum at -inf and reach y through the sums alone.
+constexpr float kNoSums = -1.0f;
 // Parts of `steps` steps of KS tiles, at most `splits`: as many as make the time of a part
 // and of the parts' way through HBM least (about 2 us a step, and for 1e6 components of all
 // rows; there are `million` times as many).  7 tokens behind 240, 370, 500 and 1000, 32 heads
@@ -262,7 +265,7 @@ void prompt_kernel(PromptArgs args) {
   vis.n = wg_hi < 0 ? 0 : wg_hi + 1 - vis.from + vis.first;
   auto token_at = [&](int i) { return i < vis.first ? i : i - vis.first + vis.from; };
   // Parts past the last one are empty (tiles are below 2^24, splits at most 64).  A single
-  // part writes y itself, and kDone for the join: the host plans for what the page table
+  // part writes y itself, and kNoSums for the join: the host plans for what the page table
   // has room for (512 tokens in a table for 131072: 22 us, 24 through the workspace).
   const int all_tiles = (vis.n + kTile - 1) / kTile;
   const int parts = max(parts_of((all_tiles + KS - 1) / KS, (int)args.splits.d, args.million), 1);
@@ -669,10 +672,10 @@ void prompt_kernel(PromptArgs args) {
     float* ml = k->a.ws + (int64_t)k->splits.d * total * D + (split * total + out) * 2;
     if (live && hi == 0) {
       ml[0] = m;
-      ml[1] = parts == 1 ? kDone : l;
+      ml[1] = parts == 1 || split >= parts ? kNoSums : l;
     }
     if (parts > 1) {
-      if (!live || m == -INFINITY) return;
+      if (!live || split >= parts) return;
       float* w = k->a.ws + (split * total + out) * D;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -719,7 +722,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
   const bool live = (int64_t)blockIdx.x * kPer + who < total && row >= a.starts[0] &&
                     row < a.starts[a.batch];
   const float* ml = a.ws + (int64_t)splits * total * D;
-  const bool done = ml[2 * out + 1] == kDone;
+  const bool done = ml[2 * out + 1] == kNoSums;
   float m = -INFINITY, l = 0.0f;
   float4_t x = {0, 0, 0, 0};
   for (int s0 = g; s0 < splits; s0 += U * G) {
@@ -734,11 +737,10 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs args, float
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      // a part without sums has written none
-      const bool some = s0 + i * G < splits && pm[i] != -INFINITY;
-      const float mn = some ? fmaxf(m, pm[i]) : m;
-      const float fade = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
-      const float f = some ? __builtin_amdgcn_exp2f(pm[i] - mn) : 0.0f;
+      const bool some = s0 + i * G < splits && pl[i] != kNoSums;
+      const float mn = some ? fmaxf(m, pm[i]) : m, ref = exp_ref(mn);
+      const float fade = __builtin_amdgcn_exp2f(m - ref);
+      const float f = some ? __builtin_amdgcn_exp2f(pm[i] - ref) : 0.0f;
       l = l * fade + (some ? pl[i] * f : 0.0f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = x[e] * fade + (some ? px[i][e] * f : 0.0f);
