@@ -54,9 +54,16 @@ class Sequences:
         return pos.int(), slots.int(), starts
 
 
+def _first_rows(codes, scales, rows):
+    """(codes, scales) of `rows` rows in the buffers of alloc_fp8_rows for as many or more:
+    scales stand [block][row] without gaps."""
+    blocks = scales.shape[0]
+    return codes[:rows], scales.view(-1)[:blocks * rows].view(blocks, rows)
+
+
 class AttentionBlock:
     """w_qkv [(heads + 2 kv_heads) * head_dim][hidden], w_o [hidden][heads * head_dim] in
-    16 bits; at most `tokens` rows a call."""
+    16 bits; at most `tokens` rows a call, which use the first rows of every buffer."""
 
     def __init__(self, gain, w_qkv, w_o, heads, cache, table, tokens, window=0, sinks=0,
                  eps=1e-6):
@@ -65,6 +72,7 @@ class AttentionBlock:
         hidden = w_o.shape[0]
         self.gain, self.eps, self.heads, self.d = gain, eps, heads, d
         self.cache, self.table, self.window, self.sinks = cache, table, window, sinks
+        self.tokens = tokens
         self.w_qkv, self.w_o = pack_fp8(w_qkv), pack_fp8(w_o)
         self.q8, self.s = wq.alloc_fp8_rows(tokens, hidden, dev)
         self.qkv = torch.empty((tokens, heads + 2 * self.kv, d), dtype=dt, device=dev)
@@ -72,36 +80,45 @@ class AttentionBlock:
         self.a = torch.empty_like(self.q)
         self.a8, self.s2 = wq.alloc_fp8_rows(tokens, heads * d, dev)
         self.y = torch.empty((tokens, hidden), dtype=dt, device=dev)
-        need = max(wq.wq_linear_fp8_workspace(tokens, self.w_qkv),
-                   wq.wq_linear_fp8_workspace(tokens, self.w_o),
-                   wq.wq_attention_decode_workspace(tokens, heads, cache),
-                   wq.wq_attention_prompt_workspace(tokens, heads, 1, cache))
+        # a linear of few rows, which splits k, may need more than one of many
+        need = max(max(wq.wq_linear_fp8_workspace(rows, self.w_qkv),
+                       wq.wq_linear_fp8_workspace(rows, self.w_o),
+                       wq.wq_attention_decode_workspace(rows, heads, cache))
+                   for rows in range(1, tokens + 1))
+        need = max(need, wq.wq_attention_prompt_workspace(tokens, heads, 1, cache))
         self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
 
     def _project(self, x, residual, positions, slots):
-        wq.wq_add_rmsnorm(x, self.gain, self.eps, residual=residual, residual_out=residual,
-                          q=self.q8, scales=self.s)
         rows, h, kv = len(x), self.heads, self.kv
-        wq.wq_linear_fp8(self.q8, self.s, self.w_qkv, self.qkv.view(rows, -1), self.ws)
-        wq.wq_append_kv(self.qkv[:, :h], self.qkv[:, h:h + kv], self.qkv[:, h + kv:], self.cache,
-                        slots, positions=positions, cos_sin=self.table, q_out=self.q)
+        if rows > self.tokens:
+            raise ValueError(f"{rows} rows in a block for {self.tokens}")
+        q8, s = _first_rows(self.q8, self.s, rows)
+        qkv, q = self.qkv[:rows], self.q[:rows]
+        wq.wq_add_rmsnorm(x, self.gain, self.eps, residual=residual, residual_out=residual,
+                          q=q8, scales=s)
+        wq.wq_linear_fp8(q8, s, self.w_qkv, qkv.view(rows, -1), self.ws)
+        wq.wq_append_kv(qkv[:, :h], qkv[:, h:h + kv], qkv[:, h + kv:], self.cache, slots,
+                        positions=positions, cos_sin=self.table, q_out=q)
+        return q, self.a[:rows]
 
-    def _output(self):
-        wq.wq_quantize_fp8_rows(self.a.view(len(self.a), -1), self.a8, self.s2)
-        wq.wq_linear_fp8(self.a8, self.s2, self.w_o, self.y, self.ws)
-        return self.y
+    def _output(self, a):
+        y = self.y[:len(a)]
+        a8, s2 = _first_rows(self.a8, self.s2, len(a))
+        wq.wq_quantize_fp8_rows(a.view(len(a), -1), a8, s2)
+        wq.wq_linear_fp8(a8, s2, self.w_o, y, self.ws)
+        return y
 
     def prompt(self, x, residual, positions, slots, starts, pages, lens):
-        self._project(x, residual, positions, slots)
-        wq.wq_attention_prompt(self.q, starts, self.cache, pages, lens, self.a, self.ws,
+        q, a = self._project(x, residual, positions, slots)
+        wq.wq_attention_prompt(q, starts, self.cache, pages, lens, a, self.ws,
                                window=self.window, sinks=self.sinks)
-        return self._output()
+        return self._output(a)
 
     def decode(self, x, residual, positions, slots, pages, lens):
-        self._project(x, residual, positions, slots)
-        wq.wq_attention_decode(self.q, self.cache, pages, lens, self.a, self.ws,
-                               window=self.window, sinks=self.sinks)
-        return self._output()
+        q, a = self._project(x, residual, positions, slots)
+        wq.wq_attention_decode(q, self.cache, pages, lens, a, self.ws, window=self.window,
+                               sinks=self.sinks)
+        return self._output(a)
 
 
 def plain(xs, gain, w_qkv, w_o, heads, kv, d, table, eps, window, sinks):
