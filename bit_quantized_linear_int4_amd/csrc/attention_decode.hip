@@ -124,8 +124,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
   constexpr int VT = F8 ? WQ_BF16 : DT;                  // type of the values' products
   // Exponents are taken from a reference that follows the running maximum only where it
   // is passed by more than 2^8, so that the sums are rarely rescaled (which the prompt
-  // kernel needs; HBM hides it here).  Weights of f16 are kept 2^7 larger: at most 2^15,
-  // and away from its subnormal range.
+  // kernel needs; HBM hides it here).  Weights of f16 are kept 2^7 larger: at most 2^15, and
+  // less of them in its subnormal range, where the second part rounds to multiples of 2^-24:
+  // a weight is off by 2^-32 at most, and the row's largest is 1 (the reference's) or more.
   constexpr float kLag = 8.0f, kShift = VT == WQ_F16 ? 7.0f : 0.0f;
   constexpr int KC = Tile<CT, D>::KC, VW = Tile<CT, D>::VW;
   constexpr int NI = D / 16;                             // O^T tiles, components of a lane
@@ -342,9 +343,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs args) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] *= vs[i];
     }
-    // two parts of 8 (bf16) or 11 bits: one part's rounding would be as large as that of a
-    // 16-bit y, and saves little (64 x 4096 tokens 186.1 us with two, 185.5 with one; 500
-    // tokens 8.2 and 7.9)
+    // two parts of 8 (bf16) or 11 bits (f16, down to 2^-24): one part's rounding would be as
+    // large as that of a 16-bit y, and saves little (64 x 4096 tokens 186.1 us with two, 185.5
+    // with one; 500 tokens 8.2 and 7.9)
     uint4_t hi, lo;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {

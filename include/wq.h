@@ -523,7 +523,8 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
  *   lse = log sum_j exp(z_j)                  (sums over the visible j)
  * A row that sees nothing (n <= 0) gets y = 0 and lse = -inf.  z and all sums are
  * fp32 and the order of every sum is fixed by the sizes and lens: results are
- * deterministic.  The weights of v are kept to 16 significant bits.
+ * deterministic.  The weights of v are kept to 16 significant bits; those of an F16
+ * cache no finer than 2^-32 of the row's largest weight.
  *
  * q [m][heads][head_dim] in dt in {F16, BF16}, rows ldq elements apart; a 16-bit
  * cache has dt.  pages int32 [m] rows of max_pages, ldp apart: token j of row i is
@@ -559,8 +560,9 @@ wq_status wq_attention_decode(const void* q, int32_t dt, int64_t m, int64_t head
  * starts[batch] on are not read, and y and lse not written there.
  * starts int32 [batch + 1], ascending, within [0, m]; lens int32 [batch]; pages
  * int32 [batch] rows of max_pages; batch * kv_heads below 2^21.  The weights of v are
- * rounded to dt (bf16 for WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), the sum of
- * weights is not.
+ * rounded to dt (bf16 for WQ_E4M3; two bf16 parts, 16 bits, when dt is F16), those of an
+ * F16 cache no finer than 2^-32 of the row's largest weight; the sum of weights is not
+ * rounded.
  * workspace: at least wq_attention_prompt_workspace(m, heads, batch, cache) bytes,
  * 256-byte aligned (may be NULL when that is 0).  The query grows with m to at most 17
  * MB and does not depend on batch: what suffices for m rows does for fewer, in any
