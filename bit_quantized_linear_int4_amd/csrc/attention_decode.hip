@@ -23,7 +23,8 @@
 // 8.2, 131072 in E4M3 for 64 query heads 58 (4.8 TB/s, the join 5 of it); 64 x 4096 bf16
 // 185 (5.8 TB/s), E4M3 109 (5.0); 24 of 1 to 8000 tokens, 32 kv heads 88 (4.6).  Heads of
 // 64 in E4M3: 64 x 4096 61 (4.7); 129 windows of 1024 for 4 kv heads 23.5, of which HBM asks
-// for 11: ten steps a workgroup, whose start, joins and page numbers are chains of latency.
+// for 11 and a launch for 2: ten steps a workgroup, whose start, joins and page numbers are
+// chains of latency.
 #include <algorithm>
 
 #include "attention.h"

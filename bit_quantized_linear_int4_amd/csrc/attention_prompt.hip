@@ -23,8 +23,9 @@
 // Measured, 32 heads on 8: 8192 tokens, heads of 128 520 us (1050 TFLOP/s at 2.0 GHz; the
 // matrix cores are busy for half of the cycles and the vector units, a third of whose time
 // is the exponentials, for the other: two waves of a SIMD are mostly in the same phase), from
-// an E4M3 cache 610, heads of 64 332 (half the products for the same weights); 64 tokens
-// 9.3; 7 behind 30000 33 (3.7 TB/s).  A wave with 64 rows, 512 registers and the scores of
+// an E4M3 cache 610 (matrix cores 37% of the cycles, vector units 49), heads of 64 332 (half
+// the products for the same weights: 39 and 67%); 64 tokens 9.3; 7 behind 30000 33 (3.7
+// TB/s).  A wave with 64 rows, 512 registers and the scores of
 // the next 32 tokens between the weights of the last ones reads LDS half as often, but has
 // nobody beside it at barriers and loads: 585.  The same with 32 rows 572.
 #include <algorithm>
