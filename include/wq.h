@@ -535,8 +535,8 @@ wq_status wq_append_kv(const void* q, const void* k, const void* v, int32_t dt, 
  * [m][heads] or NULL; neither overlaps an input, the other or the workspace.
  * A query, key or scale that is not finite makes what it enters not finite or, where
  * its z is -inf, leaves it out; a value (or its scale) that is not finite makes the
- * components that it enters not finite, unless its weight underflows to 0.  No other
- * row is touched by it.  Values past 2^118 over the number of tokens may overflow the
+ * components that it enters not finite (with a weight of 0, as z is -inf or the
+ * exponential underflows, it may or may not).  No other row is touched by it.  Values past 2^118 over the number of tokens may overflow the
  * fp32 sums, whose weights go up to 2^8.
  * heads a multiple of kv_heads, at most 1024; ldq a multiple of 8; window and sinks
  * >= 0; scale > 0, finite; q and y 16-byte, pages, lens, lse 4-byte aligned.
